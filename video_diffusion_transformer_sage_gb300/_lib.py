@@ -18,6 +18,8 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libsage_gb300.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "sage.h")
+PAGED_HEADER = os.path.join(os.path.dirname(_HERE), "include", "sage_paged.h")
+PAGED_WS_HEADER = 4096   # SAGE_PAGED_WS_HEADER: the bytes of a paged workspace that start as zeros
 
 STATUS = {0: "SAGE_OK", 1: "SAGE_ERR_INVALID_ARG", 2: "SAGE_ERR_ALIGNMENT", 3: "SAGE_ERR_UNSUPPORTED",
           4: "SAGE_ERR_WORKSPACE", 5: "SAGE_ERR_CUDA", 6: "SAGE_ERR_DEVICE_TIMEOUT"}
@@ -47,9 +49,23 @@ V_FORMATS = {"e4m3": 0, "int8": 1}
 _lib = None
 
 
-def header_functions() -> list:
-    """Names of the functions include/sage.h declares."""
-    text = open(HEADER).read()
+class SagePagedKVC(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("n_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("k_stride_page", ctypes.c_int64), ("k_stride_token", ctypes.c_int64),
+                ("k_stride_head", ctypes.c_int64), ("v_stride_page", ctypes.c_int64),
+                ("v_stride_token", ctypes.c_int64), ("v_stride_head", ctypes.c_int64), ("format", ctypes.c_int64),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class SagePagedBatchC(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int64), ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("max_pages", ctypes.c_int64), ("table_stride", ctypes.c_int64)]
+
+
+def header_functions(header: str = HEADER) -> list:
+    """Names of the functions a header (include/sage.h, or PAGED_HEADER) declares."""
+    text = open(header).read()
     return sorted(set(re.findall(r"^\s*(?:const\s+)?[a-z_0-9]+\**\s+\**(sage_[a-z_0-9]+)\s*\(", text, re.M)))
 
 
@@ -62,6 +78,7 @@ def lib():
         P, I, S, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
         VP = ctypes.POINTER(SageView)
         QP = ctypes.POINTER(SageQuantizedC)
+        KP, BP = ctypes.POINTER(SagePagedKVC), ctypes.POINTER(SagePagedBatchC)
         sig = {
             "sage_status_string": ([ctypes.c_int], ctypes.c_char_p),
             "sage_quant_scratch_bytes": ([I, I, I], S),
@@ -83,6 +100,9 @@ def lib():
             "sage_measure_mma_rate": ([I, I, I, P, P], ctypes.c_int),
             "sage_qk_rmsnorm_rope": ([VP, VP, P, P, P, P, F, P], ctypes.c_int),
             "sage_smooth_quant_qk_rmsnorm_rope": ([VP, VP, P, P, P, P, F, QP, P, S, P], ctypes.c_int),
+            "sage_paged_append": ([VP, VP, VP, P, P, P, P, I, P, F, KP, BP, P, I, I, P, P], ctypes.c_int),
+            "sage_paged_workspace_bytes": ([I], S),
+            "sage_paged_attn": ([VP, KP, BP, F, I, I, P, I, I, P, P, S, P], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -348,3 +368,165 @@ def sage_smooth_quant_qk_rmsnorm_rope(q: torch.Tensor, k: torch.Tensor, gamma_q:
                                                    float(eps), ctypes.byref(c), scratch.data_ptr(), scratch.numel(),
                                                    _stream(stream)), "sage_smooth_quant_qk_rmsnorm_rope")
     return qz
+
+
+# ------------------------------------------------------------------- paged K/V cache (include/sage_paged.h)
+class PagedKV:
+    """A paged K/V cache over the caller's page tensors [n_pages, page_size, n_heads, head_dim] (any page,
+    slot and head strides, unit channel stride): bf16, or torch.float8_e4m3fn with fp32 scales
+    k_scale and v_scale [n_heads].  `status` is the block that sage_paged_append records bad indices in
+    (read it with sage_check_device_status)."""
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+                 v_scale: Optional[torch.Tensor] = None):
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+            raise ValueError("k_pages and v_pages must be [n_pages, page_size, n_heads, head_dim] of one shape and type")
+        if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError(f"the cache holds bf16 or float8_e4m3fn, got {k_pages.dtype}")
+        e4m3 = k_pages.dtype == torch.float8_e4m3fn
+        if (k_scale is not None) != e4m3 or (v_scale is not None) != e4m3:
+            raise ValueError("k_scale and v_scale belong to a float8_e4m3fn cache, and it needs both")
+        n, ps, h, d = k_pages.shape
+        for t in (k_pages, v_pages):
+            if not t.is_cuda or t.device != k_pages.device or t.stride(3) != 1:
+                raise ValueError("expected CUDA page tensors on one device with unit channel stride")
+        for t in (k_scale, v_scale):
+            if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (h,) or not t.is_contiguous()
+                                  or t.device != k_pages.device):
+                raise ValueError(f"expected contiguous fp32 scales of shape ({h},) on the pages' device")
+        self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
+        self.n_pages, self.page_size, self.n_heads, self.head_dim = n, ps, h, d
+        self.device, self.status = k_pages.device, status_block(k_pages.device)
+        self._c = SagePagedKVC(k_pages.data_ptr(), v_pages.data_ptr(), n, ps, h, d, *k_pages.stride()[:3],
+                               *v_pages.stride()[:3], 1 if e4m3 else 0, k_scale.data_ptr() if e4m3 else None,
+                               v_scale.data_ptr() if e4m3 else None)
+        self._ref = ctypes.byref(self._c)
+
+
+class PagedBatch:
+    """The sequences of a call: int32 CUDA tensors cu_q [n + 1] (first row of each sequence's new
+    tokens), kv_len [n] (tokens in the cache, the new ones included) and page_table [n, max_pages].  The
+    tensors may be rewritten between calls (a captured graph reads them anew)."""
+
+    def __init__(self, cu_q: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor):
+        n = kv_len.numel()
+        for t in (cu_q, kv_len, page_table):
+            if t.dtype != torch.int32 or not t.is_cuda or t.device != cu_q.device:
+                raise ValueError("expected int32 CUDA tensors on one device")
+        if kv_len.dim() != 1 or tuple(cu_q.shape) != (n + 1,) or page_table.dim() != 2 or page_table.shape[0] != n:
+            raise ValueError("expected cu_q [n + 1], kv_len [n] and page_table [n, max_pages]")
+        if not cu_q.is_contiguous() or not kv_len.is_contiguous() or (page_table.shape[1] > 1
+                                                                      and page_table.stride(1) != 1):
+            raise ValueError("cu_q and kv_len must be contiguous, page_table's rows too")
+        self.cu_q, self.kv_len, self.page_table, self.n_seqs = cu_q, kv_len, page_table, n
+        self.device = cu_q.device
+        self._c = SagePagedBatchC(n, cu_q.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), page_table.shape[1],
+                                  page_table.stride(0))
+        self._ref = ctypes.byref(self._c)
+
+
+def paged_workspace(head_dim: int, device="cuda") -> torch.Tensor:
+    """Workspace for sage_paged_attn; the part that has to start as zeros (the status block first) does."""
+    need = int(lib().sage_paged_workspace_bytes(head_dim))
+    ws = torch.empty(need + 256, dtype=torch.uint8, device=device)
+    off = (-ws.data_ptr()) % 256
+    ws = ws[off:off + need]
+    ws[:PAGED_WS_HEADER].zero_()
+    return ws
+
+
+def _paged_view(t: torch.Tensor, d: int, device, what: str) -> SageView:
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.device != device:
+        raise ValueError(f"{what}: expected a bf16 [N, H, {d}] tensor on the cache's device")
+    shape, stride = t.shape, t.stride()
+    if shape[2] != d or stride[2] != 1:
+        raise ValueError(f"{what}: expected a bf16 [N, H, {d}] tensor with unit channel stride")
+    return SageView(t.data_ptr(), shape[0], shape[1], d, stride[0], stride[1])
+
+
+def _paged_call(device, stream, call):
+    """`call(raw stream)` with the cache's device current, on `stream` or that device's current stream."""
+    if device.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream))
+    with torch.cuda.device(device):
+        return call(torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream))
+
+
+def _fp32_table(t: Optional[torch.Tensor], shape: tuple, device, what: str):
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous fp32 tensor of shape {shape} on the cache's device")
+    return t.data_ptr()
+
+
+def sage_paged_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKV, batch: PagedBatch,
+                      q: Optional[torch.Tensor] = None, gamma_q: Optional[torch.Tensor] = None,
+                      gamma_k: Optional[torch.Tensor] = None, rope_cos: Optional[torch.Tensor] = None,
+                      rope_sin: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                      eps: float = 1e-6, q_out: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """New tokens' K and V [N, n_heads, D] into the cache, after the optional per-head RMSNorm (gamma_q,
+    gamma_k: fp32 [D]) and rotation (rope_cos, rope_sin: fp32 [rows, D / 2]; row = position in the
+    sequence, or positions[t], int32) of Q and K.  Returns Q so treated (q_out, made here when None; it
+    may be q itself), or None without q."""
+    d, dev = cache.head_dim, cache.device
+    vk, vv = _paged_view(k, d, dev, "k"), _paged_view(v, d, dev, "v")
+    if batch.device != dev:
+        raise ValueError("the batch lies on another device than the cache")
+    vq, oargs = None, (None, 0, 0)
+    if q is not None:
+        vq = _paged_view(q, d, dev, "q")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        vo = _paged_view(q_out, d, dev, "q_out")
+        if vo.n_tokens != vq.n_tokens or vo.n_heads != vq.n_heads:
+            raise ValueError("q_out must have q's shape")
+        oargs = (vo.data, vo.stride_token, vo.stride_head)
+    elif q_out is not None or gamma_q is not None:
+        raise ValueError("q_out and gamma_q belong to q")
+    rows = rope_cos.shape[0] if rope_cos is not None else 0
+    if positions is not None and (positions.dtype is not torch.int32 or tuple(positions.shape) != (k.shape[0],)
+                                  or not positions.is_contiguous() or positions.device != dev):
+        raise ValueError("positions: expected a contiguous int32 tensor [N] on the cache's device")
+    status = cache.status if status is None else status
+    if status.device != dev or status.numel() * status.element_size() < 256:
+        raise ValueError("status: expected a zeroed block of 256 bytes on the cache's device")
+    args = (_fp32_table(gamma_q, (d,), dev, "gamma_q"), _fp32_table(gamma_k, (d,), dev, "gamma_k"),
+            _fp32_table(rope_cos, (rows, d // 2), dev, "rope_cos"), _fp32_table(rope_sin, (rows, d // 2), dev, "rope_sin"))
+    fn, by = lib().sage_paged_append, ctypes.byref
+    _check(_paged_call(dev, stream, lambda s: fn(
+        None if vq is None else by(vq), by(vk), by(vv), *args, rows, None if positions is None else positions.data_ptr(),
+        eps, cache._ref, batch._ref, *oargs, status.data_ptr(), s)), "sage_paged_append")
+    return q_out
+
+
+def sage_paged_attn(q: torch.Tensor, cache: PagedKV, batch: PagedBatch, sm_scale: Optional[float] = None,
+                    causal: bool = True, window: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of the batch's new tokens q [N, Hq, D] over the cache: all stored tokens of their sequence
+    (causal False), those up to their own position, or the last `window` of these.  lse: optional fp32
+    [N, Hq], receives the log of the sum of exponentials.  ws: a paged_workspace (made here when None)."""
+    d, dev = cache.head_dim, cache.device
+    vq = _paged_view(q, d, dev, "q")
+    if batch.device != dev:
+        raise ValueError("the batch lies on another device than the cache")
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    vo = _paged_view(out, d, dev, "out")
+    if vo.n_tokens != vq.n_tokens or vo.n_heads != vq.n_heads:
+        raise ValueError("out must have q's shape")
+    if lse is not None and (lse.dtype is not torch.float32 or tuple(lse.shape) != tuple(q.shape[:2])
+                            or not lse.is_contiguous() or lse.device != dev):
+        raise ValueError("lse: expected a contiguous fp32 tensor [N, Hq] on the cache's device")
+    if ws is None:
+        ws = paged_workspace(d, dev)
+    elif ws.device != dev:
+        raise ValueError("ws lies on another device than the cache")
+    sm_scale = 1.0 / math.sqrt(d) if sm_scale is None else sm_scale
+    fn, by = lib().sage_paged_attn, ctypes.byref
+    _check(_paged_call(dev, stream, lambda s: fn(
+        by(vq), cache._ref, batch._ref, sm_scale, 1 if causal else 0, window or 0, vo.data, vo.stride_token,
+        vo.stride_head, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), s)),
+        "sage_paged_attn")
+    return out

@@ -41,14 +41,13 @@
 // common exit, which frees the tensor memory.
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <cudaTypedefs.h>
 
 #include <cmath>
 #include <cstring>
-#include <mutex>
 
 #include "sage_internal.h"
 #include "sm103_ptx.cuh"
+#include "tensor_map.h"
 
 namespace sage {
 namespace {
@@ -785,20 +784,6 @@ __global__ void debug_wait_timeout_kernel(int32_t* status, uint64_t limit) {
 }
 
 // --------------------------------------------------------------------------- host side
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
-
 // The bf16 output as a [N][H][D] tensor with the caller's token and head strides (elements),
 // 128-byte swizzled boxes of 32 rows x 1 head x 64 channels.  False if the strides do not suit a
 // tensor map (the epilogue then stores row by row).

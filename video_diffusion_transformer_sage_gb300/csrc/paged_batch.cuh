@@ -1,0 +1,38 @@
+// paged_batch.cuh -- device side: finding a token's sequence and its bounds, and the error record.
+#pragma once
+#include "paged_internal.h"
+#include "sm103_ptx.cuh"
+
+namespace sage {
+
+// The first bad index of a call stays recorded until the host reads it; nothing stops for it.
+__device__ __forceinline__ void record_bad_index(int32_t* status, int32_t where) {
+  if (atomicCAS(status, 0, kStatusBadIndex) == 0) status[1] = where;
+}
+
+// The rows of sequence b, [start, end), whatever cu_q holds: inside [0, n_tokens), never reversed.
+__device__ __forceinline__ void seq_rows(const PagedBatchDev& b, int s, int& start, int& end) {
+  start = min(max(__ldg(b.cu_q + s), 0), b.n_tokens);
+  end = min(max(__ldg(b.cu_q + s + 1), start), b.n_tokens);
+}
+
+// The sequence whose rows hold row t, or -1.  Every lane of the warp calls it with the same t: each
+// step compares 32 evenly spaced entries of cu_q, so 1024 sequences take two loads in a row.
+__device__ __forceinline__ int find_seq(const PagedBatchDev& b, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = b.n_seqs;
+  while (true) {
+    const int step = (n + 31) / 32;
+    const int off = lane * step;
+    const bool le = off < n && __ldg(b.cu_q + lo + off) <= t;
+    const uint32_t m = __ballot_sync(0xffffffffu, le);
+    if (m == 0) return -1;
+    const int k = (31 - __clz(m)) * step;
+    lo += k;
+    n = min(step, n - k);
+    if (step == 1) break;
+  }
+  return t < __ldg(b.cu_q + lo + 1) ? lo : -1;
+}
+
+}  // namespace sage

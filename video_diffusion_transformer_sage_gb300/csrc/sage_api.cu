@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "paged_internal.h"
 #include "sage_internal.h"
 
 namespace {
@@ -384,7 +385,7 @@ sage_status sage_check_device_status(void* status_block, void* stream, int32_t* 
   if (where) *where = host[1];
   if (host[0] != 0) {
     if (cudaMemset(status_block, 0, sizeof(host)) != cudaSuccess) return SAGE_ERR_CUDA;
-    return SAGE_ERR_DEVICE_TIMEOUT;
+    return host[0] == sage::kStatusBadIndex ? SAGE_ERR_INVALID_ARG : SAGE_ERR_DEVICE_TIMEOUT;
   }
   return SAGE_OK;
 }
