@@ -248,6 +248,19 @@ def test_attention_of_a_long_split_sequence():
     paged_ref.check_attention(p, out, paged_ref.attention(p, p.q, True))
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_attention_of_a_long_ragged_batch(fmt):
+    """Many key tiles and several units to each SM: the ring of stages goes round often, across units."""
+    p = Problem([1] * 40, [700 + 61 * ((7 * i) % 40) for i in range(40)], 64, 8, 128, 64, fmt, seed=30)
+    cache, batch = _handles(p)
+    ws = sage.paged_workspace(128)
+    out = sage.sage_paged_attn(p.q, cache, batch, ws=ws)
+    paged_ref.check_attention(p, out, paged_ref.attention(p, p.q, True))
+    for _ in range(10):
+        assert torch.equal(_bits(sage.sage_paged_attn(p.q, cache, batch, ws=ws)), _bits(out))
+    assert sage.sage_check_device_status(ws) == (0, 0)
+
+
 def test_attention_shared_prefix_and_strided_views():
     """Sequences with a page in common; q a slice of the projection buffer, out a slice of a wider one."""
     p = Problem([3, 2, 4], [40, 70, 20], 6, 2, 64, 16, seed=10, share_first_page=True)

@@ -48,7 +48,10 @@ struct FewCfg {
   static constexpr int kKeys = 16384 / kRowBytes;             // keys per stage: 64, 128 or 256
   static constexpr int kPanelBytes = kKeys * kPanelRow;
   static constexpr int kStageBytes = 32768;                   // 16 KB of K, 16 KB of V
-  static constexpr int kStages = 5;
+  // Even, so that a stage is always the same team's: a team that skipped every other phase of a
+  // barrier could take a phase two back, of the same parity, for the one it waits for.
+  static constexpr int kStages = 4;
+  static_assert(kStages % 2 == 0, "a ring stage must stay with one team");
   static constexpr int kWarpKeys = kKeys / 4;
   static constexpr int kNT = kWarpKeys / 8;                   // 8-key score tiles per warp
   static constexpr int kOT = D / 8;                           // 8-channel O tiles
@@ -178,7 +181,7 @@ struct Walk {
     end = min(total, at + quota);
     if (at >= end) return false;
     int64_t base = 0;
-    for (int b0 = 0;; b0 += 32) {
+    for (int b0 = 0; b0 < p.a.b.n_seqs; b0 += 32) {
       int64_t n = 0;
       if (b0 + lane < p.a.b.n_seqs) {
         const SeqWork s = seq_work<kRows, kKeys>(p, b0 + lane);
@@ -202,6 +205,7 @@ struct Walk {
       }
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
+    return false;
   }
   __device__ __forceinline__ int seg_tiles() const {
     return static_cast<int>(min(static_cast<int64_t>(w.nt - k), end - at));
@@ -215,7 +219,11 @@ struct Walk {
     if (++u < w.qt * p.a.hkv) return;
     u = 0;
     do {
-      w = seq_work<kRows, kKeys>(p, ++b);
+      if (++b >= p.a.b.n_seqs) {   // the lengths changed under the call: stop
+        at = end;
+        return;
+      }
+      w = seq_work<kRows, kKeys>(p, b);
     } while (w.qt == 0);
   }
 };
@@ -228,7 +236,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   constexpr int R = C::kRows, KT = C::kKeys;
   extern __shared__ uint8_t smem_raw[];
   __shared__ volatile int s_abort;
-  __shared__ int s_last;
+  __shared__ int s_last, s_skip;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* empty = full + C::kStages;
@@ -238,8 +246,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PagedAttnArgs& a = p.a;
 
-  if (*reinterpret_cast<volatile int32_t*>(a.status) == kStatusTimeout) return;
   if (threadIdx.x == 0) {
+    s_skip = *reinterpret_cast<volatile int32_t*>(a.status) == kStatusTimeout;
     s_abort = 0;
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(full + s, 1);
@@ -252,6 +260,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     fence_mbar_init();
   }
   __syncthreads();
+  if (s_skip) return;   // an earlier wait ran out: no work until the status has been read
 
   auto fail = [&](int where) {
     if (atomicCAS(a.status, 0, kStatusTimeout) == 0) a.status[1] = where;
@@ -336,8 +345,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       // Every copy issued has landed before the CTA ends.
       for (int j = max(0, it - C::kStages); j < it; ++j)
         mbar_wait(full + j % C::kStages, (j / C::kStages) & 1, kFewWaitNs);
-      asm volatile("cp.async.wait_all;" ::: "memory");
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
 
