@@ -196,7 +196,12 @@ sage_status sage_paged_attn(const sage_view* q, const sage_paged_kv* cache, cons
   a.counters = reinterpret_cast<int32_t*>(w + kCountersOff);
   a.part_ml = reinterpret_cast<float2*>(w + kMlOff);
   a.part_o = reinterpret_cast<float*>(w + kPartOff);
-  return cuda_status(sage::launch_paged_few(a, *cache, static_cast<int>(d), static_cast<cudaStream_t>(stream)));
+  // By the mean query rows of a K/V head and sequence: up to 32 the cache's bandwidth is the limit and the
+  // warp-level kernel meets it, above the tensor cores' tiles pay.
+  const int64_t rows = n * (q->n_heads / cache->n_heads), seqs = batch->n_seqs < n ? batch->n_seqs : n;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_status(rows <= 32 * seqs ? sage::launch_paged_few(a, *cache, static_cast<int>(d), s)
+                                       : sage::launch_paged_chunk(a, *cache, static_cast<int>(d), s));
 }
 
 }  // extern "C"

@@ -1,0 +1,810 @@
+// paged_chunk.cu -- attention of many query rows per K/V head over the paged cache (prompts, chunks of
+// a video) on the 5th-generation tensor cores.
+//
+// A unit is (sequence, K/V head, 256 query rows): the rows of a K/V head are the sequence's new tokens
+// times the query heads that share it, so grouped heads fill the 128-row tiles and every K and V
+// tile that is loaded serves all of them.  Two 128-row tiles t = 0, 1 per CTA and 128-key tiles:
+//   S_t = Q_t K^T    tcgen05.mma 128 x 128 x 16, fp32 in tensor memory
+//   online softmax   one thread per row: fp32 maximum and sum; P_t in 16 bits over S_t's columns
+//                    (its own columns at D = 64)
+//   O_t += P_t V     A from tensor memory, B = V as it lies in the cache, keys by channels: the
+//                    MN-major operand of the 128-byte swizzle, so V is never transposed
+// as in attn_fwd.cu (Q tiles in turn, so one tile's softmax overlaps the other's MMAs).  O is rescaled only
+// when a row's maximum rises by more than 2^8 (P then stays below 2^8, far inside both 16-bit types
+// and fp32): the result is the same ratio, and most tiles rescale nothing.
+//
+// bf16 cache: bf16 operands, one TMA box per page and 64 channels, straight into the swizzled tiles.
+// E4M3 cache: the codes come by TMA into a staging tile and one warpgroup widens them to fp16 (exact) in
+// the swizzled tiles; Q is held as fp16 times a power of two per row and P as fp16.
+//
+// Warp roles: warp 0 page table and TMA, warp 1 MMA issue (one thread), warp 2 tensor memory; warps 4-7 and
+// 8-11 softmax and epilogue of tile 0 and 1; with E4M3 warps 12-15 widen.  Every wait is bounded.
+//
+// What bounds it: 4 rows keys D FLOPs at the 16-bit tensor rate (for few rows the cache's bytes).  The key axis
+// is split over gridDim.y CTAs where the units alone leave SMs idle; each then leaves (maximum, sum, O) in the
+// workspace, and paged_join_kernel adds the parts in the order of their keys.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "paged_batch.cuh"
+#include "tensor_map.h"
+
+namespace sage {
+namespace {
+
+constexpr int kBM = 128, kBN = 128;
+constexpr uint64_t kChunkWaitNs = 2000000000ull;
+constexpr float kRise = 8.0f;   // log2 of how far a maximum may fall behind before O is rescaled
+
+template <int D, bool kE4M3>
+struct ChunkCfg {
+  static constexpr int kThreads = kE4M3 ? 512 : 384;
+  static constexpr int kPanels = D / 64;
+  static constexpr int kPanelBytes = 128 * 128;               // 128 rows of 64 channels
+  static constexpr int kQTileBytes = kBM * D * 2;
+  static constexpr int kTileBytes = kBN * D * 2;              // a K or V tile in 16 bits
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kRawTile = kBN * D;                    // a tile of codes
+  static constexpr int kRawBytes = kE4M3 ? 2 * kRawTile : 0;
+  // Tensor memory columns: S_t at 128 t, O_t at 256 + D t; P_t over S_t, or at 384 + 64 t (D = 64).
+  static constexpr int kColO0 = 256;
+  static constexpr bool kSepP = D == 64;
+  static constexpr int kColP0 = kSepP ? 384 : 0, kStepP = kSepP ? 64 : 128;
+  static constexpr int kKvOff = 2 * kQTileBytes;
+  static constexpr int kRawOff = kKvOff + kStages * kStageBytes;
+  static constexpr int kExpOff = kRawOff + kRawBytes;         // 2^e of each Q row (E4M3)
+  static constexpr int kBarOff = kExpOff + (kE4M3 ? 1024 : 0);
+  // q_full, kv_full[S], kv_empty[S], s_full[2], p_full[2], pv_done[2], s_free[2], mma_final, raw_full, raw_empty
+  static constexpr int kNumBars = 1 + 2 * kStages + 8 + 3;
+  static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;
+  // Registers a thread: launched at 168 (384 threads) or 128 (512).
+  static constexpr int kRegsRoles = kE4M3 ? 56 : 72, kRegsSoftmax = kE4M3 ? 192 : 216, kRegsWiden = 72;
+  static_assert(128 * kRegsRoles + 256 * kRegsSoftmax + (kE4M3 ? 128 * kRegsWiden : 0) <= (kE4M3 ? 512 * 128 : 384 * 168),
+                "register split exceeds launch");
+  static_assert(kSmem <= 232448 - 256, "shared memory");
+};
+
+struct ChunkParams {
+  PagedAttnArgs a;
+  int group;
+  int box_shift;   // log2 of the slots per TMA box (a page, or 128)
+  int splits;
+};
+
+__device__ __forceinline__ void record_timeout(int32_t* status, int32_t where, volatile int* abort_flag) {
+  if (atomicCAS(status, 0, kStatusTimeout) == 0) status[1] = where;
+  *abort_flag = 1;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, kChunkWaitNs));
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, uint64_t* bar, int32_t x, int32_t y,
+                                            int32_t z, int32_t w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+// One unit's work; the same for every thread of a CTA.
+struct Unit {
+  int b, h;
+  int start, n_new, len;    // first row of q, new tokens, tokens in the cache
+  int row0, rows;           // first row (token x group) of the unit, rows it has (at most 256)
+  int t0, nt;               // its key tiles (this CTA's share of them)
+  int ulo, uhi;             // keys that some row sees
+  int index;                // among all units of the call
+};
+
+__device__ __forceinline__ void token_keys(const PagedAttnArgs& a, int len, int n_new, int j, int& lo, int& hi) {
+  const int pos = len - n_new + j;
+  hi = a.causal ? max(0, pos + 1) : len;
+  lo = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
+}
+
+// Unit number `index` of the call, found by one warp; false past the last.  Units of a sequence and head
+// lie together, the later rows (more keys when causal) first.
+__device__ __forceinline__ bool find_unit(const PagedAttnArgs& a, int group, int index, Unit& u) {
+  const int lane = threadIdx.x & 31;
+  int base = 0;
+  for (int b0 = 0; b0 < a.b.n_seqs; b0 += 32) {
+    int blocks = 0;
+    if (b0 + lane < a.b.n_seqs) {
+      int s, e;
+      seq_rows(a.b, b0 + lane, s, e);
+      blocks = ((e - s) * group + 255) / 256;
+    }
+    int incl = blocks * a.hkv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, base + incl > index);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      const int nb = __shfl_sync(0xffffffffu, blocks, l);
+      const int off = index - base - (__shfl_sync(0xffffffffu, incl, l) - nb * a.hkv);
+      int e;
+      u.b = b0 + l;
+      seq_rows(a.b, u.b, u.start, e);
+      u.n_new = e - u.start;
+      u.len = min(max(__ldg(a.b.kv_len + u.b), 0), a.b.cap);
+      u.h = off / nb;
+      u.row0 = (nb - 1 - off % nb) * 256;
+      u.rows = min(256, u.n_new * group - u.row0);
+      int unused;
+      token_keys(a, u.len, u.n_new, u.row0 / group, u.ulo, unused);
+      token_keys(a, u.len, u.n_new, (u.row0 + u.rows - 1) / group, unused, u.uhi);
+      u.t0 = u.ulo / kBN;
+      u.nt = max(1, (u.uhi + kBN - 1) / kBN - u.t0);
+      u.index = index;
+      return true;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return false;
+}
+
+// Max of 64 consecutive fp32 values (as bits): four independent chains of 3-input maxima.
+__device__ __forceinline__ float max64(const uint32_t* s) {
+  auto f = [s](int i) { return __uint_as_float(s[i]); };
+  float a = fmax3(f(0), f(1), f(2)), b = fmax3(f(3), f(4), f(5));
+  float c = fmax3(f(6), f(7), f(8)), d = fmax3(f(9), f(10), f(11));
+#pragma unroll
+  for (int k = 12; k < 60; k += 8) {
+    a = fmax3(a, f(k), f(k + 1));
+    b = fmax3(b, f(k + 2), f(k + 3));
+    c = fmax3(c, f(k + 4), f(k + 5));
+    d = fmax3(d, f(k + 6), f(k + 7));
+  }
+  a = fmax3(a, f(60), f(61));
+  b = fmax3(b, f(62), f(63));
+  return fmaxf(fmax3(a, b, c), d);
+}
+
+// Instruction descriptor bits: bf16 operands (fp16 is 0), B MN-major.
+constexpr uint32_t kIdescBf16 = (1u << 7) | (1u << 10), kIdescBmn = 1u << 16;
+// Low descriptor word of a V tile as MN-major B: rows of 64 channels (128 bytes), 8-key groups 1024 bytes
+// apart (the stride offset of kSdescHi), the next 64 channels a panel further (leading offset).
+__device__ __forceinline__ uint32_t vdesc_lo(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((128u * 128u >> 4) << 16);
+}
+
+template <int D, bool kE4M3>
+__device__ __forceinline__ void issue_qk(uint32_t s_tmem, uint32_t ql, uint32_t kl) {
+  constexpr uint32_t idesc = idesc_f32acc(kBM, kBN) | (kE4M3 ? 0u : kIdescBf16);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = ((kk >> 2) * ChunkCfg<D, kE4M3>::kPanelBytes + (kk & 3) * 32) >> 4;
+    mma_f16_ss(s_tmem, sdesc_of_lo(ql + off), sdesc_of_lo(kl + off), idesc, kk > 0 ? 1u : 0u);
+  }
+}
+// P: 16 keys in 8 tensor-memory columns; V: 16 keys are 2048 bytes.
+template <int D, bool kE4M3>
+__device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint32_t vl, bool first) {
+  constexpr uint32_t idesc = idesc_f32acc(kBM, D) | kIdescBmn | (kE4M3 ? 0u : kIdescBf16);
+#pragma unroll
+  for (int kk = 0; kk < kBN / 16; ++kk)
+    mma_f16_ts(o_tmem, p_tmem + kk * 8, sdesc_of_lo(vl + kk * (2048 >> 4)), idesc, (first && kk == 0) ? 0u : 1u);
+}
+
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t w;
+  if (kF16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
+
+// Bit k of word w: key 32 w + k of the tile lies in [lo, hi) and its box was loaded.
+__device__ __forceinline__ uint32_t key_mask(int w, int lo, int hi, uint32_t bits, int box_shift) {
+  const int l = max(lo - 32 * w, 0), h = min(hi - 32 * w, 32);
+  if (l >= h) return 0u;
+  uint32_t m = (h == 32 ? ~0u : (1u << h) - 1u) & ~((1u << l) - 1u);
+  if (box_shift >= 5) {
+    if (!((bits >> ((32 * w) >> box_shift)) & 1u)) m = 0u;
+  } else {
+    const int box = 1 << box_shift;
+    for (int k = 0; k < 32; k += box)
+      if (!((bits >> ((32 * w + k) >> box_shift)) & 1u)) m &= ~(((1u << box) - 1u) << k);
+  }
+  return m;
+}
+
+// One 128-key tile of the online softmax for the calling thread's row (= tensor-memory lane): S is read,
+// masked where kMask, its maximum taken; P = 2^(S c - m) is written in 16 bits, l the sum of the unrounded P; O is
+// multiplied by 2^(m_old - m) where the maximum rose by more than kRise.  With separate P columns S is
+// released as soon as it is in registers and P waits for the P.V of the tile before (pv_done).
+template <int D, bool kE4M3, bool kMask>
+__device__ __forceinline__ bool softmax_step(uint32_t tS, uint32_t tO, uint32_t tP, float c, const uint32_t mask[4],
+                                             bool first, float& m, float& l, uint64_t* s_free, uint64_t* pv_done, int j) {
+  constexpr bool kSep = ChunkCfg<D, kE4M3>::kSepP;
+  uint32_t sr[128];
+  SAGE_TMEM_LD32(tS + 0, (sr + 0));
+  SAGE_TMEM_LD32(tS + 32, (sr + 32));
+  SAGE_TMEM_LD32(tS + 64, (sr + 64));
+  SAGE_TMEM_LD32(tS + 96, (sr + 96));
+  tmem_wait_ld();
+  if (kSep) {
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(s_free);
+  }
+  if (kMask) {
+#pragma unroll
+    for (int k = 0; k < 128; ++k)
+      if (!((mask[k >> 5] >> (k & 31)) & 1u)) sr[k] = 0xFF800000u;   // -infinity
+  }
+  const float mx = fmaxf(max64(sr), max64(sr + 64)) * c;
+  const bool up = mx > m + kRise;          // also the first visible key: m is -infinity before it
+  const float alpha = (up && !first) ? ex2_approx(m - mx) : 1.0f;
+  const bool rise = up && !first;
+  if (up) m = mx;
+  const float base = (kMask && m == -INFINITY) ? 0.0f : m;   // no key so far: every P below is 0
+  const uint64_t bias2 = f2_pack(-base, -base), c2 = f2_pack(c, c);
+  uint64_t l2[4][2];
+  uint32_t pkeep[kSep ? 64 : 1];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t pw[16];
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const int k = q * 32 + w * 4;
+      float p[4];
+      f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), c2, bias2), p[0], p[1]);
+      f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[k + 2]), __uint_as_float(sr[k + 3])), c2, bias2), p[2], p[3]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = ex2_approx(p[i]);
+      if (w == 0) {
+        l2[q][0] = f2_pack(p[0], p[1]);
+        l2[q][1] = f2_pack(p[2], p[3]);
+      } else {
+        l2[q][0] = f2_add(l2[q][0], f2_pack(p[0], p[1]));
+        l2[q][1] = f2_add(l2[q][1], f2_pack(p[2], p[3]));
+      }
+      pw[2 * w] = pack2<kE4M3>(p[0], p[1]);
+      pw[2 * w + 1] = pack2<kE4M3>(p[2], p[3]);
+    }
+    if (kSep) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pkeep[q * 16 + i] = pw[i];
+    } else {
+      SAGE_TMEM_ST16(tS + q * 16, pw);
+    }
+  }
+  float x, y;
+  f2_unpack(f2_add(f2_add(f2_add(l2[0][0], l2[0][1]), f2_add(l2[1][0], l2[1][1])),
+                   f2_add(f2_add(l2[2][0], l2[2][1]), f2_add(l2[3][0], l2[3][1]))), x, y);
+  l = l * alpha + (x + y);
+  if (kSep) {
+    if (!first) {
+      if (!warp_wait(pv_done, (j - 1) & 1)) return false;
+      tc_fence_after();
+    }
+    SAGE_TMEM_ST32(tP, pkeep);
+    SAGE_TMEM_ST32(tP + 32, (pkeep + 32));
+  }
+  if (__any_sync(0xffffffffu, rise)) {
+    const uint64_t a2 = f2_pack(alpha, alpha);
+    uint32_t o[D];
+#pragma unroll
+    for (int i = 0; i < D; i += 32) SAGE_TMEM_LD32(tO + i, (o + i));
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < D; i += 2) {
+      float lo, hi;
+      f2_unpack(f2_mul(f2_pack(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), a2), lo, hi);
+      o[i] = __float_as_uint(lo);
+      o[i + 1] = __float_as_uint(hi);
+    }
+#pragma unroll
+    for (int i = 0; i < D; i += 32) SAGE_TMEM_ST32(tO + i, (o + i));
+  }
+  tmem_wait_st();
+  return true;
+}
+
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <int D, bool kE4M3>
+__global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                       const __grid_constant__ ChunkParams p) {
+  using C = ChunkCfg<D, kE4M3>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int s_skip;
+  __shared__ volatile int s_abort;
+  __shared__ Unit s_unit;
+  __shared__ uint32_t s_bits[C::kStages], s_raw_bits, s_tmem;
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* sQ = smem;
+  uint8_t* sKV = smem + C::kKvOff;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* kv_full = q_full + 1;
+  uint64_t* kv_empty = kv_full + C::kStages;
+  uint64_t* s_full = kv_empty + C::kStages;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* pv_done = p_full + 2;
+  uint64_t* s_free = pv_done + 2;
+  uint64_t* mma_final = s_free + 2;
+  uint64_t* raw_full = mma_final + 1;
+  uint64_t* raw_empty = raw_full + 1;
+  const PagedAttnArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (warp == 0) {
+    Unit u;
+    const bool found = find_unit(a, p.group, blockIdx.x, u);
+    if (lane == 0) {
+      s_skip = !found || *reinterpret_cast<volatile int32_t*>(a.status) == kStatusTimeout;
+      s_abort = 0;
+      if (found) {
+        // This CTA's share of the unit's key tiles; a share may be empty when there are few.
+        const int per = (u.nt + p.splits - 1) / p.splits;
+        const int from = min(u.nt, per * static_cast<int>(blockIdx.y));
+        u.t0 += from;
+        u.nt = min(per, u.nt - from);
+        s_unit = u;
+      }
+      mbar_init(q_full, found && u.rows > 128 ? 256 : 128);
+      for (int s = 0; s < C::kStages; ++s) {
+        mbar_init(kv_full + s, kE4M3 ? 128 : 1);
+        mbar_init(kv_empty + s, 1);
+      }
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(s_full + t, 1);
+        mbar_init(p_full + t, 128);
+        mbar_init(pv_done + t, 1);
+        mbar_init(s_free + t, 4);
+      }
+      mbar_init(mma_final, 1);
+      mbar_init(raw_full, 1);
+      mbar_init(raw_empty, 128);
+      fence_mbar_init();
+    }
+  }
+  __syncthreads();
+  if (s_skip) return;
+  const Unit u = s_unit;
+  const int nq = u.rows > 128 ? 2 : 1;     // 128-row tiles in use
+  const int ntiles = u.nt;
+  const int slot = u.index * p.splits + blockIdx.y;
+  if (ntiles == 0) {   // an empty share of a split unit
+    for (int r = threadIdx.x; r < u.rows; r += C::kThreads)
+      a.part_ml[slot * kPagedChunkRows + r] = make_float2(-INFINITY, 0.0f);
+    return;
+  }
+  if (warp == 2) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int boxes = kBN >> p.box_shift;
+
+  if (warp < 4) {
+    regs_dec<C::kRegsRoles>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ page table and TMA
+      tma_prefetch_desc(&kmap);
+      tma_prefetch_desc(&vmap);
+      if (lane == 0 && __ldg(a.b.kv_len + u.b) > a.b.cap) record_bad_index(a.status, kWhereLength);
+      const int box = 1 << p.box_shift;
+      const uint32_t box_bytes = 2u * static_cast<uint32_t>(box) * D * (kE4M3 ? 1 : 2);
+      const int32_t* row = a.b.table + u.b * a.b.table_stride;
+      bool ok = true;
+      int j = 0;
+      for (; j < ntiles; ++j) {
+        const int key0 = (u.t0 + j) * kBN + (lane << p.box_shift);
+        const bool need = lane < boxes && key0 < u.uhi && key0 + box > u.ulo;
+        int page = -1;
+        if (need) page = __ldg(row + (key0 >> a.b.page_shift));
+        const bool good = need && page >= 0 && page < a.b.n_pages;
+        if (need && !good) record_bad_index(a.status, kWherePage);
+        const uint32_t bits = __ballot_sync(0xffffffffu, good);
+        const int s = kE4M3 ? 0 : j % C::kStages;
+        uint64_t* full = kE4M3 ? raw_full : kv_full + s;
+        if (kE4M3 ? j >= 1 : j >= C::kStages)
+          ok = kE4M3 ? warp_wait(raw_empty, (j - 1) & 1) : warp_wait(kv_empty + s, (j / C::kStages - 1) & 1);
+        if (!ok) record_timeout(a.status, kWherePagedEmpty, &s_abort);
+        if (__any_sync(0xffffffffu, !ok || s_abort)) break;
+        if (lane == 0) {
+          if (kE4M3) s_raw_bits = bits;
+          else s_bits[s] = bits;
+          mbar_arrive_expect_tx(full, __popc(bits) * box_bytes);
+        }
+        __syncwarp();
+        if (good) {
+          const int slot_in_page = key0 & ((1 << a.b.page_shift) - 1);
+          if (kE4M3) {
+            const uint32_t raw = smem_u32(smem + C::kRawOff) + (lane << p.box_shift) * D;
+            tma_load_4d(raw, &kmap, full, 0, u.h, slot_in_page, page);
+            tma_load_4d(raw + C::kRawTile, &vmap, full, 0, u.h, slot_in_page, page);
+          } else {
+            const uint32_t sk = smem_u32(sKV + s * C::kStageBytes) + (lane << p.box_shift) * 128;
+#pragma unroll
+            for (int pn = 0; pn < C::kPanels; ++pn) {
+              tma_load_4d(sk + pn * C::kPanelBytes, &kmap, full, pn * 64, u.h, slot_in_page, page);
+              tma_load_4d(sk + C::kTileBytes + pn * C::kPanelBytes, &vmap, full, pn * 64, u.h, slot_in_page, page);
+            }
+          }
+        }
+      }
+      if (j < ntiles) {
+        // After a timeout: the copies issued have landed before the CTA ends.
+        if (kE4M3) {
+          if (j > 0) mbar_wait(raw_full, (j - 1) & 1, kChunkWaitNs);
+        } else {
+          for (int i = max(0, j - C::kStages); i < j; ++i)
+            mbar_wait(kv_full + i % C::kStages, (i / C::kStages) & 1, kChunkWaitNs);
+        }
+      }
+    } else if (warp == 1 && lane == 0) {
+      // ------------------------------------------------------------ MMA issue
+      const uint32_t colS = tmem, colO = tmem + C::kColO0, colP = tmem + C::kColP0;
+      const uint32_t q_lo = sdesc_lo(smem_u32(sQ)), k_lo = sdesc_lo(smem_u32(sKV)),
+                     v_lo = vdesc_lo(smem_u32(sKV) + C::kTileBytes);
+      constexpr uint32_t kQLo = C::kQTileBytes >> 4, kStageLo = C::kStageBytes >> 4;
+      bool ok = mbar_wait(q_full, 0, kChunkWaitNs) && mbar_wait(kv_full, 0, kChunkWaitNs);
+      if (!ok) record_timeout(a.status, kWherePagedFull, &s_abort);
+      if (ok) {
+        tc_fence_after();
+        for (int t = 0; t < nq; ++t) {
+          issue_qk<D, kE4M3>(colS + t * kBN, q_lo + t * kQLo, k_lo);
+          tc_commit(s_full + t);
+        }
+      }
+      int s = 0, sn = 1 % C::kStages;
+      uint32_t phn = 0;
+      for (int j = 0; ok && j < ntiles; ++j) {
+        const uint32_t k_next = k_lo + sn * kStageLo;
+        if (C::kSepP) {
+          // S_t of the next tile as soon as S_t is read, P.V once P_t is written.
+          if (j + 1 < ntiles) {
+            ok = mbar_wait(kv_full + sn, phn, kChunkWaitNs);
+            for (int t = 0; t < nq && ok; ++t) {
+              ok = mbar_wait(s_free + t, j & 1, kChunkWaitNs);
+              if (!ok) break;
+              tc_fence_after();
+              issue_qk<D, kE4M3>(colS + t * kBN, q_lo + t * kQLo, k_next);
+              tc_commit(s_full + t);
+            }
+          }
+          for (int t = 0; t < nq && ok; ++t) {
+            ok = mbar_wait(p_full + t, j & 1, kChunkWaitNs);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv<D, kE4M3>(colO + t * D, colP + t * C::kStepP, v_lo + s * kStageLo, j == 0);
+            tc_commit(pv_done + t);
+          }
+          if (ok) tc_commit(kv_empty + s);
+        } else {
+          for (int t = 0; t < nq && ok; ++t) {
+            ok = mbar_wait(p_full + t, j & 1, kChunkWaitNs);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv<D, kE4M3>(colO + t * D, colP + t * C::kStepP, v_lo + s * kStageLo, j == 0);
+            tc_commit(pv_done + t);
+            if (t == nq - 1) tc_commit(kv_empty + s);
+            if (j + 1 < ntiles) {
+              if (t == 0) ok = mbar_wait(kv_full + sn, phn, kChunkWaitNs);
+              // P_t lies in S_t's columns: the next S_t only once P_t.V is done.
+              ok = ok && mbar_wait(pv_done + t, j & 1, kChunkWaitNs);
+              if (!ok) break;
+              tc_fence_after();
+              issue_qk<D, kE4M3>(colS + t * kBN, q_lo + t * kQLo, k_next);
+              tc_commit(s_full + t);
+            }
+          }
+        }
+        if (!ok) record_timeout(a.status, kWherePagedMma, &s_abort);
+        s = sn;
+        if (++sn == C::kStages) {
+          sn = 0;
+          phn ^= 1u;
+        }
+      }
+      // Every MMA issued has finished before the tensor memory is freed.
+      tc_commit(mma_final);
+      mbar_wait(mma_final, 0, kChunkWaitNs);
+    }
+  } else if (kE4M3 && warp >= 12) {
+    // -------------------------------------------------------------- widen the codes
+    regs_dec<C::kRegsWiden>();
+    const int r = threadIdx.x - 384;   // the key of the tile
+    const uint32_t raw = smem_u32(smem + C::kRawOff) + r * D;
+    const uint32_t rsw = D == 128 ? (r & 7) : ((r >> 1) & 3);
+    for (int j = 0; j < ntiles; ++j) {
+      const int s = j % C::kStages;
+      bool ok = j < C::kStages || warp_wait(kv_empty + s, (j / C::kStages - 1) & 1);
+      ok = ok && warp_wait(raw_full, j & 1);
+      if (!ok) record_timeout(a.status, kWherePagedFull, &s_abort);
+      if (__any_sync(0xffffffffu, !ok || s_abort)) break;
+      const uint32_t bits = s_raw_bits;
+      const int key = (u.t0 + j) * kBN + r;
+      // Keys that no row sees count as zeros, whatever their slots hold.
+      const bool live = ((bits >> (r >> p.box_shift)) & 1u) && key >= u.ulo && key < u.uhi;
+      uint8_t* tile = sKV + s * C::kStageBytes;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+        for (int ch = 0; ch < D / 16; ++ch) {
+          uint4 v;
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "r"(raw + kv * C::kRawTile + ((ch ^ rsw) << 4)));
+          if (!live) v = make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t f[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f[2 * i]) : "h"(static_cast<uint16_t>(w[i])));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f[2 * i + 1]) : "h"(static_cast<uint16_t>(w[i] >> 16)));
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int c8 = ch * 2 + i;   // 8-channel chunk of the 16-bit row
+            *reinterpret_cast<uint4*>(tile + kv * C::kTileBytes + (c8 >> 3) * C::kPanelBytes + r * 128 +
+                                      (((c8 & 7) ^ (r & 7)) << 4)) =
+                make_uint4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+          }
+        }
+      }
+      if (r == 0) s_bits[s] = bits;
+      mbar_arrive(raw_empty);
+      fence_proxy_async_smem();
+      mbar_arrive(kv_full + s);
+    }
+  } else {
+    // -------------------------------------------------------------- softmax and epilogue
+    regs_inc<C::kRegsSoftmax>();
+    const int t = (warp - 4) >> 2, wq = warp & 3, r = wq * 32 + lane;
+    if (t < nq) {
+      // ---- Q: each warp its 32 rows, 8 lanes to a row's 128 bytes; rows past the last are zeros.
+      float* q_exp = reinterpret_cast<float*>(smem + C::kExpOff);
+      uint8_t* tile = sQ + t * C::kQTileBytes;
+      if (!kE4M3) {
+#pragma unroll 4
+        for (int i = 0; i < 8 * C::kPanels; ++i) {
+          const int rr = wq * 32 + (i / C::kPanels) * 4 + (lane >> 3), ch = lane & 7, pn = i % C::kPanels;
+          const int ur = t * 128 + rr, row = u.row0 + ur;
+          const bool valid = ur < u.rows;
+          const int tok = valid ? row / p.group : 0, hd = u.h * p.group + (valid ? row % p.group : 0);
+          const uint16_t* src = a.q + static_cast<int64_t>(u.start + tok) * a.qst + static_cast<int64_t>(hd) * a.qsh +
+                                pn * 64 + ch * 8;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           smem_u32(tile + pn * C::kPanelBytes + rr * 128 + ((ch ^ (rr & 7)) << 4))),
+                       "l"(src), "r"(valid ? 16 : 0)
+                       : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+      } else {
+        // fp16 times a power of two that brings the row's largest value into [1, 2): exact but for values
+        // 2^-14 below it, which keep an absolute error of 2^-25 of the row's largest.  D/8 lanes a row.
+        constexpr int kLanes = D / 8, kPer = 32 / kLanes;
+#pragma unroll 4
+        for (int i = 0; i < 32 / kPer; ++i) {
+          const int rr = wq * 32 + i * kPer + lane / kLanes, c8 = lane % kLanes;
+          const int ur = t * 128 + rr, row = u.row0 + ur;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (ur < u.rows)
+            v = __ldg(reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(u.start + row / p.group) * a.qst +
+                                                     static_cast<int64_t>(u.h * p.group + row % p.group) * a.qsh + c8 * 8));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          float mx = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          int e = static_cast<int>((__float_as_uint(mx) >> 23) & 255) - 127;
+          e = mx == 0.0f ? 0 : min(max(e, -126), 126);
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          uint32_t f[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            f[k] = pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+          *reinterpret_cast<uint4*>(tile + (c8 >> 3) * C::kPanelBytes + rr * 128 + (((c8 & 7) ^ (rr & 7)) << 4)) =
+              make_uint4(f[0], f[1], f[2], f[3]);
+          if (c8 == 0) q_exp[t * 128 + rr] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        }
+        __syncwarp();
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(q_full);
+
+      const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
+      const uint32_t tS = tmem + lane_base + t * kBN, tO = tmem + lane_base + C::kColO0 + t * D;
+      const uint32_t tP = tmem + lane_base + C::kColP0 + t * C::kStepP;
+      // This row's visible keys, and those that all rows of the tile see.
+      const int last = min(u.rows, t * 128 + 128) - 1, mine = min(t * 128 + r, last);
+      int klo, khi, alo, ahi, unused;
+      token_keys(a, u.len, u.n_new, (u.row0 + mine) / p.group, klo, khi);
+      token_keys(a, u.len, u.n_new, (u.row0 + t * 128) / p.group, unused, ahi);
+      token_keys(a, u.len, u.n_new, (u.row0 + last) / p.group, alo, unused);
+      const uint32_t all = boxes == 32 ? ~0u : (1u << boxes) - 1u;
+      const float c = kE4M3 ? a.scale_log2 * __ldg(a.k_scale + u.h) * q_exp[t * 128 + r] : a.scale_log2;
+      float m = -INFINITY, l = 0.0f;
+      bool ok = true;
+      for (int j = 0; j < ntiles; ++j) {
+        if (!warp_wait(s_full + t, j & 1)) {
+          if (lane == 0) record_timeout(a.status, kWherePagedMma, &s_abort);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int kb = (u.t0 + j) * kBN, s = j % C::kStages;
+        const uint32_t bits = s_bits[s];
+        uint32_t mask[4] = {0, 0, 0, 0};
+        bool stepped;
+        if (kb >= alo && kb + kBN <= ahi && bits == all) {
+          stepped = softmax_step<D, kE4M3, false>(tS, tO, tP, c, mask, j == 0, m, l, s_free + t, pv_done + t, j);
+        } else {
+          if (!kE4M3) {
+            // Keys that no row of the unit sees may hold anything: their V counts as 0.
+            const int key = kb + r;
+            if (!(((bits >> (r >> p.box_shift)) & 1u) && key >= u.ulo && key < u.uhi)) {
+              uint8_t* v = sKV + s * C::kStageBytes + C::kTileBytes + r * 128;
+#pragma unroll
+              for (int i = 0; i < 8 * C::kPanels; ++i)
+                *reinterpret_cast<uint4*>(v + (i >> 3) * C::kPanelBytes + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+#pragma unroll
+          for (int w = 0; w < 4; ++w) mask[w] = key_mask(w, klo - kb, khi - kb, bits, p.box_shift);
+          __syncwarp();
+          stepped = softmax_step<D, kE4M3, true>(tS, tO, tP, c, mask, j == 0, m, l, s_free + t, pv_done + t, j);
+        }
+        if (!stepped) {
+          if (lane == 0) record_timeout(a.status, kWherePagedMma, &s_abort);
+          ok = false;
+          break;
+        }
+        tc_fence_before();
+        mbar_arrive(p_full + t);
+      }
+      if (ok && !warp_wait(pv_done + t, (ntiles - 1) & 1)) {
+        if (lane == 0) record_timeout(a.status, kWherePagedMma, &s_abort);
+        ok = false;
+      }
+      if (ok) {
+        tc_fence_after();
+        const int ur = t * 128 + r;
+        const bool live = ur < u.rows;
+        const int row = u.row0 + (live ? ur : 0);
+        const int tok = u.start + row / p.group, hd = u.h * p.group + row % p.group;
+        const bool whole = p.splits == 1;
+        const float vs = kE4M3 ? __ldg(a.v_scale + u.h) : 1.0f;
+        const float inv = l > 0.0f ? vs / l : 0.0f;
+        uint16_t* orow = a.out + static_cast<int64_t>(tok) * a.ost + static_cast<int64_t>(hd) * a.osh;
+        float* prow = a.part_o + (static_cast<int64_t>(slot) * kPagedChunkRows + ur) * D;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t o[32];
+          __syncwarp();
+          SAGE_TMEM_LD32(tO + c0, o);
+          tmem_wait_ld();
+          if (live && whole) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack2<false>(__uint_as_float(o[i * 8 + 2 * k]) * inv, __uint_as_float(o[i * 8 + 2 * k + 1]) * inv);
+              // A row that saw no key: 0, whatever 0 times the V tiles gave.
+              *reinterpret_cast<uint4*>(orow + c0 + i * 8) =
+                  l > 0.0f || l != l ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0, 0, 0, 0);
+            }
+          } else if (live) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(prow + c0 + i * 4) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        if (live) {
+          if (!whole) a.part_ml[slot * kPagedChunkRows + ur] = make_float2(m, l);
+          else if (a.lse) a.lse[static_cast<int64_t>(tok) * a.hq + hd] = lse_of(m, l);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// The parts of split units, joined in the order of their keys: a CTA takes 8 rows of a unit, 32 threads
+// a row.
+template <int D>
+__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ ChunkParams p) {
+  const PagedAttnArgs& a = p.a;
+  const int lane = threadIdx.x & 31;
+  Unit u;
+  if (!find_unit(a, p.group, blockIdx.x, u)) return;
+  const int ur = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (ur >= u.rows) return;
+  const float2* ml = a.part_ml + static_cast<int64_t>(u.index) * p.splits * kPagedChunkRows + ur;
+  float m = -INFINITY, l = 0.0f;
+  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, ml[s * kPagedChunkRows].x);
+  constexpr int kC = D / 32;   // channels of a lane
+  float v[kC];
+#pragma unroll
+  for (int i = 0; i < kC; ++i) v[i] = 0.0f;
+  if (m != -INFINITY)
+    for (int s = 0; s < p.splits; ++s) {
+      const float2 x = ml[s * kPagedChunkRows];
+      if (x.x == -INFINITY) continue;     // saw no key: its O was not written, or counts nothing
+      const float f = ex2_approx(x.x - m);
+      const float* o = a.part_o + ((static_cast<int64_t>(u.index) * p.splits + s) * kPagedChunkRows + ur) * D + lane * kC;
+      l += x.y * f;
+#pragma unroll
+      for (int i = 0; i < kC; ++i) v[i] += o[i] * f;
+    }
+  const int row = u.row0 + ur, tok = u.start + row / p.group, hd = u.h * p.group + row % p.group;
+  const float inv = m == -INFINITY ? 0.0f : (a.v_scale ? __ldg(a.v_scale + u.h) : 1.0f) / l;
+  uint16_t* dst = a.out + static_cast<int64_t>(tok) * a.ost + static_cast<int64_t>(hd) * a.osh + lane * kC;
+#pragma unroll
+  for (int i = 0; i < kC; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = pack2<false>(v[i] * inv, v[i + 1] * inv);
+  if (a.lse && lane == 0) a.lse[static_cast<int64_t>(tok) * a.hq + hd] = lse_of(m, l);
+}
+
+template <int D, bool kE4M3>
+cudaError_t launch_t(const PagedAttnArgs& a, const sage_paged_kv& kv, cudaStream_t s) {
+  using C = ChunkCfg<D, kE4M3>;
+  ChunkParams p;
+  p.a = a;
+  if (!kE4M3) p.a.v_scale = nullptr;
+  p.group = a.hq / a.hkv;
+  p.box_shift = std::min(a.b.page_shift, 7);
+  const int64_t e = kE4M3 ? 1 : 2;
+  CUtensorMap kmap, vmap;
+  const int box_c = kE4M3 ? D : 64;
+  if (!make_page_map(&kmap, kv.k_pages, kE4M3, D, kv.n_heads, kv.page_size, kv.n_pages, kv.k_stride_head * e,
+                     kv.k_stride_token * e, kv.k_stride_page * e, box_c, 1 << p.box_shift) ||
+      !make_page_map(&vmap, kv.v_pages, kE4M3, D, kv.n_heads, kv.page_size, kv.n_pages, kv.v_stride_head * e,
+                     kv.v_stride_token * e, kv.v_stride_page * e, box_c, 1 << p.box_shift))
+    return cudaErrorInvalidValue;
+  int dev = 0, sms = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (err == cudaSuccess)
+    err = cudaFuncSetAttribute(paged_chunk_kernel<D, kE4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (err != cudaSuccess) return err;
+  // Units: sum over sequences of ceil(rows / 256), at most (all rows + 255 per sequence with tokens) / 256.
+  const int64_t rows = static_cast<int64_t>(a.b.n_tokens) * p.group;
+  const int64_t seqs = std::min<int64_t>(a.b.n_seqs, a.b.n_tokens);
+  const int64_t units = (rows + 255 * seqs) / 256 * a.hkv;
+  p.splits = 1;
+  paged_chunk_kernel<D, kE4M3><<<dim3(static_cast<unsigned>(units), p.splits), C::kThreads, C::kSmem, s>>>(kmap, vmap, p);
+  err = cudaGetLastError();
+  if (err == cudaSuccess && p.splits > 1) {
+    paged_join_kernel<D><<<dim3(static_cast<unsigned>(units), kPagedChunkRows / 8), 256, 0, s>>>(p);
+    err = cudaGetLastError();
+  }
+  return err;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_chunk(const PagedAttnArgs& a, const sage_paged_kv& c, int d, cudaStream_t s) {
+  if (d == 128) return c.format == 1 ? launch_t<128, true>(a, c, s) : launch_t<128, false>(a, c, s);
+  return c.format == 1 ? launch_t<64, true>(a, c, s) : launch_t<64, false>(a, c, s);
+}
+
+}  // namespace sage

@@ -69,5 +69,7 @@ struct PagedAttnArgs {
 
 // paged_few.cu: up to 32 query rows (tokens x query heads of one K/V head) per tile.
 cudaError_t launch_paged_few(const PagedAttnArgs& a, const sage_paged_kv& c, int d, cudaStream_t s);
+// paged_chunk.cu: 256 query rows per unit.
+cudaError_t launch_paged_chunk(const PagedAttnArgs& a, const sage_paged_kv& c, int d, cudaStream_t s);
 
 }  // namespace sage
