@@ -21,7 +21,7 @@
 // 8-11 softmax and epilogue of tile 0 and 1; with E4M3 warps 12-15 widen.  Every wait is bounded.
 //
 // What bounds it: 4 rows keys D FLOPs at the 16-bit tensor rate (for few rows the cache's bytes).  The key axis
-// is split over gridDim.y CTAs where the units alone leave SMs idle; each then leaves (maximum, sum, O) in the
+// is split over several CTAs for the units that do not fill the SMs a last time; each then leaves (maximum, sum, O) in the
 // workspace, and paged_join_kernel adds the parts in the order of their keys.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -72,6 +72,7 @@ struct ChunkParams {
   PagedAttnArgs a;
   int group;
   int box_shift;   // log2 of the slots per TMA box (a page, or 128)
+  int whole;       // units below this number are one CTA's; each of the rest is `splits` CTAs'
   int splits;
 };
 
@@ -98,7 +99,7 @@ struct Unit {
   int row0, rows;           // first row (token x group) of the unit, rows it has (at most 256)
   int t0, nt;               // its key tiles (this CTA's share of them)
   int ulo, uhi;             // keys that some row sees
-  int index;                // among all units of the call
+  int slot;                 // of its partial result; -1: the unit is one CTA's
 };
 
 __device__ __forceinline__ void token_keys(const PagedAttnArgs& a, int len, int n_new, int j, int& lo, int& hi) {
@@ -143,7 +144,6 @@ __device__ __forceinline__ bool find_unit(const PagedAttnArgs& a, int group, int
       token_keys(a, u.len, u.n_new, (u.row0 + u.rows - 1) / group, unused, u.uhi);
       u.t0 = u.ulo / kBN;
       u.nt = max(1, (u.uhi + kBN - 1) / kBN - u.t0);
-      u.index = index;
       return true;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
@@ -344,16 +344,22 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
 
   if (warp == 0) {
     Unit u;
-    const bool found = find_unit(a, p.group, blockIdx.x, u);
+    const int bx = blockIdx.x, split = bx >= p.whole;
+    const int part = split ? (bx - p.whole) % p.splits : 0;
+    const bool found = find_unit(a, p.group, split ? p.whole + (bx - p.whole) / p.splits : bx, u);
     if (lane == 0) {
       s_skip = !found || *reinterpret_cast<volatile int32_t*>(a.status) == kStatusTimeout;
       s_abort = 0;
       if (found) {
         // This CTA's share of the unit's key tiles; a share may be empty when there are few.
-        const int per = (u.nt + p.splits - 1) / p.splits;
-        const int from = min(u.nt, per * static_cast<int>(blockIdx.y));
-        u.t0 += from;
-        u.nt = min(per, u.nt - from);
+        u.slot = -1;
+        if (split) {
+          const int per = (u.nt + p.splits - 1) / p.splits;
+          const int from = min(u.nt, per * part);
+          u.t0 += from;
+          u.nt = min(per, u.nt - from);
+          u.slot = bx - p.whole;
+        }
         s_unit = u;
       }
       mbar_init(q_full, found && u.rows > 128 ? 256 : 128);
@@ -378,10 +384,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
   const Unit u = s_unit;
   const int nq = u.rows > 128 ? 2 : 1;     // 128-row tiles in use
   const int ntiles = u.nt;
-  const int slot = u.index * p.splits + blockIdx.y;
   if (ntiles == 0) {   // an empty share of a split unit
     for (int r = threadIdx.x; r < u.rows; r += C::kThreads)
-      a.part_ml[slot * kPagedChunkRows + r] = make_float2(-INFINITY, 0.0f);
+      a.part_ml[u.slot * kPagedChunkRows + r] = make_float2(-INFINITY, 0.0f);
     return;
   }
   if (warp == 2) {
@@ -686,11 +691,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
         const bool live = ur < u.rows;
         const int row = u.row0 + (live ? ur : 0);
         const int tok = u.start + row / p.group, hd = u.h * p.group + row % p.group;
-        const bool whole = p.splits == 1;
+        const bool whole = u.slot < 0;
         const float vs = kE4M3 ? __ldg(a.v_scale + u.h) : 1.0f;
         const float inv = l > 0.0f ? vs / l : 0.0f;
         uint16_t* orow = a.out + static_cast<int64_t>(tok) * a.ost + static_cast<int64_t>(hd) * a.osh;
-        float* prow = a.part_o + (static_cast<int64_t>(slot) * kPagedChunkRows + ur) * D;
+        float* prow = a.part_o + (static_cast<int64_t>(u.slot) * kPagedChunkRows + ur) * D;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t o[32];
@@ -715,7 +720,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
           }
         }
         if (live) {
-          if (!whole) a.part_ml[slot * kPagedChunkRows + ur] = make_float2(m, l);
+          if (!whole) a.part_ml[u.slot * kPagedChunkRows + ur] = make_float2(m, l);
           else if (a.lse) a.lse[static_cast<int64_t>(tok) * a.hq + hd] = lse_of(m, l);
         }
       }
@@ -735,11 +740,12 @@ template <int D>
 __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ ChunkParams p) {
   const PagedAttnArgs& a = p.a;
   const int lane = threadIdx.x & 31;
+  grid_dep_wait();
   Unit u;
-  if (!find_unit(a, p.group, blockIdx.x, u)) return;
+  if (!find_unit(a, p.group, p.whole + blockIdx.x, u)) return;
   const int ur = blockIdx.y * 8 + (threadIdx.x >> 5);
   if (ur >= u.rows) return;
-  const float2* ml = a.part_ml + static_cast<int64_t>(u.index) * p.splits * kPagedChunkRows + ur;
+  const float2* ml = a.part_ml + static_cast<int64_t>(blockIdx.x) * p.splits * kPagedChunkRows + ur;
   float m = -INFINITY, l = 0.0f;
   for (int s = 0; s < p.splits; ++s) m = fmaxf(m, ml[s * kPagedChunkRows].x);
   constexpr int kC = D / 32;   // channels of a lane
@@ -751,7 +757,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
       const float2 x = ml[s * kPagedChunkRows];
       if (x.x == -INFINITY) continue;     // saw no key: its O was not written, or counts nothing
       const float f = ex2_approx(x.x - m);
-      const float* o = a.part_o + ((static_cast<int64_t>(u.index) * p.splits + s) * kPagedChunkRows + ur) * D + lane * kC;
+      const float* o = a.part_o + ((static_cast<int64_t>(blockIdx.x) * p.splits + s) * kPagedChunkRows + ur) * D + lane * kC;
       l += x.y * f;
 #pragma unroll
       for (int i = 0; i < kC; ++i) v[i] += o[i] * f;
@@ -790,13 +796,22 @@ cudaError_t launch_t(const PagedAttnArgs& a, const sage_paged_kv& kv, cudaStream
   const int64_t rows = static_cast<int64_t>(a.b.n_tokens) * p.group;
   const int64_t seqs = std::min<int64_t>(a.b.n_seqs, a.b.n_tokens);
   const int64_t units = (rows + 255 * seqs) / 256 * a.hkv;
-  p.splits = 1;
-  paged_chunk_kernel<D, kE4M3><<<dim3(static_cast<unsigned>(units), p.splits), C::kThreads, C::kSmem, s>>>(kmap, vmap, p);
+  // Whole units fill the SMs as often as they can; those left over are split along the keys, into as many parts as
+  // shorten the last wave by a tenth or more each (ceil(rest splits / SMs) / splits of a unit's time).
+  const int64_t rest = units % sms;
+  const int64_t most = std::min<int64_t>({kPagedSlots / std::max<int64_t>(rest, 1), sms, std::max(1, a.b.cap / (4 * kBN))});
+  auto last_wave = [&](int64_t k) { return static_cast<double>((rest * k + sms - 1) / sms) / static_cast<double>(k); };
+  int64_t splits = 1;
+  for (int64_t k = 2; k <= most; ++k)
+    if (last_wave(k) < 0.9 * last_wave(splits)) splits = k;
+  p.splits = static_cast<int>(splits);
+  p.whole = static_cast<int>(splits > 1 ? units - rest : units);
+  const unsigned grid = static_cast<unsigned>(p.whole + (units - p.whole) * splits);
+  paged_chunk_kernel<D, kE4M3><<<grid, C::kThreads, C::kSmem, s>>>(kmap, vmap, p);
   err = cudaGetLastError();
-  if (err == cudaSuccess && p.splits > 1) {
-    paged_join_kernel<D><<<dim3(static_cast<unsigned>(units), kPagedChunkRows / 8), 256, 0, s>>>(p);
-    err = cudaGetLastError();
-  }
+  if (err == cudaSuccess && splits > 1)
+    err = launch_dependent(true, paged_join_kernel<D>, dim3(static_cast<unsigned>(rest), kPagedChunkRows / 8), dim3(256), 0,
+                           s, p);
   return err;
 }
 

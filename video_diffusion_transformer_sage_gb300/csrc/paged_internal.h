@@ -49,6 +49,7 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, int d, bool e4m3, cuda
 // The most CTAs whose partial results the workspace holds, and the rows of one partial result.
 constexpr int kPagedMaxCtas = 320;
 constexpr int kPagedChunkRows = 256;
+constexpr int kPagedSlots = 2 * kPagedMaxCtas;
 
 struct PagedAttnArgs {
   PagedBatchDev b;
