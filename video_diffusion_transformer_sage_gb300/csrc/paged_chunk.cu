@@ -9,7 +9,9 @@
 //                    (its own columns at D = 64)
 //   O_t += P_t V     A from tensor memory, B = V as it lies in the cache, keys by channels: the
 //                    MN-major operand of the 128-byte swizzle, so V is never transposed
-// as in attn_fwd.cu (Q tiles in turn, so one tile's softmax overlaps the other's MMAs).  O is rescaled only
+// as in attn_fwd.cu (Q tiles in turn, so one tile's softmax overlaps the other's MMAs).  A unit of at most 128
+// rows has one Q tile; its key tiles then go to the two slots t in turn, each with a maximum, sum and O of its
+// own, joined at the end: the same overlap, and half the steps.  O is rescaled only
 // when a row's maximum rises by more than 2^8 (P then stays below 2^8, far inside both 16-bit types
 // and fp32): the result is the same ratio, and most tiles rescale nothing.
 //
@@ -47,19 +49,24 @@ struct ChunkCfg {
   static constexpr int kQTileBytes = kBM * D * 2;
   static constexpr int kTileBytes = kBN * D * 2;              // a K or V tile in 16 bits
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kStages = D == 128 ? 2 : 4;            // with two row tiles
+  // With one row tile the second Q tile's shared memory holds another stage (D = 128, bf16).
+  static constexpr int kStages1 = D == 128 ? (kE4M3 ? 2 : 3) : 4;
+  static constexpr int kMaxStages = kStages1;
   static constexpr int kRawTile = kBN * D;                    // a tile of codes
   static constexpr int kRawBytes = kE4M3 ? 2 * kRawTile : 0;
   // Tensor memory columns: S_t at 128 t, O_t at 256 + D t; P_t over S_t, or at 384 + 64 t (D = 64).
   static constexpr int kColO0 = 256;
   static constexpr bool kSepP = D == 64;
   static constexpr int kColP0 = kSepP ? 384 : 0, kStepP = kSepP ? 64 : 128;
-  static constexpr int kKvOff = 2 * kQTileBytes;
-  static constexpr int kRawOff = kKvOff + kStages * kStageBytes;
+  static constexpr int kKvOff = 2 * kQTileBytes, kKvOff1 = kStages1 > kStages ? kQTileBytes : kKvOff;
+  static constexpr int kKvEnd = kKvOff + kStages * kStageBytes > kKvOff1 + kStages1 * kStageBytes
+                                    ? kKvOff + kStages * kStageBytes : kKvOff1 + kStages1 * kStageBytes;
+  static constexpr int kRawOff = kKvEnd;
   static constexpr int kExpOff = kRawOff + kRawBytes;         // 2^e of each Q row (E4M3)
   static constexpr int kBarOff = kExpOff + (kE4M3 ? 1024 : 0);
   // q_full, kv_full[S], kv_empty[S], s_full[2], p_full[2], pv_done[2], s_free[2], mma_final, raw_full, raw_empty
-  static constexpr int kNumBars = 1 + 2 * kStages + 8 + 3;
+  static constexpr int kNumBars = 1 + 2 * kMaxStages + 8 + 3;
   static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;
   // Registers a thread: launched at 168 (384 threads) or 128 (512).
   static constexpr int kRegsRoles = kE4M3 ? 56 : 72, kRegsSoftmax = kE4M3 ? 192 : 216, kRegsWiden = 72;
@@ -109,16 +116,30 @@ __device__ __forceinline__ void token_keys(const PagedAttnArgs& a, int len, int 
 }
 
 // Unit number `index` of the call, found by one warp; false past the last.  Units of a sequence and head
-// lie together, the later rows (more keys when causal) first.
+// lie together (they share K and V in L2), the later rows (more keys when causal) first.
 __device__ __forceinline__ bool find_unit(const PagedAttnArgs& a, int group, int index, Unit& u) {
   const int lane = threadIdx.x & 31;
   int base = 0;
   for (int b0 = 0; b0 < a.b.n_seqs; b0 += 32) {
-    int blocks = 0;
-    if (b0 + lane < a.b.n_seqs) {
+    int blocks = 0, seq = b0 + lane;
+    if (seq < a.b.n_seqs) {
       int s, e;
-      seq_rows(a.b, b0 + lane, s, e);
+      seq_rows(a.b, seq, s, e);
       blocks = ((e - s) * group + 255) / 256;
+    }
+    if (a.b.n_seqs > 1) {
+      // Among these 32, the longest sequences' units come first: the short ones fill the last wave.
+      const int n = min(32, a.b.n_seqs - b0);
+      const int len = lane < n ? __ldg(a.b.kv_len + seq) : INT32_MIN;
+      int rank = 0, from = lane;
+      for (int k = 0; k < n; ++k) {
+        const int x = __shfl_sync(0xffffffffu, len, k);
+        rank += x > len || (x == len && k < lane);
+      }
+      for (int k = 0; k < n; ++k)
+        if (__shfl_sync(0xffffffffu, rank, k) == lane) from = k;
+      blocks = __shfl_sync(0xffffffffu, blocks, from);
+      seq = b0 + from;
     }
     int incl = blocks * a.hkv;
 #pragma unroll
@@ -132,7 +153,7 @@ __device__ __forceinline__ bool find_unit(const PagedAttnArgs& a, int group, int
       const int nb = __shfl_sync(0xffffffffu, blocks, l);
       const int off = index - base - (__shfl_sync(0xffffffffu, incl, l) - nb * a.hkv);
       int e;
-      u.b = b0 + l;
+      u.b = __shfl_sync(0xffffffffu, seq, l);
       seq_rows(a.b, u.b, u.start, e);
       u.n_new = e - u.start;
       u.len = min(max(__ldg(a.b.kv_len + u.b), 0), a.b.cap);
@@ -220,11 +241,11 @@ __device__ __forceinline__ uint32_t key_mask(int w, int lo, int hi, uint32_t bit
 }
 
 // One 128-key tile of the online softmax for the calling thread's row (= tensor-memory lane): S is read,
-// masked where kMask, its maximum taken; P = 2^(S c - m) is written in 16 bits, l the sum of the unrounded P; O is
+// masked where `masked`, its maximum taken; P = 2^(S c - m) is written in 16 bits, l the sum of the unrounded P; O is
 // multiplied by 2^(m_old - m) where the maximum rose by more than kRise.  With separate P columns S is
 // released as soon as it is in registers and P waits for the P.V of the tile before (pv_done).
-template <int D, bool kE4M3, bool kMask>
-__device__ __forceinline__ bool softmax_step(uint32_t tS, uint32_t tO, uint32_t tP, float c, const uint32_t mask[4],
+template <int D, bool kE4M3, typename Mask>
+__device__ __forceinline__ bool softmax_step(uint32_t tS, uint32_t tO, uint32_t tP, float c, bool masked, Mask&& make_mask,
                                              bool first, float& m, float& l, uint64_t* s_free, uint64_t* pv_done, int j) {
   constexpr bool kSep = ChunkCfg<D, kE4M3>::kSepP;
   uint32_t sr[128];
@@ -238,7 +259,9 @@ __device__ __forceinline__ bool softmax_step(uint32_t tS, uint32_t tO, uint32_t 
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(s_free);
   }
-  if (kMask) {
+  if (masked) {
+    uint32_t mask[4];
+    make_mask(mask);
 #pragma unroll
     for (int k = 0; k < 128; ++k)
       if (!((mask[k >> 5] >> (k & 31)) & 1u)) sr[k] = 0xFF800000u;   // -infinity
@@ -248,7 +271,7 @@ __device__ __forceinline__ bool softmax_step(uint32_t tS, uint32_t tO, uint32_t 
   const float alpha = (up && !first) ? ex2_approx(m - mx) : 1.0f;
   const bool rise = up && !first;
   if (up) m = mx;
-  const float base = (kMask && m == -INFINITY) ? 0.0f : m;   // no key so far: every P below is 0
+  const float base = m == -INFINITY ? 0.0f : m;   // no key so far: every P below is 0
   const uint64_t bias2 = f2_pack(-base, -base), c2 = f2_pack(c, c);
   uint64_t l2[4][2];
   uint32_t pkeep[kSep ? 64 : 1];
@@ -316,88 +339,39 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <int D, bool kE4M3>
-__global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
-    paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                       const __grid_constant__ ChunkParams p) {
+// What the roles of a CTA share.
+struct ChunkShared {
+  Unit unit;
+  int skip;
+  volatile int abort;
+  uint32_t bits[4], raw_bits;   // boxes loaded, per stage and of the staging tile
+  uint32_t tmem;
+};
+
+// The roles of one CTA on its unit.  kOne: at most 128 rows, key tile j is slot j & 1's; otherwise both slots
+// (row tiles) take every key tile.
+template <int D, bool kE4M3, bool kOne>
+__device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUtensorMap& vmap, const ChunkParams& p,
+                                            ChunkShared& sh, uint8_t* smem) {
   using C = ChunkCfg<D, kE4M3>;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ int s_skip;
-  __shared__ volatile int s_abort;
-  __shared__ Unit s_unit;
-  __shared__ uint32_t s_bits[C::kStages], s_raw_bits, s_tmem;
-  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  constexpr int kStages = kOne ? C::kStages1 : C::kStages;
+  const PagedAttnArgs& a = p.a;
+  const Unit& u = sh.unit;
   uint8_t* sQ = smem;
-  uint8_t* sKV = smem + C::kKvOff;
+  uint8_t* sKV = smem + (kOne ? C::kKvOff1 : C::kKvOff);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* kv_full = q_full + 1;
-  uint64_t* kv_empty = kv_full + C::kStages;
-  uint64_t* s_full = kv_empty + C::kStages;
+  uint64_t* kv_empty = kv_full + C::kMaxStages;
+  uint64_t* s_full = kv_empty + C::kMaxStages;
   uint64_t* p_full = s_full + 2;
   uint64_t* pv_done = p_full + 2;
   uint64_t* s_free = pv_done + 2;
   uint64_t* mma_final = s_free + 2;
   uint64_t* raw_full = mma_final + 1;
   uint64_t* raw_empty = raw_full + 1;
-  const PagedAttnArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  if (warp == 0) {
-    Unit u;
-    const int bx = blockIdx.x, split = bx >= p.whole;
-    const int part = split ? (bx - p.whole) % p.splits : 0;
-    const bool found = find_unit(a, p.group, split ? p.whole + (bx - p.whole) / p.splits : bx, u);
-    if (lane == 0) {
-      s_skip = !found || *reinterpret_cast<volatile int32_t*>(a.status) == kStatusTimeout;
-      s_abort = 0;
-      if (found) {
-        // This CTA's share of the unit's key tiles; a share may be empty when there are few.
-        u.slot = -1;
-        if (split) {
-          const int per = (u.nt + p.splits - 1) / p.splits;
-          const int from = min(u.nt, per * part);
-          u.t0 += from;
-          u.nt = min(per, u.nt - from);
-          u.slot = bx - p.whole;
-        }
-        s_unit = u;
-      }
-      mbar_init(q_full, found && u.rows > 128 ? 256 : 128);
-      for (int s = 0; s < C::kStages; ++s) {
-        mbar_init(kv_full + s, kE4M3 ? 128 : 1);
-        mbar_init(kv_empty + s, 1);
-      }
-      for (int t = 0; t < 2; ++t) {
-        mbar_init(s_full + t, 1);
-        mbar_init(p_full + t, 128);
-        mbar_init(pv_done + t, 1);
-        mbar_init(s_free + t, 4);
-      }
-      mbar_init(mma_final, 1);
-      mbar_init(raw_full, 1);
-      mbar_init(raw_empty, 128);
-      fence_mbar_init();
-    }
-  }
-  __syncthreads();
-  if (s_skip) return;
-  const Unit u = s_unit;
-  const int nq = u.rows > 128 ? 2 : 1;     // 128-row tiles in use
-  const int ntiles = u.nt;
-  if (ntiles == 0) {   // an empty share of a split unit
-    for (int r = threadIdx.x; r < u.rows; r += C::kThreads)
-      a.part_ml[u.slot * kPagedChunkRows + r] = make_float2(-INFINITY, 0.0f);
-    return;
-  }
-  if (warp == 2) {
-    tmem_alloc(&s_tmem, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = s_tmem;
-  const int boxes = kBN >> p.box_shift;
+  const int ntiles = u.nt, boxes = kBN >> p.box_shift;
+  const uint32_t tmem = sh.tmem;
 
   if (warp < 4) {
     regs_dec<C::kRegsRoles>();
@@ -419,15 +393,15 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
         const bool good = need && page >= 0 && page < a.b.n_pages;
         if (need && !good) record_bad_index(a.status, kWherePage);
         const uint32_t bits = __ballot_sync(0xffffffffu, good);
-        const int s = kE4M3 ? 0 : j % C::kStages;
+        const int s = kE4M3 ? 0 : j % kStages;
         uint64_t* full = kE4M3 ? raw_full : kv_full + s;
-        if (kE4M3 ? j >= 1 : j >= C::kStages)
-          ok = kE4M3 ? warp_wait(raw_empty, (j - 1) & 1) : warp_wait(kv_empty + s, (j / C::kStages - 1) & 1);
-        if (!ok) record_timeout(a.status, kWherePagedEmpty, &s_abort);
-        if (__any_sync(0xffffffffu, !ok || s_abort)) break;
+        if (kE4M3 ? j >= 1 : j >= kStages)
+          ok = kE4M3 ? warp_wait(raw_empty, (j - 1) & 1) : warp_wait(kv_empty + s, (j / kStages - 1) & 1);
+        if (!ok) record_timeout(a.status, kWherePagedEmpty, &sh.abort);
+        if (__any_sync(0xffffffffu, !ok || sh.abort)) break;
         if (lane == 0) {
-          if (kE4M3) s_raw_bits = bits;
-          else s_bits[s] = bits;
+          if (kE4M3) sh.raw_bits = bits;
+          else sh.bits[s] = bits;
           mbar_arrive_expect_tx(full, __popc(bits) * box_bytes);
         }
         __syncwarp();
@@ -452,8 +426,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
         if (kE4M3) {
           if (j > 0) mbar_wait(raw_full, (j - 1) & 1, kChunkWaitNs);
         } else {
-          for (int i = max(0, j - C::kStages); i < j; ++i)
-            mbar_wait(kv_full + i % C::kStages, (i / C::kStages) & 1, kChunkWaitNs);
+          for (int i = max(0, j - kStages); i < j; ++i)
+            mbar_wait(kv_full + i % kStages, (i / kStages) & 1, kChunkWaitNs);
         }
       }
     } else if (warp == 1 && lane == 0) {
@@ -462,65 +436,110 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
       const uint32_t q_lo = sdesc_lo(smem_u32(sQ)), k_lo = sdesc_lo(smem_u32(sKV)),
                      v_lo = vdesc_lo(smem_u32(sKV) + C::kTileBytes);
       constexpr uint32_t kQLo = C::kQTileBytes >> 4, kStageLo = C::kStageBytes >> 4;
-      bool ok = mbar_wait(q_full, 0, kChunkWaitNs) && mbar_wait(kv_full, 0, kChunkWaitNs);
-      if (!ok) record_timeout(a.status, kWherePagedFull, &s_abort);
-      if (ok) {
+      bool ok = mbar_wait(q_full, 0, kChunkWaitNs);
+      // The ring stage of the next key tile to multiply with Q, its phase, and of the next one with P.
+      int sk = 0, sv = 0;
+      uint32_t ph = 0;
+      auto step_k = [&]() {
+        if (++sk == kStages) {
+          sk = 0;
+          ph ^= 1u;
+        }
+      };
+      auto step_v = [&]() {
+        if (++sv == kStages) sv = 0;
+      };
+      auto qk = [&](int t) {
         tc_fence_after();
-        for (int t = 0; t < nq; ++t) {
-          issue_qk<D, kE4M3>(colS + t * kBN, q_lo + t * kQLo, k_lo);
-          tc_commit(s_full + t);
+        issue_qk<D, kE4M3>(colS + t * kBN, q_lo + (kOne ? 0 : t * kQLo), k_lo + sk * kStageLo);
+        tc_commit(s_full + t);
+      };
+      auto pv = [&](int t, bool first) {
+        tc_fence_after();
+        issue_pv<D, kE4M3>(colO + t * D, colP + t * C::kStepP, v_lo + sv * kStageLo, first);
+        tc_commit(pv_done + t);
+      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, kChunkWaitNs); };
+      if (kOne) {
+        for (int j = 0; j < 2 && j < ntiles && ok; ++j) {
+          ok = wait(kv_full + sk, ph);
+          if (ok) qk(j);
+          step_k();
         }
-      }
-      int s = 0, sn = 1 % C::kStages;
-      uint32_t phn = 0;
-      for (int j = 0; ok && j < ntiles; ++j) {
-        const uint32_t k_next = k_lo + sn * kStageLo;
-        if (C::kSepP) {
-          // S_t of the next tile as soon as S_t is read, P.V once P_t is written.
-          if (j + 1 < ntiles) {
-            ok = mbar_wait(kv_full + sn, phn, kChunkWaitNs);
-            for (int t = 0; t < nq && ok; ++t) {
-              ok = mbar_wait(s_free + t, j & 1, kChunkWaitNs);
+        for (int j = 0; j < ntiles && ok; ++j) {
+          const int t = j & 1;
+          const uint32_t phase = (j >> 1) & 1;
+          const bool more = j + 2 < ntiles;
+          if (C::kSepP && more) {
+            // S_t of the slot's next tile as soon as S_t is read.
+            ok = wait(kv_full + sk, ph) && wait(s_free + t, phase);
+            if (!ok) break;
+            qk(t);
+            step_k();
+          }
+          ok = wait(p_full + t, phase);
+          if (!ok) break;
+          pv(t, j < 2);
+          tc_commit(kv_empty + sv);
+          step_v();
+          if (!C::kSepP && more) {
+            // P_t lies in S_t's columns: the next S_t only once P_t.V is done.
+            ok = wait(kv_full + sk, ph) && wait(pv_done + t, phase);
+            if (!ok) break;
+            qk(t);
+            step_k();
+          }
+        }
+      } else {
+        ok = ok && wait(kv_full, 0);
+        if (ok) {
+          qk(0);
+          qk(1);
+        }
+        step_k();
+        for (int j = 0; j < ntiles && ok; ++j) {
+          const uint32_t phase = j & 1;
+          const bool more = j + 1 < ntiles;
+          if (C::kSepP) {
+            if (more) {
+              ok = wait(kv_full + sk, ph) && wait(s_free, phase);
               if (!ok) break;
-              tc_fence_after();
-              issue_qk<D, kE4M3>(colS + t * kBN, q_lo + t * kQLo, k_next);
-              tc_commit(s_full + t);
+              qk(0);
+              ok = wait(s_free + 1, phase);
+              if (!ok) break;
+              qk(1);
+            }
+            ok = wait(p_full, phase);
+            if (!ok) break;
+            pv(0, j == 0);
+            ok = wait(p_full + 1, phase);
+            if (!ok) break;
+            pv(1, j == 0);
+            tc_commit(kv_empty + sv);
+          } else {
+            ok = wait(p_full, phase);
+            if (!ok) break;
+            pv(0, j == 0);
+            if (more) {
+              ok = wait(kv_full + sk, ph) && wait(pv_done, phase);
+              if (!ok) break;
+              qk(0);
+            }
+            ok = wait(p_full + 1, phase);
+            if (!ok) break;
+            pv(1, j == 0);
+            tc_commit(kv_empty + sv);
+            if (more) {
+              ok = wait(pv_done + 1, phase);
+              if (!ok) break;
+              qk(1);
             }
           }
-          for (int t = 0; t < nq && ok; ++t) {
-            ok = mbar_wait(p_full + t, j & 1, kChunkWaitNs);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv<D, kE4M3>(colO + t * D, colP + t * C::kStepP, v_lo + s * kStageLo, j == 0);
-            tc_commit(pv_done + t);
-          }
-          if (ok) tc_commit(kv_empty + s);
-        } else {
-          for (int t = 0; t < nq && ok; ++t) {
-            ok = mbar_wait(p_full + t, j & 1, kChunkWaitNs);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv<D, kE4M3>(colO + t * D, colP + t * C::kStepP, v_lo + s * kStageLo, j == 0);
-            tc_commit(pv_done + t);
-            if (t == nq - 1) tc_commit(kv_empty + s);
-            if (j + 1 < ntiles) {
-              if (t == 0) ok = mbar_wait(kv_full + sn, phn, kChunkWaitNs);
-              // P_t lies in S_t's columns: the next S_t only once P_t.V is done.
-              ok = ok && mbar_wait(pv_done + t, j & 1, kChunkWaitNs);
-              if (!ok) break;
-              tc_fence_after();
-              issue_qk<D, kE4M3>(colS + t * kBN, q_lo + t * kQLo, k_next);
-              tc_commit(s_full + t);
-            }
-          }
-        }
-        if (!ok) record_timeout(a.status, kWherePagedMma, &s_abort);
-        s = sn;
-        if (++sn == C::kStages) {
-          sn = 0;
-          phn ^= 1u;
+          step_k();
+          step_v();
         }
       }
+      if (!ok) record_timeout(a.status, kWherePagedMma, &sh.abort);
       // Every MMA issued has finished before the tensor memory is freed.
       tc_commit(mma_final);
       mbar_wait(mma_final, 0, kChunkWaitNs);
@@ -532,12 +551,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
     const uint32_t raw = smem_u32(smem + C::kRawOff) + r * D;
     const uint32_t rsw = D == 128 ? (r & 7) : ((r >> 1) & 3);
     for (int j = 0; j < ntiles; ++j) {
-      const int s = j % C::kStages;
-      bool ok = j < C::kStages || warp_wait(kv_empty + s, (j / C::kStages - 1) & 1);
+      const int s = j % kStages;
+      bool ok = j < kStages || warp_wait(kv_empty + s, (j / kStages - 1) & 1);
       ok = ok && warp_wait(raw_full, j & 1);
-      if (!ok) record_timeout(a.status, kWherePagedFull, &s_abort);
-      if (__any_sync(0xffffffffu, !ok || s_abort)) break;
-      const uint32_t bits = s_raw_bits;
+      if (!ok) record_timeout(a.status, kWherePagedFull, &sh.abort);
+      if (__any_sync(0xffffffffu, !ok || sh.abort)) break;
+      const uint32_t bits = sh.raw_bits;
       const int key = (u.t0 + j) * kBN + r;
       // Keys that no row sees count as zeros, whatever their slots hold.
       const bool live = ((bits >> (r >> p.box_shift)) & 1u) && key >= u.ulo && key < u.uhi;
@@ -567,7 +586,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
           }
         }
       }
-      if (r == 0) s_bits[s] = bits;
+      if (r == 0) sh.bits[s] = bits;
       mbar_arrive(raw_empty);
       fence_proxy_async_smem();
       mbar_arrive(kv_full + s);
@@ -576,9 +595,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
     // -------------------------------------------------------------- softmax and epilogue
     regs_inc<C::kRegsSoftmax>();
     const int t = (warp - 4) >> 2, wq = warp & 3, r = wq * 32 + lane;
-    if (t < nq) {
+    float* q_exp = reinterpret_cast<float*>(smem + C::kExpOff);
+    const int steps = kOne ? (ntiles + 1 - t) / 2 : ntiles;   // key tiles of this slot
+    if (!kOne || t == 0) {
       // ---- Q: each warp its 32 rows, 8 lanes to a row's 128 bytes; rows past the last are zeros.
-      float* q_exp = reinterpret_cast<float*>(smem + C::kExpOff);
       uint8_t* tile = sQ + t * C::kQTileBytes;
       if (!kE4M3) {
 #pragma unroll 4
@@ -629,71 +649,106 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
       }
       fence_proxy_async_smem();
       mbar_arrive(q_full);
-
+    }
+    {
       const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
       const uint32_t tS = tmem + lane_base + t * kBN, tO = tmem + lane_base + C::kColO0 + t * D;
       const uint32_t tP = tmem + lane_base + C::kColP0 + t * C::kStepP;
       // This row's visible keys, and those that all rows of the tile see.
-      const int last = min(u.rows, t * 128 + 128) - 1, mine = min(t * 128 + r, last);
+      const int first = kOne ? 0 : t * 128;   // the slot's first row
+      const int last = min(u.rows, first + 128) - 1, mine = min(first + r, last);
       int klo, khi, alo, ahi, unused;
       token_keys(a, u.len, u.n_new, (u.row0 + mine) / p.group, klo, khi);
-      token_keys(a, u.len, u.n_new, (u.row0 + t * 128) / p.group, unused, ahi);
+      token_keys(a, u.len, u.n_new, (u.row0 + first) / p.group, unused, ahi);
       token_keys(a, u.len, u.n_new, (u.row0 + last) / p.group, alo, unused);
       const uint32_t all = boxes == 32 ? ~0u : (1u << boxes) - 1u;
-      const float c = kE4M3 ? a.scale_log2 * __ldg(a.k_scale + u.h) * q_exp[t * 128 + r] : a.scale_log2;
+      float c = a.scale_log2;
+      if (kE4M3) {
+        if (kOne && t == 1) warp_wait(q_full, 0);   // the other warpgroup wrote the exponents
+        c *= __ldg(a.k_scale + u.h) * q_exp[first + r];
+      }
       float m = -INFINITY, l = 0.0f;
       bool ok = true;
-      for (int j = 0; j < ntiles; ++j) {
-        if (!warp_wait(s_full + t, j & 1)) {
-          if (lane == 0) record_timeout(a.status, kWherePagedMma, &s_abort);
+      const int t0 = u.t0;
+      for (int i = 0; i < steps; ++i) {
+        if (!warp_wait(s_full + t, i & 1)) {
+          if (lane == 0) record_timeout(a.status, kWherePagedMma, &sh.abort);
           ok = false;
           break;
         }
         tc_fence_after();
-        const int kb = (u.t0 + j) * kBN, s = j % C::kStages;
-        const uint32_t bits = s_bits[s];
-        uint32_t mask[4] = {0, 0, 0, 0};
-        bool stepped;
-        if (kb >= alo && kb + kBN <= ahi && bits == all) {
-          stepped = softmax_step<D, kE4M3, false>(tS, tO, tP, c, mask, j == 0, m, l, s_free + t, pv_done + t, j);
-        } else {
+        const int j = kOne ? 2 * i + t : i, kb = (t0 + j) * kBN, s = j % kStages;
+        const uint32_t bits = sh.bits[s];
+        const bool masked = kb < alo || kb + kBN > ahi || bits != all;
+        const bool stepped = softmax_step<D, kE4M3>(tS, tO, tP, c, masked, [&](uint32_t mask[4]) {
           if (!kE4M3) {
             // Keys that no row of the unit sees may hold anything: their V counts as 0.
             const int key = kb + r;
             if (!(((bits >> (r >> p.box_shift)) & 1u) && key >= u.ulo && key < u.uhi)) {
               uint8_t* v = sKV + s * C::kStageBytes + C::kTileBytes + r * 128;
 #pragma unroll
-              for (int i = 0; i < 8 * C::kPanels; ++i)
-                *reinterpret_cast<uint4*>(v + (i >> 3) * C::kPanelBytes + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+              for (int x = 0; x < 8 * C::kPanels; ++x)
+                *reinterpret_cast<uint4*>(v + (x >> 3) * C::kPanelBytes + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
           }
 #pragma unroll
           for (int w = 0; w < 4; ++w) mask[w] = key_mask(w, klo - kb, khi - kb, bits, p.box_shift);
-          __syncwarp();
-          stepped = softmax_step<D, kE4M3, true>(tS, tO, tP, c, mask, j == 0, m, l, s_free + t, pv_done + t, j);
-        }
+        }, i == 0, m, l, s_free + t, pv_done + t, i);
         if (!stepped) {
-          if (lane == 0) record_timeout(a.status, kWherePagedMma, &s_abort);
+          if (lane == 0) record_timeout(a.status, kWherePagedMma, &sh.abort);
           ok = false;
           break;
         }
         tc_fence_before();
         mbar_arrive(p_full + t);
       }
-      if (ok && !warp_wait(pv_done + t, (ntiles - 1) & 1)) {
-        if (lane == 0) record_timeout(a.status, kWherePagedMma, &s_abort);
+      if (ok && steps > 0 && !warp_wait(pv_done + t, (steps - 1) & 1)) {
+        if (lane == 0) record_timeout(a.status, kWherePagedMma, &sh.abort);
         ok = false;
       }
-      if (ok) {
-        tc_fence_after();
-        const int ur = t * 128 + r;
+      tc_fence_after();
+      float own = 1.0f, other = 0.0f;   // factors of slot 0's and slot 1's O (kOne)
+      if (kOne) {
+        // Slot 1's maximum, sum and O go to slot 0 through the K / V ring, which nothing reads any more once
+        // both slots are past their last P.V.  Both warpgroups meet both barriers whatever happened.
+        float4* xo = reinterpret_cast<float4*>(sKV) + r * (D / 4);
+        float2* xml = reinterpret_cast<float2*>(sKV + 128 * D * 4) + r;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (t == 1) {
+          if (steps > 0)
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t o[32];
+              SAGE_TMEM_LD32(tO + c0, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                xo[(c0 / 4 + i) ^ (r & 7)] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                         __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+            }
+          *xml = make_float2(m, l);
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (t == 0) {
+          const float2 x = *xml;
+          const float mm = fmaxf(m, x.x);
+          // A slot that saw no key counts nothing.
+          own = m == -INFINITY ? 0.0f : ex2_approx(m - mm);
+          other = x.x == -INFINITY ? 0.0f : ex2_approx(x.x - mm);
+          l = l * own + x.y * other;
+          m = mm;
+        }
+      }
+      if (ok && (!kOne || t == 0)) {
+        const int ur = first + r;
         const bool live = ur < u.rows;
         const int row = u.row0 + (live ? ur : 0);
         const int tok = u.start + row / p.group, hd = u.h * p.group + row % p.group;
         const bool whole = u.slot < 0;
         const float vs = kE4M3 ? __ldg(a.v_scale + u.h) : 1.0f;
-        const float inv = l > 0.0f ? vs / l : 0.0f;
+        // A row that saw no key (l = 0) becomes 0.
+        const float inv = whole ? (l > 0.0f ? vs / l : l) : 1.0f;
         uint16_t* orow = a.out + static_cast<int64_t>(tok) * a.ost + static_cast<int64_t>(hd) * a.osh;
         float* prow = a.part_o + (static_cast<int64_t>(u.slot) * kPagedChunkRows + ur) * D;
 #pragma unroll 1
@@ -702,6 +757,18 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
           __syncwarp();
           SAGE_TMEM_LD32(tO + c0, o);
           tmem_wait_ld();
+          if (kOne) {
+            const float4* xo = reinterpret_cast<const float4*>(sKV) + r * (D / 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (ntiles > 1) x = xo[(c0 / 4 + i) ^ (r & 7)];
+              o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * own + x.x * other);
+              o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * own + x.y * other);
+              o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * own + x.z * other);
+              o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * own + x.w * other);
+            }
+          }
           if (live && whole) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -709,9 +776,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 w[k] = pack2<false>(__uint_as_float(o[i * 8 + 2 * k]) * inv, __uint_as_float(o[i * 8 + 2 * k + 1]) * inv);
-              // A row that saw no key: 0, whatever 0 times the V tiles gave.
-              *reinterpret_cast<uint4*>(orow + c0 + i * 8) =
-                  l > 0.0f || l != l ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(orow + c0 + i * 8) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else if (live) {
 #pragma unroll
@@ -726,11 +791,73 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
       }
     }
   }
+}
+
+template <int D, bool kE4M3>
+__global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                       const __grid_constant__ ChunkParams p) {
+  using C = ChunkCfg<D, kE4M3>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ ChunkShared sh;
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const PagedAttnArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (warp == 0) {
+    Unit u;
+    const int bx = blockIdx.x, split = bx >= p.whole;
+    const int part = split ? (bx - p.whole) % p.splits : 0;
+    const bool found = find_unit(a, p.group, split ? p.whole + (bx - p.whole) / p.splits : bx, u);
+    if (lane == 0) {
+      sh.skip = !found || *reinterpret_cast<volatile int32_t*>(a.status) == kStatusTimeout;
+      sh.abort = 0;
+      if (found) {
+        // This CTA's share of the unit's key tiles; a share may be empty when there are few.
+        u.slot = -1;
+        if (split) {
+          const int per = (u.nt + p.splits - 1) / p.splits;
+          const int from = min(u.nt, per * part);
+          u.t0 += from;
+          u.nt = min(per, u.nt - from);
+          u.slot = bx - p.whole;
+        }
+        sh.unit = u;
+      }
+      uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+      mbar_init(bar++, found && u.rows > 128 ? 256 : 128);                                   // q_full
+      for (int s = 0; s < C::kMaxStages; ++s) mbar_init(bar++, kE4M3 ? 128 : 1);             // kv_full
+      for (int s = 0; s < C::kMaxStages + 2; ++s) mbar_init(bar++, 1);                       // kv_empty, s_full
+      for (int t = 0; t < 2; ++t) mbar_init(bar++, 128);                                     // p_full
+      for (int t = 0; t < 2; ++t) mbar_init(bar++, 1);                                       // pv_done
+      for (int t = 0; t < 2; ++t) mbar_init(bar++, 4);                                       // s_free
+      mbar_init(bar++, 1);                                                                   // mma_final
+      mbar_init(bar++, 1);                                                                   // raw_full
+      mbar_init(bar++, 128);                                                                 // raw_empty
+      fence_mbar_init();
+    }
+  }
+  __syncthreads();
+  if (sh.skip) return;
+  if (sh.unit.nt == 0) {   // an empty share of a split unit
+    for (int r = threadIdx.x; r < sh.unit.rows; r += C::kThreads)
+      a.part_ml[sh.unit.slot * kPagedChunkRows + r] = make_float2(-INFINITY, 0.0f);
+    return;
+  }
+  if (warp == 2) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (sh.unit.rows > 128) chunk_roles<D, kE4M3, false>(kmap, vmap, p, sh, smem);
+  else chunk_roles<D, kE4M3, true>(kmap, vmap, p, sh, smem);
   tc_fence_before();
   __syncthreads();
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(sh.tmem, 512);
   }
 }
 
