@@ -598,21 +598,26 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
     float* q_exp = reinterpret_cast<float*>(smem + C::kExpOff);
     const int steps = kOne ? (ntiles + 1 - t) / 2 : ntiles;   // key tiles of this slot
     if (!kOne || t == 0) {
-      // ---- Q: each warp its 32 rows, 8 lanes to a row's 128 bytes; rows past the last are zeros.
+      // ---- Q: each warp its 32 rows.  Lane i finds row i (one division), the others get it by shuffle.
       uint8_t* tile = sQ + t * C::kQTileBytes;
+      const int my = t * 128 + wq * 32 + lane, my_row = u.row0 + my;
+      const int64_t my_at = my < u.rows ? static_cast<int64_t>(u.start + my_row / p.group) * a.qst +
+                                              static_cast<int64_t>(u.h * p.group + my_row % p.group) * a.qsh
+                                        : -1;
+      const uint16_t* q = a.q;
       if (!kE4M3) {
-#pragma unroll 4
-        for (int i = 0; i < 8 * C::kPanels; ++i) {
-          const int rr = wq * 32 + (i / C::kPanels) * 4 + (lane >> 3), ch = lane & 7, pn = i % C::kPanels;
-          const int ur = t * 128 + rr, row = u.row0 + ur;
-          const bool valid = ur < u.rows;
-          const int tok = valid ? row / p.group : 0, hd = u.h * p.group + (valid ? row % p.group : 0);
-          const uint16_t* src = a.q + static_cast<int64_t>(u.start + tok) * a.qst + static_cast<int64_t>(hd) * a.qsh +
-                                pn * 64 + ch * 8;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                           smem_u32(tile + pn * C::kPanelBytes + rr * 128 + ((ch ^ (rr & 7)) << 4))),
-                       "l"(src), "r"(valid ? 16 : 0)
-                       : "memory");
+        // 8 lanes to a row's 128 bytes; rows past the last are zeros.
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = wq * 32 + i * 4 + (lane >> 3), ch = lane & 7;
+          const int64_t at = __shfl_sync(0xffffffffu, my_at, i * 4 + (lane >> 3));
+          const uint32_t n = at >= 0 ? 16 : 0;
+          const uint16_t* src = q + (at >= 0 ? at : 0) + ch * 8;
+#pragma unroll
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             smem_u32(tile + pn * C::kPanelBytes + rr * 128 + ((ch ^ (rr & 7)) << 4))),
+                         "l"(src + pn * 64), "r"(n));
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
       } else {
@@ -622,11 +627,9 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
 #pragma unroll 4
         for (int i = 0; i < 32 / kPer; ++i) {
           const int rr = wq * 32 + i * kPer + lane / kLanes, c8 = lane % kLanes;
-          const int ur = t * 128 + rr, row = u.row0 + ur;
+          const int64_t at = __shfl_sync(0xffffffffu, my_at, i * kPer + lane / kLanes);
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (ur < u.rows)
-            v = __ldg(reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(u.start + row / p.group) * a.qst +
-                                                     static_cast<int64_t>(u.h * p.group + row % p.group) * a.qsh + c8 * 8));
+          if (at >= 0) v = __ldg(reinterpret_cast<const uint4*>(q + at + c8 * 8));
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           float mx = 0.0f;
 #pragma unroll
@@ -749,40 +752,66 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
         const float vs = kE4M3 ? __ldg(a.v_scale + u.h) : 1.0f;
         // A row that saw no key (l = 0) becomes 0.
         const float inv = whole ? (l > 0.0f ? vs / l : l) : 1.0f;
-        uint16_t* orow = a.out + static_cast<int64_t>(tok) * a.ost + static_cast<int64_t>(hd) * a.osh;
-        float* prow = a.part_o + (static_cast<int64_t>(u.slot) * kPagedChunkRows + ur) * D;
+        // The rows leave through the slot's Q tile, which no MMA reads any more: each thread writes its own row
+        // there, 2 D bytes at a time (bf16 rows, or half an fp32 row of a partial result), and the warp
+        // stores whole rows.  Storing 16 bytes of 32 rows at a time took 2.0 us of a unit, this 0.9.
+        constexpr int kRowChunks = D / 8;
+        uint8_t* stage = sQ + t * C::kQTileBytes + wq * 32 * (2 * D);
+        const int64_t o_at = static_cast<int64_t>(tok) * a.ost + static_cast<int64_t>(hd) * a.osh;
+        float* part = whole ? nullptr : a.part_o + (static_cast<int64_t>(u.slot) * kPagedChunkRows + first + wq * 32) * D;
+        const int rows_here = u.rows - first - wq * 32;   // of this warp's 32
+        uint16_t* out = a.out;
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          uint32_t o[32];
+        for (int half = 0; half < (whole ? 1 : 2); ++half) {
+          const int c_end = whole ? D : (half + 1) * (D / 2);
+#pragma unroll 1
+          for (int c0 = half * (D / 2); c0 < c_end; c0 += 32) {
+            uint32_t o[32];
+            __syncwarp();
+            SAGE_TMEM_LD32(tO + c0, o);
+            tmem_wait_ld();
+            if (kOne) {
+              const float4* xo = reinterpret_cast<const float4*>(sKV) + r * (D / 4);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (ntiles > 1) x = xo[(c0 / 4 + i) ^ (r & 7)];
+                o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * own + x.x * other);
+                o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * own + x.y * other);
+                o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * own + x.z * other);
+                o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * own + x.w * other);
+              }
+            }
+            if (whole) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  w[k] = pack2<false>(__uint_as_float(o[i * 8 + 2 * k]) * inv, __uint_as_float(o[i * 8 + 2 * k + 1]) * inv);
+                *reinterpret_cast<uint4*>(stage + lane * (2 * D) + (((c0 / 8 + i) ^ (lane & 7)) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else {
+              const int b = (c0 - half * (D / 2)) / 4;
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(stage + lane * (2 * D) + (((b + i) ^ (lane & 7)) << 4)) =
+                    make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+          }
           __syncwarp();
-          SAGE_TMEM_LD32(tO + c0, o);
-          tmem_wait_ld();
-          if (kOne) {
-            const float4* xo = reinterpret_cast<const float4*>(sKV) + r * (D / 4);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (ntiles > 1) x = xo[(c0 / 4 + i) ^ (r & 7)];
-              o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * own + x.x * other);
-              o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * own + x.y * other);
-              o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * own + x.z * other);
-              o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * own + x.w * other);
+#pragma unroll 4
+          for (int i = 0; i < kRowChunks; ++i) {
+            const int rr = i * (32 / kRowChunks) + lane / kRowChunks, ch = lane % kRowChunks;
+            const int64_t at = __shfl_sync(0xffffffffu, o_at, rr);
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * (2 * D) + ((ch ^ (rr & 7)) << 4));
+            if (rr < rows_here) {
+              if (whole) *reinterpret_cast<uint4*>(out + at + ch * 8) = v;
+              else *reinterpret_cast<uint4*>(part + rr * D + half * (D / 2) + ch * 4) = v;
             }
           }
-          if (live && whole) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = pack2<false>(__uint_as_float(o[i * 8 + 2 * k]) * inv, __uint_as_float(o[i * 8 + 2 * k + 1]) * inv);
-              *reinterpret_cast<uint4*>(orow + c0 + i * 8) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          } else if (live) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4*>(prow + c0 + i * 4) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          }
+          __syncwarp();
         }
         if (live) {
           if (!whole) a.part_ml[u.slot * kPagedChunkRows + ur] = make_float2(m, l);

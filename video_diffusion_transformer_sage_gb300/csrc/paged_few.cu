@@ -290,15 +290,18 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok || s_abort) break;
       const uint32_t sq = smem_u32(smem + C::kQOff + buf * R * C::kQRow);
-#pragma unroll 4
-      for (int i = lane; i < R * (D / 8); i += 32) {
-        const int r = i / (D / 8), c = i % (D / 8), rr = qi * R + r;
-        const bool valid = rr < wk.w.rows;
-        const int tok = valid ? rr / p.group : 0, g = valid ? rr % p.group : 0;
-        cp_async16(sq + r * C::kQRow + c * 16,
-                   a.q + static_cast<int64_t>(wk.w.start + tok) * a.qst +
-                       static_cast<int64_t>(h * p.group + g) * a.qsh + c * 8,
-                   valid);
+      // Lane i finds row i (one division), the others get it by shuffle; rows past the last are zeros.
+      const int my = qi * R + lane;
+      const int64_t my_at = lane < R && my < wk.w.rows
+                                ? static_cast<int64_t>(wk.w.start + my / p.group) * a.qst +
+                                      static_cast<int64_t>(h * p.group + my % p.group) * a.qsh
+                                : -1;
+      constexpr int kLanes = D / 8;   // lanes to a row
+#pragma unroll
+      for (int i = 0; i < R * kLanes / 32; ++i) {
+        const int r = i * (32 / kLanes) + lane / kLanes, c = lane % kLanes;
+        const int64_t at = __shfl_sync(0xffffffffu, my_at, r);
+        cp_async16(sq + r * C::kQRow + c * 16, a.q + (at >= 0 ? at : 0) + c * 8, at >= 0);
       }
       cp_async_arrive(q_full + buf);
       // The keys any row of this tile sees.
