@@ -53,6 +53,10 @@ struct ChunkCfg {
   // With one row tile the second Q tile's shared memory holds another stage (D = 128, bf16).
   static constexpr int kStages1 = D == 128 ? (kE4M3 ? 2 : 3) : 4;
   static constexpr int kMaxStages = kStages1;
+  // K and V of a tile have barriers of their own where the ring is short (D = 128): a K stage is free again once
+  // Q K^T has read it, a softmax before P V is done with V (chunk_frames 2358 -> 2236 us).  The four stages at
+  // D = 64 hide the loads anyway, and there the extra waits of the issuing thread cost 5 %.
+  static constexpr bool kSplitKV = D == 128;
   static constexpr int kRawTile = kBN * D;                    // a tile of codes
   static constexpr int kRawBytes = kE4M3 ? 2 * kRawTile : 0;
   // Tensor memory columns: S_t at 128 t, O_t at 256 + D t; P_t over S_t, or at 384 + 64 t (D = 64).
@@ -65,8 +69,9 @@ struct ChunkCfg {
   static constexpr int kRawOff = kKvEnd;
   static constexpr int kExpOff = kRawOff + kRawBytes;         // 2^e of each Q row (E4M3)
   static constexpr int kBarOff = kExpOff + (kE4M3 ? 1024 : 0);
-  // q_full, kv_full[S], kv_empty[S], s_full[2], p_full[2], pv_done[2], s_free[2], mma_final, raw_full, raw_empty
-  static constexpr int kNumBars = 1 + 2 * kMaxStages + 8 + 3;
+  // q_full, k_full[S], v_full[S], k_empty[S], v_empty[S], s_full[2], p_full[2], pv_done[2], s_free[2], mma_final,
+  // raw_full[2] (K, V), raw_empty[2]
+  static constexpr int kNumBars = 1 + 4 * kMaxStages + 8 + 5;
   static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;
   // Registers a thread: launched at 168 (384 threads) or 128 (512).
   static constexpr int kRegsRoles = kE4M3 ? 56 : 72, kRegsSoftmax = kE4M3 ? 192 : 216, kRegsWiden = 72;
@@ -344,7 +349,7 @@ struct ChunkShared {
   Unit unit;
   int skip;
   volatile int abort;
-  uint32_t bits[4], raw_bits;   // boxes loaded, per stage and of the staging tile
+  uint32_t bits[8], raw_bits[2];   // boxes loaded: of the last key tiles, and of the staging K and V tile
   uint32_t tmem;
 };
 
@@ -360,15 +365,17 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + (kOne ? C::kKvOff1 : C::kKvOff);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-  uint64_t* kv_full = q_full + 1;
-  uint64_t* kv_empty = kv_full + C::kMaxStages;
-  uint64_t* s_full = kv_empty + C::kMaxStages;
+  uint64_t* k_full = q_full + 1;
+  uint64_t* v_full = k_full + C::kMaxStages;
+  uint64_t* k_empty = v_full + C::kMaxStages;
+  uint64_t* v_empty = k_empty + C::kMaxStages;
+  uint64_t* s_full = v_empty + C::kMaxStages;
   uint64_t* p_full = s_full + 2;
   uint64_t* pv_done = p_full + 2;
   uint64_t* s_free = pv_done + 2;
   uint64_t* mma_final = s_free + 2;
   uint64_t* raw_full = mma_final + 1;
-  uint64_t* raw_empty = raw_full + 1;
+  uint64_t* raw_empty = raw_full + 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ntiles = u.nt, boxes = kBN >> p.box_shift;
   const uint32_t tmem = sh.tmem;
@@ -381,53 +388,64 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
       tma_prefetch_desc(&vmap);
       if (lane == 0 && __ldg(a.b.kv_len + u.b) > a.b.cap) record_bad_index(a.status, kWhereLength);
       const int box = 1 << p.box_shift;
-      const uint32_t box_bytes = 2u * static_cast<uint32_t>(box) * D * (kE4M3 ? 1 : 2);
+      const uint32_t box_bytes = static_cast<uint32_t>(box) * D * (kE4M3 ? 1 : 2);
       const int32_t* row = a.b.table + u.b * a.b.table_stride;
+      const int h = u.h, t0 = u.t0, ulo = u.ulo, uhi = u.uhi;
       bool ok = true;
-      int j = 0;
-      for (; j < ntiles; ++j) {
-        const int key0 = (u.t0 + j) * kBN + (lane << p.box_shift);
-        const bool need = lane < boxes && key0 < u.uhi && key0 + box > u.ulo;
+      int j = 0, kv = 0;
+      for (; j < ntiles && ok; ++j) {
+        const int key0 = (t0 + j) * kBN + (lane << p.box_shift);
+        const bool need = lane < boxes && key0 < uhi && key0 + box > ulo;
         int page = -1;
         if (need) page = __ldg(row + (key0 >> a.b.page_shift));
         const bool good = need && page >= 0 && page < a.b.n_pages;
         if (need && !good) record_bad_index(a.status, kWherePage);
         const uint32_t bits = __ballot_sync(0xffffffffu, good);
-        const int s = kE4M3 ? 0 : j % kStages;
-        uint64_t* full = kE4M3 ? raw_full : kv_full + s;
-        if (kE4M3 ? j >= 1 : j >= kStages)
-          ok = kE4M3 ? warp_wait(raw_empty, (j - 1) & 1) : warp_wait(kv_empty + s, (j / kStages - 1) & 1);
-        if (!ok) record_timeout(a.status, kWherePagedEmpty, &sh.abort);
-        if (__any_sync(0xffffffffu, !ok || sh.abort)) break;
-        if (lane == 0) {
-          if (kE4M3) sh.raw_bits = bits;
-          else sh.bits[s] = bits;
-          mbar_arrive_expect_tx(full, __popc(bits) * box_bytes);
-        }
-        __syncwarp();
-        if (good) {
-          const int slot_in_page = key0 & ((1 << a.b.page_shift) - 1);
+        const int slot_in_page = key0 & ((1 << a.b.page_shift) - 1);
+        const int s = j % kStages;
+        for (kv = 0; kv < 2; ++kv) {
+          const CUtensorMap* map = kv ? &vmap : &kmap;
+          const bool own_bar = C::kSplitKV || kv == 0;   // V shares K's barriers otherwise
+          uint64_t* full = kE4M3 ? raw_full + kv : (kv && own_bar ? v_full : k_full) + s;
           if (kE4M3) {
-            const uint32_t raw = smem_u32(smem + C::kRawOff) + (lane << p.box_shift) * D;
-            tma_load_4d(raw, &kmap, full, 0, u.h, slot_in_page, page);
-            tma_load_4d(raw + C::kRawTile, &vmap, full, 0, u.h, slot_in_page, page);
-          } else {
-            const uint32_t sk = smem_u32(sKV + s * C::kStageBytes) + (lane << p.box_shift) * 128;
+            if (j >= 1) ok = warp_wait(raw_empty + kv, (j - 1) & 1);
+          } else if (own_bar && j >= kStages) {
+            ok = warp_wait((kv || !C::kSplitKV ? v_empty : k_empty) + s, (j / kStages - 1) & 1);
+          }
+          if (!ok) record_timeout(a.status, kWherePagedEmpty, &sh.abort);
+          ok = !__any_sync(0xffffffffu, !ok || sh.abort);
+          if (!ok) break;
+          if (lane == 0) {
+            if (kE4M3) sh.raw_bits[kv] = bits;
+            else if (kv == 0) sh.bits[j % (2 * kStages)] = bits;
+            if (kE4M3 || own_bar)
+              mbar_arrive_expect_tx(full, __popc(bits) * box_bytes * (kE4M3 || C::kSplitKV ? 1u : 2u));
+          }
+          __syncwarp();
+          if (good) {
+            if (kE4M3) {
+              tma_load_4d(smem_u32(smem + C::kRawOff) + kv * C::kRawTile + (lane << p.box_shift) * D, map, full, 0, h,
+                          slot_in_page, page);
+            } else {
+              const uint32_t dst = smem_u32(sKV + s * C::kStageBytes) + kv * C::kTileBytes + (lane << p.box_shift) * 128;
 #pragma unroll
-            for (int pn = 0; pn < C::kPanels; ++pn) {
-              tma_load_4d(sk + pn * C::kPanelBytes, &kmap, full, pn * 64, u.h, slot_in_page, page);
-              tma_load_4d(sk + C::kTileBytes + pn * C::kPanelBytes, &vmap, full, pn * 64, u.h, slot_in_page, page);
+              for (int pn = 0; pn < C::kPanels; ++pn)
+                tma_load_4d(dst + pn * C::kPanelBytes, map, full, pn * 64, h, slot_in_page, page);
             }
           }
         }
+        if (!ok) break;
       }
-      if (j < ntiles) {
-        // After a timeout: the copies issued have landed before the CTA ends.
+      if (!ok) {
+        // After a timeout: the copies issued (K tiles up to nk, V tiles up to j) have landed before the CTA ends.
+        const int nk = j + (kv > 0 ? 1 : 0);   // (without split barriers kv is 0 here)
         if (kE4M3) {
-          if (j > 0) mbar_wait(raw_full, (j - 1) & 1, kChunkWaitNs);
+          if (nk > 0) mbar_wait(raw_full, (nk - 1) & 1, kChunkWaitNs);
+          if (j > 0) mbar_wait(raw_full + 1, (j - 1) & 1, kChunkWaitNs);
         } else {
-          for (int i = max(0, j - kStages); i < j; ++i)
-            mbar_wait(kv_full + i % kStages, (i / kStages) & 1, kChunkWaitNs);
+          for (int i = max(0, nk - kStages); i < nk; ++i) mbar_wait(k_full + i % kStages, (i / kStages) & 1, kChunkWaitNs);
+          for (int i = max(0, j - kStages); C::kSplitKV && i < j; ++i)
+            mbar_wait(v_full + i % kStages, (i / kStages) & 1, kChunkWaitNs);
         }
       }
     } else if (warp == 1 && lane == 0) {
@@ -437,18 +455,24 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
                      v_lo = vdesc_lo(smem_u32(sKV) + C::kTileBytes);
       constexpr uint32_t kQLo = C::kQTileBytes >> 4, kStageLo = C::kStageBytes >> 4;
       bool ok = mbar_wait(q_full, 0, kChunkWaitNs);
-      // The ring stage of the next key tile to multiply with Q, its phase, and of the next one with P.
+      // The ring stage and phase of the next K tile and of the next V tile.
       int sk = 0, sv = 0;
-      uint32_t ph = 0;
+      uint32_t phk = 0, phv = 0;
       auto step_k = [&]() {
+        if (C::kSplitKV) tc_commit(k_empty + sk);
         if (++sk == kStages) {
           sk = 0;
-          ph ^= 1u;
+          phk ^= 1u;
         }
       };
       auto step_v = [&]() {
-        if (++sv == kStages) sv = 0;
+        tc_commit(v_empty + sv);
+        if (++sv == kStages) {
+          sv = 0;
+          phv ^= 1u;
+        }
       };
+      auto v_ready = [&]() { return !C::kSplitKV || mbar_wait(v_full + sv, phv, kChunkWaitNs); };
       auto qk = [&](int t) {
         tc_fence_after();
         issue_qk<D, kE4M3>(colS + t * kBN, q_lo + (kOne ? 0 : t * kQLo), k_lo + sk * kStageLo);
@@ -462,8 +486,9 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
       auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, kChunkWaitNs); };
       if (kOne) {
         for (int j = 0; j < 2 && j < ntiles && ok; ++j) {
-          ok = wait(kv_full + sk, ph);
-          if (ok) qk(j);
+          ok = wait(k_full + sk, phk);
+          if (!ok) break;
+          qk(j);
           step_k();
         }
         for (int j = 0; j < ntiles && ok; ++j) {
@@ -472,71 +497,70 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
           const bool more = j + 2 < ntiles;
           if (C::kSepP && more) {
             // S_t of the slot's next tile as soon as S_t is read.
-            ok = wait(kv_full + sk, ph) && wait(s_free + t, phase);
+            ok = wait(k_full + sk, phk) && wait(s_free + t, phase);
             if (!ok) break;
             qk(t);
             step_k();
           }
-          ok = wait(p_full + t, phase);
+          ok = wait(p_full + t, phase) && v_ready();
           if (!ok) break;
           pv(t, j < 2);
-          tc_commit(kv_empty + sv);
           step_v();
           if (!C::kSepP && more) {
             // P_t lies in S_t's columns: the next S_t only once P_t.V is done.
-            ok = wait(kv_full + sk, ph) && wait(pv_done + t, phase);
+            ok = wait(k_full + sk, phk) && wait(pv_done + t, phase);
             if (!ok) break;
             qk(t);
             step_k();
           }
         }
       } else {
-        ok = ok && wait(kv_full, 0);
+        ok = ok && wait(k_full, 0);
         if (ok) {
           qk(0);
           qk(1);
+          step_k();
         }
-        step_k();
         for (int j = 0; j < ntiles && ok; ++j) {
           const uint32_t phase = j & 1;
           const bool more = j + 1 < ntiles;
           if (C::kSepP) {
             if (more) {
-              ok = wait(kv_full + sk, ph) && wait(s_free, phase);
+              ok = wait(k_full + sk, phk) && wait(s_free, phase);
               if (!ok) break;
               qk(0);
               ok = wait(s_free + 1, phase);
               if (!ok) break;
               qk(1);
+              step_k();
             }
-            ok = wait(p_full, phase);
+            ok = wait(p_full, phase) && v_ready();
             if (!ok) break;
             pv(0, j == 0);
             ok = wait(p_full + 1, phase);
             if (!ok) break;
             pv(1, j == 0);
-            tc_commit(kv_empty + sv);
+            step_v();
           } else {
-            ok = wait(p_full, phase);
+            ok = wait(p_full, phase) && v_ready();
             if (!ok) break;
             pv(0, j == 0);
             if (more) {
-              ok = wait(kv_full + sk, ph) && wait(pv_done, phase);
+              ok = wait(k_full + sk, phk) && wait(pv_done, phase);
               if (!ok) break;
               qk(0);
             }
             ok = wait(p_full + 1, phase);
             if (!ok) break;
             pv(1, j == 0);
-            tc_commit(kv_empty + sv);
+            step_v();
             if (more) {
               ok = wait(pv_done + 1, phase);
               if (!ok) break;
               qk(1);
+              step_k();
             }
           }
-          step_k();
-          step_v();
         }
       }
       if (!ok) record_timeout(a.status, kWherePagedMma, &sh.abort);
@@ -550,32 +574,38 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
     const int r = threadIdx.x - 384;   // the key of the tile
     const uint32_t raw = smem_u32(smem + C::kRawOff) + r * D;
     const uint32_t rsw = D == 128 ? (r & 7) : ((r >> 1) & 3);
+    const int key_r = u.t0 * kBN + r, ulo = u.ulo, uhi = u.uhi;
     for (int j = 0; j < ntiles; ++j) {
       const int s = j % kStages;
-      bool ok = j < kStages || warp_wait(kv_empty + s, (j / kStages - 1) & 1);
-      ok = ok && warp_wait(raw_full, j & 1);
-      if (!ok) record_timeout(a.status, kWherePagedFull, &sh.abort);
-      if (__any_sync(0xffffffffu, !ok || sh.abort)) break;
-      const uint32_t bits = sh.raw_bits;
-      const int key = (u.t0 + j) * kBN + r;
-      // Keys that no row sees count as zeros, whatever their slots hold.
-      const bool live = ((bits >> (r >> p.box_shift)) & 1u) && key >= u.ulo && key < u.uhi;
       uint8_t* tile = sKV + s * C::kStageBytes;
+      bool ok = true;
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
+        if (j >= kStages && (C::kSplitKV || kv == 0))
+          ok = warp_wait((kv || !C::kSplitKV ? v_empty : k_empty) + s, (j / kStages - 1) & 1);
+        ok = ok && warp_wait(raw_full + kv, j & 1);
+        if (!ok) record_timeout(a.status, kWherePagedFull, &sh.abort);
+        ok = !__any_sync(0xffffffffu, !ok || sh.abort);
+        if (!ok) break;
+        const uint32_t bits = sh.raw_bits[kv];
+        const int key = key_r + j * kBN;
+        // Keys that no row sees count as zeros, whatever their slots hold.
+        const bool live = ((bits >> (r >> p.box_shift)) & 1u) && key >= ulo && key < uhi;
+        uint4 v[D / 16];
+#pragma unroll
+        for (int ch = 0; ch < D / 16; ++ch)
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(v[ch].x), "=r"(v[ch].y), "=r"(v[ch].z), "=r"(v[ch].w)
+                       : "r"(raw + kv * C::kRawTile + ((ch ^ rsw) << 4)));
+        if (r == 0 && kv == 0) sh.bits[j % (2 * kStages)] = bits;
 #pragma unroll
         for (int ch = 0; ch < D / 16; ++ch) {
-          uint4 v;
-          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                       : "r"(raw + kv * C::kRawTile + ((ch ^ rsw) << 4)));
-          if (!live) v = make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t w[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
           uint32_t f[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f[2 * i]) : "h"(static_cast<uint16_t>(w[i])));
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f[2 * i + 1]) : "h"(static_cast<uint16_t>(w[i] >> 16)));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f[2 * i]) : "h"(static_cast<uint16_t>(live ? w[i] : 0u)));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f[2 * i + 1]) : "h"(static_cast<uint16_t>(live ? w[i] >> 16 : 0u)));
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -585,11 +615,11 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
                 make_uint4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
           }
         }
+        mbar_arrive(raw_empty + kv);
+        fence_proxy_async_smem();
+        if (C::kSplitKV || kv == 1) mbar_arrive((kv && C::kSplitKV ? v_full : k_full) + s);
       }
-      if (r == 0) sh.bits[s] = bits;
-      mbar_arrive(raw_empty);
-      fence_proxy_async_smem();
-      mbar_arrive(kv_full + s);
+      if (!ok) break;
     }
   } else {
     // -------------------------------------------------------------- softmax and epilogue
@@ -681,12 +711,13 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
         }
         tc_fence_after();
         const int j = kOne ? 2 * i + t : i, kb = (t0 + j) * kBN, s = j % kStages;
-        const uint32_t bits = sh.bits[s];
+        const uint32_t bits = sh.bits[j % (2 * kStages)];
         const bool masked = kb < alo || kb + kBN > ahi || bits != all;
         const bool stepped = softmax_step<D, kE4M3>(tS, tO, tP, c, masked, [&](uint32_t mask[4]) {
           if (!kE4M3) {
             // Keys that no row of the unit sees may hold anything: their V counts as 0.
             const int key = kb + r;
+            if (C::kSplitKV && !warp_wait(v_full + s, (j / kStages) & 1)) record_timeout(a.status, kWherePagedFull, &sh.abort);
             if (!(((bits >> (r >> p.box_shift)) & 1u) && key >= u.ulo && key < u.uhi)) {
               uint8_t* v = sKV + s * C::kStageBytes + C::kTileBytes + r * 128;
 #pragma unroll
@@ -855,14 +886,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
       }
       uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
       mbar_init(bar++, found && u.rows > 128 ? 256 : 128);                                   // q_full
-      for (int s = 0; s < C::kMaxStages; ++s) mbar_init(bar++, kE4M3 ? 128 : 1);             // kv_full
-      for (int s = 0; s < C::kMaxStages + 2; ++s) mbar_init(bar++, 1);                       // kv_empty, s_full
+      for (int s = 0; s < 2 * C::kMaxStages; ++s) mbar_init(bar++, kE4M3 ? 128 : 1);         // k_full, v_full
+      for (int s = 0; s < 2 * C::kMaxStages + 2; ++s) mbar_init(bar++, 1);                   // k_empty, v_empty, s_full
       for (int t = 0; t < 2; ++t) mbar_init(bar++, 128);                                     // p_full
       for (int t = 0; t < 2; ++t) mbar_init(bar++, 1);                                       // pv_done
       for (int t = 0; t < 2; ++t) mbar_init(bar++, 4);                                       // s_free
       mbar_init(bar++, 1);                                                                   // mma_final
-      mbar_init(bar++, 1);                                                                   // raw_full
-      mbar_init(bar++, 128);                                                                 // raw_empty
+      for (int t = 0; t < 2; ++t) mbar_init(bar++, 1);                                       // raw_full
+      for (int t = 0; t < 2; ++t) mbar_init(bar++, 128);                                     // raw_empty
       fence_mbar_init();
     }
   }
@@ -952,14 +983,21 @@ cudaError_t launch_t(const PagedAttnArgs& a, const sage_paged_kv& kv, cudaStream
   const int64_t rows = static_cast<int64_t>(a.b.n_tokens) * p.group;
   const int64_t seqs = std::min<int64_t>(a.b.n_seqs, a.b.n_tokens);
   const int64_t units = (rows + 255 * seqs) / 256 * a.hkv;
-  // Whole units fill the SMs as often as they can; those left over are split along the keys, into as many parts as
-  // shorten the last wave by a tenth or more each (ceil(rest splits / SMs) / splits of a unit's time).
-  const int64_t rest = units % sms;
-  const int64_t most = std::min<int64_t>({kPagedSlots / std::max<int64_t>(rest, 1), sms, std::max(1, a.b.cap / (4 * kBN))});
-  auto last_wave = [&](int64_t k) { return static_cast<double>((rest * k + sms - 1) / sms) / static_cast<double>(k); };
+  // Whole units fill the SMs as often as they can; those left over are split along the keys into the number of
+  // parts that ends them soonest, estimated in microseconds: a unit's key tiles (at most the table's) at 1.6 us for
+  // two row tiles of D = 128, 12 us for a part's start and end, and the parts' O written and read again at 2.5 TB/s
+  // with 4 us for the join.
+  const int64_t rest = units % sms, tiles = std::max(1, (a.b.cap + kBN - 1) / kBN);
+  const int64_t most = std::min<int64_t>({kPagedSlots / std::max<int64_t>(rest, 1), sms, std::max<int64_t>(1, tiles / 4)});
+  auto last_wave = [&](int64_t k) {
+    const double waves = static_cast<double>((rest * k + sms - 1) / sms);
+    const double part_bytes = std::min<double>(static_cast<double>(rows), 256.0) * D * 4;
+    return waves * (1.6 * D / 128 * static_cast<double>((tiles + k - 1) / k) + 12.0) +
+           (k > 1 ? 4.0 + static_cast<double>(rest * k) * part_bytes * 2 / 2.5e6 : 0.0);
+  };
   int64_t splits = 1;
   for (int64_t k = 2; k <= most; ++k)
-    if (last_wave(k) < 0.9 * last_wave(splits)) splits = k;
+    if (last_wave(k) < last_wave(splits)) splits = k;
   p.splits = static_cast<int>(splits);
   p.whole = static_cast<int>(splits > 1 ? units - rest : units);
   const unsigned grid = static_cast<unsigned>(p.whole + (units - p.whole) * splits);
