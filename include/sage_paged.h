@@ -31,7 +31,8 @@ extern "C" {
  * slot * k_stride_token + head * k_stride_head + c, strides in elements; V likewise.
  *   format      0: bf16 values.
  *               1: FP8 E4M3 codes; a code c of head h stands for c * k_scale[h] (V: v_scale[h]).
- *                  k_scale, v_scale: device fp32 [n_heads], positive, fixed while the cache is in use.
+ *                  k_scale, v_scale: device fp32 [n_heads], positive normal numbers below 2^126, fixed while
+ *                  the cache is in use.
  *   page_size   tokens per page, a power of two from 8 to 1024.
  *   head_dim    64 or 128; n_heads 1 to 4096; n_pages 1 to 2^31 - 1.
  * Pages 16-byte aligned, strides positive multiples of 16 bytes below 2^40 bytes (a stride whose
@@ -80,8 +81,8 @@ typedef struct sage_paged_batch {
  *   y = (x / sqrt(mean x^2 + eps)) * gamma   where gamma is given,
  *   z_2i = y_2i cos_i - y_2i+1 sin_i,  z_2i+1 = y_2i sin_i + y_2i+1 cos_i   where the table is given.
  *   K: stored as bf16_rn(z), or as the E4M3 code (round to nearest even, saturating) of
- *      fl32(z / k_scale[h]), z itself not rounded to bf16 first.
- *   V: stored as it is, or as the E4M3 code of fl32(v / v_scale[h]).
+ *      fl32(z * fl32(1 / k_scale[h])), z itself not rounded to bf16 first.
+ *   V: stored as it is, or as the E4M3 code of fl32(v * fl32(1 / v_scale[h])).
  *   Q: bf16_rn(z) to q_out.
  * With gamma, a table and a bf16 cache, the values are those of sage_qk_rmsnorm_rope bit for bit.
  *   q               bf16 [n_tokens, n_heads_q, head_dim] view, or NULL: K and V alone; its head

@@ -436,26 +436,26 @@ def paged_workspace(head_dim: int, device="cuda") -> torch.Tensor:
 
 
 def _paged_view(t: torch.Tensor, d: int, device, what: str) -> SageView:
-    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.device != device:
-        raise ValueError(f"{what}: expected a bf16 [N, H, {d}] tensor on the cache's device")
     shape, stride = t.shape, t.stride()
-    if shape[2] != d or stride[2] != 1:
-        raise ValueError(f"{what}: expected a bf16 [N, H, {d}] tensor with unit channel stride")
+    if len(shape) != 3 or shape[2] != d or stride[2] != 1 or t.dtype is not torch.bfloat16 or t.device != device:
+        raise ValueError(f"{what}: expected a bf16 [N, H, {d}] tensor with unit channel stride on the cache's device")
     return SageView(t.data_ptr(), shape[0], shape[1], d, stride[0], stride[1])
 
 
-def _paged_call(device, stream, call):
-    """`call(raw stream)` with the cache's device current, on `stream` or that device's current stream."""
-    if device.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream))
+def _paged_call(device, stream, fn, args) -> int:
+    """fn(*args, raw stream) with the cache's device current, on `stream` or that device's current stream."""
+    index = device.index
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args, raw)
     with torch.cuda.device(device):
-        return call(torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream))
+        return fn(*args, raw)
 
 
 def _fp32_table(t: Optional[torch.Tensor], shape: tuple, device, what: str):
     if t is None:
         return None
-    if t.dtype is not torch.float32 or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not torch.float32 or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous fp32 tensor of shape {shape} on the cache's device")
     return t.data_ptr()
 
@@ -492,12 +492,13 @@ def sage_paged_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKV, batch: P
     status = cache.status if status is None else status
     if status.device != dev or status.numel() * status.element_size() < 256:
         raise ValueError("status: expected a zeroed block of 256 bytes on the cache's device")
-    args = (_fp32_table(gamma_q, (d,), dev, "gamma_q"), _fp32_table(gamma_k, (d,), dev, "gamma_k"),
-            _fp32_table(rope_cos, (rows, d // 2), dev, "rope_cos"), _fp32_table(rope_sin, (rows, d // 2), dev, "rope_sin"))
-    fn, by = lib().sage_paged_append, ctypes.byref
-    _check(_paged_call(dev, stream, lambda s: fn(
-        None if vq is None else by(vq), by(vk), by(vv), *args, rows, None if positions is None else positions.data_ptr(),
-        eps, cache._ref, batch._ref, *oargs, status.data_ptr(), s)), "sage_paged_append")
+    by = ctypes.byref
+    _check(_paged_call(dev, stream, lib().sage_paged_append, (
+        None if vq is None else by(vq), by(vk), by(vv), _fp32_table(gamma_q, (d,), dev, "gamma_q"),
+        _fp32_table(gamma_k, (d,), dev, "gamma_k"), _fp32_table(rope_cos, (rows, d // 2), dev, "rope_cos"),
+        _fp32_table(rope_sin, (rows, d // 2), dev, "rope_sin"), rows,
+        None if positions is None else positions.data_ptr(), eps, cache._ref, batch._ref, *oargs, status.data_ptr())),
+        "sage_paged_append")
     return q_out
 
 
@@ -524,9 +525,8 @@ def sage_paged_attn(q: torch.Tensor, cache: PagedKV, batch: PagedBatch, sm_scale
     elif ws.device != dev:
         raise ValueError("ws lies on another device than the cache")
     sm_scale = 1.0 / math.sqrt(d) if sm_scale is None else sm_scale
-    fn, by = lib().sage_paged_attn, ctypes.byref
-    _check(_paged_call(dev, stream, lambda s: fn(
-        by(vq), cache._ref, batch._ref, sm_scale, 1 if causal else 0, window or 0, vo.data, vo.stride_token,
-        vo.stride_head, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), s)),
+    _check(_paged_call(dev, stream, lib().sage_paged_attn, (
+        ctypes.byref(vq), cache._ref, batch._ref, sm_scale, 1 if causal else 0, window or 0, vo.data, vo.stride_token,
+        vo.stride_head, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())),
         "sage_paged_attn")
     return out
