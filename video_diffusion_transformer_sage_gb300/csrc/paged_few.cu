@@ -8,12 +8,11 @@
 // 64 MMAs per warp of a team against ~1400 cycles of one SM's share of the bandwidth, and it leaves
 // the accumulators in registers, so the warps need no barrier between key tiles.
 //
-// The key axis.  A unit (sequence, K/V head, row tile) has nt tiles of kKeys keys; all units' tiles,
-// in order, are split evenly over one CTA per SM, so ragged batches and single long sequences
-// load every SM alike.  A CTA walks its tiles through one ring of TMA stages that does not stop
-// at unit borders.  A unit that lies in one CTA is finished there.  Otherwise each CTA leaves
-// (maximum, sum, O) of its part in the workspace and takes a ticket; the last one joins the parts in
-// the order of their keys, so the result does not depend on which CTA came last.
+// The key axis.  A unit (sequence, K/V head, row tile) has nt tiles of kKeys keys; the units' tiles are dealt to one
+// CTA per SM (struct Walk), so ragged batches and single long sequences load every SM alike.  A CTA walks its tiles
+// through one ring of TMA stages that does not stop at unit borders.  A unit that lies in one CTA is finished
+// there.  Otherwise each CTA leaves (maximum, sum, O) of its part in the workspace and takes a ticket; the last
+// one joins the parts in the order of their keys, so the result does not depend on which CTA came last.
 //
 // Inside a CTA: one producer warp (page table entries by lane, one TMA box per page) and two teams of
 // four consumer warps that take the tiles in turn, a quarter of a tile's keys to each warp.  Each warp
@@ -155,66 +154,129 @@ __device__ __forceinline__ void token_keys(const PagedAttnArgs& a, const SeqWork
   lo = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
 }
 
-// Position in the flat list of key tiles, walked alike by every warp of a CTA.
+// A CTA's share of the units' key tiles, walked alike by every warp of it.  One of two ways:
+//  - aligned: where every unit can have CTAs of its own, a unit's tiles are dealt evenly to ceil(nt / q) CTAs, with
+//    the smallest q (at least 4: below that the join costs more than the tiles) that the grid allows;
+//  - even: the flat list of all tiles is cut into equal runs, whatever units they cross.  It balances many units or
+//    very unequal ones, at the price of two partial units per CTA.
 template <int kRows, int kKeys>
 struct Walk {
   SeqWork w;
   int b;
   int u;            // unit within the sequence (at most n_tokens * query heads / 16 + heads < 2^31)
   int k;            // tile within the unit
-  int64_t at, end;  // flat tile index now, end of the CTA's share
+  int64_t at, end;  // even: flat tile index now, end of the CTA's share; aligned: 0, tiles of the share
+  int64_t quota;    // even: tiles per CTA; aligned: 0
+  int part, parts;  // aligned: this CTA's part of its unit
 
-  // Total tiles of the batch and the CTA's start; false if it has none.
-  __device__ __forceinline__ bool init(const FewParams& p, int64_t& quota) {
-    const int lane = threadIdx.x & 31;
-    int64_t total = 0;
-    for (int b0 = 0; b0 < p.a.b.n_seqs; b0 += 32) {
-      if (b0 + lane < p.a.b.n_seqs) {
-        const SeqWork s = seq_work<kRows, kKeys>(p, b0 + lane);
-        total += static_cast<int64_t>(s.qt) * p.a.hkv * s.nt;
-      }
+  // Units and tiles per unit of sequence b; (0, 1) past the last.
+  __device__ __forceinline__ void count(const FewParams& p, int b, int& units, int& nt) {
+    units = 0;
+    nt = 1;
+    if (b < p.a.b.n_seqs) {
+      const SeqWork s = seq_work<kRows, kKeys>(p, b);
+      units = s.qt * p.a.hkv;
+      nt = s.nt;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    quota = (total + gridDim.x - 1) / gridDim.x;
-    at = quota * blockIdx.x;
-    end = min(total, at + quota);
-    if (at >= end) return false;
+  }
+  // The sequence in which the running sum of f(units, nt) passes `target`, and the sum before it.
+  template <typename F>
+  __device__ __forceinline__ bool locate(const FewParams& p, int64_t target, int units, int nt, F f, int64_t& before) {
+    const int lane = threadIdx.x & 31;
     int64_t base = 0;
     for (int b0 = 0; b0 < p.a.b.n_seqs; b0 += 32) {
-      int64_t n = 0;
-      if (b0 + lane < p.a.b.n_seqs) {
-        const SeqWork s = seq_work<kRows, kKeys>(p, b0 + lane);
-        n = static_cast<int64_t>(s.qt) * p.a.hkv * s.nt;
-      }
+      if (p.a.b.n_seqs > 32) count(p, b0 + lane, units, nt);
+      const int64_t n = f(units, nt);
       int64_t incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += up;
       }
-      const uint32_t past = __ballot_sync(0xffffffffu, base + incl > at);
+      const uint32_t past = __ballot_sync(0xffffffffu, base + incl > target);
       if (past) {
         const int l = __ffs(past) - 1;
         b = b0 + l;
-        const int64_t off = at - base - __shfl_sync(0xffffffffu, incl - n, l);
+        before = base + __shfl_sync(0xffffffffu, incl - n, l);
         w = seq_work<kRows, kKeys>(p, b);
-        u = static_cast<int>(off / w.nt);
-        k = static_cast<int>(off - static_cast<int64_t>(u) * w.nt);
         return true;
       }
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
     return false;
   }
+  // Sum of f(units, nt) over the sequences.
+  template <typename F>
+  __device__ __forceinline__ int64_t sum(const FewParams& p, int units, int nt, F f) {
+    const int lane = threadIdx.x & 31;
+    int64_t total = 0;
+    for (int b0 = 0; b0 < p.a.b.n_seqs; b0 += 32) {
+      if (p.a.b.n_seqs > 32) count(p, b0 + lane, units, nt);
+      total += f(units, nt);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    return total;
+  }
+
+  // False if the CTA has no share.
+  __device__ __forceinline__ bool init(const FewParams& p) {
+    const int grid = gridDim.x;
+    int units, nt;   // of this lane's sequence, where there are at most 32
+    count(p, threadIdx.x & 31, units, nt);
+    const int64_t total = sum(p, units, nt, [](int u, int n) { return static_cast<int64_t>(u) * n; });
+    const int64_t all = sum(p, units, nt, [](int u, int) { return static_cast<int64_t>(u); });
+    const uint32_t even = static_cast<uint32_t>(min((total + grid - 1) / grid, static_cast<int64_t>(1 << 30)));
+    int64_t before;
+    part = parts = 0;
+    if (all <= grid) {
+      // At q = the largest nt the parts are the units, which the grid holds: the search ends.
+      uint32_t q = max(even, 4u);
+      const uint32_t most = even + even / 4 + 4;
+      while (q <= most && sum(p, units, nt, [q](int u, int n) { return static_cast<int64_t>(u) * ((n + q - 1) / q); }) > grid)
+        q += max(1u, q / 8);
+      if (q <= most) {
+        if (!locate(p, blockIdx.x, units, nt, [q](int u, int n) { return static_cast<int64_t>(u) * ((n + q - 1) / q); },
+                    before))
+          return false;
+        const int off = static_cast<int>(blockIdx.x - before);
+        parts = (w.nt + q - 1) / q;
+        u = off / parts;
+        part = off - u * parts;
+        k = static_cast<int>(static_cast<int64_t>(w.nt) * part / parts);
+        at = 0;
+        end = static_cast<int>(static_cast<int64_t>(w.nt) * (part + 1) / parts) - k;
+        quota = 0;
+        return true;
+      }
+    }
+    quota = even;
+    at = quota * blockIdx.x;
+    end = min(total, at + quota);
+    if (at >= end || !locate(p, at, units, nt, [](int u, int n) { return static_cast<int64_t>(u) * n; }, before)) return false;
+    const int64_t off = at - before;
+    u = static_cast<int>(off / w.nt);
+    k = static_cast<int>(off - static_cast<int64_t>(u) * w.nt);
+    return true;
+  }
   __device__ __forceinline__ int seg_tiles() const {
-    return static_cast<int>(min(static_cast<int64_t>(w.nt - k), end - at));
+    return quota ? static_cast<int>(min(static_cast<int64_t>(w.nt - k), end - at)) : static_cast<int>(end);
+  }
+  // The CTAs that hold parts of the current unit: n of them from the first.
+  __device__ __forceinline__ void unit_parts(int& first, int& n) const {
+    if (quota == 0) {
+      first = blockIdx.x - part;
+      n = parts;
+      return;
+    }
+    first = static_cast<int>((at - k) / quota);
+    n = static_cast<int>((at - k + w.nt - 1) / quota) - first + 1;
   }
   // Past the segment of n tiles; afterwards valid only while at < end.
   __device__ __forceinline__ void next(const FewParams& p, int n) {
     at += n;
     k += n;
-    if (k < w.nt || at >= end) return;
+    if (at >= end || k < w.nt) return;
     k = 0;
     if (++u < w.qt * p.a.hkv) return;
     u = 0;
@@ -268,11 +330,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   };
 
   Walk<R, KT> wk;
-  int64_t quota;
   if (warp < 4) {
     // ------------------------------------------------------------------ producer
     regs_dec<kFewRegsProducer>();
-    if (warp != 0 || !wk.init(p, quota)) return;
+    if (warp != 0 || !wk.init(p)) return;
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
     const int box = 1 << p.box_shift, boxes = KT >> p.box_shift;   // boxes per stage, at most 32
@@ -355,7 +416,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
   // -------------------------------------------------------------------- consumers
   regs_inc<kFewRegsConsumer>();
-  if (!wk.init(p, quota)) return;
+  if (!wk.init(p)) return;
   const int g = lane >> 2, c = lane & 3;
   const int tid = threadIdx.x - 128, cw = warp - 4;   // among the consumers
   const int team = cw >> 2, kw0 = (cw & 3) * C::kWarpKeys;
@@ -678,9 +739,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
     consumer_sync();
     const bool whole_unit = wk.k == 0 && n == wk.w.nt;
-    const int64_t unit0 = wk.at - wk.k;
-    const int cf = static_cast<int>(unit0 / quota);
-    const int parts = static_cast<int>((unit0 + wk.w.nt - 1) / quota) - cf + 1;
+    int cf = 0, parts = 1;
+    if (!whole_unit) wk.unit_parts(cf, parts);
     const int slot = blockIdx.x * 2 + (wk.k == 0 ? 1 : 0);
     const int live = min(R, wk.w.rows - qi * R);        // rows of the tile that exist
     const float vs = kE4M3 ? __ldg(a.v_scale + h) : 1.0f;
@@ -758,32 +818,46 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     }
     if (!whole_unit) {
       // ---- the unit's parts joined by the CTA that finishes last, in the order of their keys
-      __threadfence();
-      consumer_sync();
+      // (the loop above ended with the CTA's barrier: thread 0's release covers every thread's stores)
       if (tid == 0) {
-        const int before = atomicAdd(a.counters + cf, 1);
+        int before;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(a.counters + cf) : "memory");
         s_last = before == parts - 1;
         if (before == parts - 1) a.counters[cf] = 0;
-        __threadfence();
       }
       consumer_sync();
       if (s_last) {
+        constexpr int kAhead = 4;   // parts whose loads are in flight together
         for (int i = tid; i < live * (D / 4); i += kFewConsumers) {
           const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
           float mm = -INFINITY, ll = 0.0f;
-          for (int q = 0; q < parts; ++q)
-            mm = fmaxf(mm, __ldcg(a.part_ml + ((cf + q) * 2 + (q == 0 ? 1 : 0)) * R + r).x);
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (mm != -INFINITY)
-#pragma unroll 4
-            for (int q = 0; q < parts; ++q) {
-              const int sl = (cf + q) * 2 + (q == 0 ? 1 : 0);
-              const float2 ml = __ldcg(a.part_ml + sl * R + r);
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + (static_cast<int64_t>(sl) * R + r) * D + d4));
-              const float f = ex2_approx(ml.x - mm);
-              ll += ml.y * f;
-              v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
+          for (int q0 = 0; q0 < parts; q0 += kAhead) {
+            float2 ml[kAhead];
+            float4 x[kAhead];
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+              ml[q] = make_float2(-INFINITY, 0.0f);
+              x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (q0 + q < parts) {
+                const int sl = (cf + q0 + q) * 2 + (q0 + q == 0 ? 1 : 0);
+                ml[q] = __ldcg(a.part_ml + sl * R + r);
+                x[q] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (static_cast<int64_t>(sl) * R + r) * D + d4));
+              }
             }
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+              const float mn = fmaxf(mm, ml[q].x);
+              if (mn == -INFINITY) continue;        // no key so far
+              const float f0 = ex2_approx(mm - mn), f1 = ex2_approx(ml[q].x - mn);
+              ll = ll * f0 + ml[q].y * f1;
+              v.x = v.x * f0 + x[q].x * f1;
+              v.y = v.y * f0 + x[q].y * f1;
+              v.z = v.z * f0 + x[q].z * f1;
+              v.w = v.w * f0 + x[q].w * f1;
+              mm = mn;
+            }
+          }
           store4(r, d4, ll > 0.0f ? vs / ll : 0.0f, v.x, v.y, v.z, v.w);
           if (a.lse && d4 == 0) store_lse(r, mm, ll);
         }
