@@ -37,6 +37,9 @@ constexpr int kFewConsumers = 256, kFewThreads = 384;
 constexpr int kFewRegsProducer = 40, kFewRegsConsumer = 232;
 static_assert(128 * kFewRegsProducer + 256 * kFewRegsConsumer <= kFewThreads * 168, "register split exceeds launch");
 constexpr uint64_t kFewWaitNs = 2000000000ull;
+// Parts take two slots per CTA from the front, joined groups one from the back.
+constexpr int kFewMaxCtas = (kPagedSlots - 1) / 3;
+constexpr float kFewRise = 8.0f;   // log2 of how far a maximum may fall behind
 
 template <int D, bool kE4M3, int MT>
 struct FewCfg {
@@ -232,7 +235,7 @@ struct Walk {
     if (all <= grid) {
       // At q = the largest nt the parts are the units, which the grid holds: the search ends.
       uint32_t q = max(even, 4u);
-      const uint32_t most = even + even / 4 + 4;
+      const uint32_t most = even + 4;
       while (q <= most && sum(p, units, nt, [q](int u, int n) { return static_cast<int64_t>(u) * ((n + q - 1) / q); }) > grid)
         q += max(1u, q / 8);
       if (q <= most) {
@@ -463,7 +466,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       consumer_sync();
     }
     // Per-row score factor (log2 units) and visible keys; rows past the last take the last one's.
-    float sc[MT][2], m[MT][2], l[MT][2];
+    float sc[MT][2], m[MT][2];
     int klo[MT][2], khi[MT][2];
     const float scale = kE4M3 ? a.scale_log2 * __ldg(a.k_scale + h) : a.scale_log2;
 #pragma unroll
@@ -474,17 +477,18 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         token_keys(a, wk.w, min(qi * R + r, wk.w.rows - 1) / p.group, klo[mt][e], khi[mt][e]);
         sc[mt][e] = kE4M3 ? scale * q_exp[buf * R + r] : scale;
         m[mt][e] = -INFINITY;
-        l[mt][e] = 0.0f;
       }
     // Visible to all rows: [alo, ahi); to some: [ulo, uhi).
     int alo, ahi, ulo, uhi;
     token_keys(a, wk.w, qi * R / p.group, ulo, ahi);
     token_keys(a, wk.w, (min(qi * R + R, wk.w.rows) - 1) / p.group, alo, uhi);
-    float o[MT][C::kOT][4];
+    float o[MT][C::kOT][4], ol[MT][4];   // ol: the sums of P, every column alike
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
+      ol[mt][0] = ol[mt][1] = ol[mt][2] = ol[mt][3] = 0.0f;
 #pragma unroll
       for (int i = 0; i < C::kOT; ++i) o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.0f;
+    }
     // Q fragments: in registers for one row tile, re-read from shared memory for two.
     uint32_t qf[MT == 1 ? D / 16 : 1][4];
     auto load_q = [&](int mt, int kk, uint32_t f[4]) {
@@ -595,54 +599,51 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             seen_bits |= (in ? 1u : 0u) << (t * 2 + j);
           }
       }
+      // The maximum moves only when it rises by more than 2^8 (P stays below 2^8, the ratio is the same), so O is
+      // rarely rescaled.
       bool rise = false;
       float al[MT][2];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mx = -INFINITY;
+          if (!whole) {
 #pragma unroll
-          for (int t = 0; t < C::kNT; ++t)
+            for (int t = 0; t < C::kNT; ++t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float v = x[mt][t][e * 2 + j] * sc[mt][e];
-              if (!whole) {
+              for (int j = 0; j < 2; ++j) {
                 const int key = kb + key_of(t, j);
-                if (!((seen_bits >> (t * 2 + j)) & 1u) || key < klo[mt][e] || key >= khi[mt][e]) v = -INFINITY;
+                if (!((seen_bits >> (t * 2 + j)) & 1u) || key < klo[mt][e] || key >= khi[mt][e])
+                  x[mt][t][e * 2 + j] = -INFINITY;
               }
-              x[mt][t][e * 2 + j] = v;
-              mx = fmaxf(mx, v);
-            }
+          }
+          float mx = fmaxf(x[mt][0][e * 2], x[mt][0][e * 2 + 1]);
+#pragma unroll
+          for (int t = 1; t < C::kNT; ++t) mx = fmax3(mx, x[mt][t][e * 2], x[mt][t][e * 2 + 1]);
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m[mt][e], mx);
-          const float mu = mn == -INFINITY ? 0.0f : mn;   // no key so far: every p below is 0
-          al[mt][e] = ex2_approx(m[mt][e] - mu);
-          rise |= mn > m[mt][e];
-          m[mt][e] = mn;
-          float sum = 0.0f;
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * sc[mt][e];
+          const bool up = mx > m[mt][e] + kFewRise;          // also the first visible key
+          al[mt][e] = up ? ex2_approx(m[mt][e] - mx) : 1.0f;
+          rise |= up;
+          if (up) m[mt][e] = mx;
+          const float base = m[mt][e] == -INFINITY ? 0.0f : m[mt][e];   // no key so far: every p below is 0
 #pragma unroll
           for (int t = 0; t < C::kNT; ++t) {
-            // p rounded to the 16 bits that multiply V; the sum takes the rounded values, so the
-            // weights add up to 1.
-            const float p0 = ex2_approx(x[mt][t][e * 2] - mu), p1 = ex2_approx(x[mt][t][e * 2 + 1] - mu);
-            uint32_t pk;
-            if (kE4M3) {
-              const __half2 hh = __floats2half2_rn(p0, p1);
-              pk = *reinterpret_cast<const uint32_t*>(&hh);
-              sum += __low2float(hh) + __high2float(hh);
-            } else {
+            const float p0 = ex2_approx(fmaf(x[mt][t][e * 2], sc[mt][e], -base));
+            const float p1 = ex2_approx(fmaf(x[mt][t][e * 2 + 1], sc[mt][e], -base));
+            uint32_t pk;   // P in the 16 bits that multiply V
+            if (kE4M3)
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk) : "f"(p1), "f"(p0));
+            else
               asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk) : "f"(p1), "f"(p0));
-              sum += __uint_as_float(pk << 16) + __uint_as_float(pk & 0xFFFF0000u);
-            }
             x[mt][t][e * 2] = __uint_as_float(pk);
           }
-          l[mt][e] = l[mt][e] * al[mt][e] + sum;
         }
       if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < MT; ++mt) {
+          ol[mt][0] *= al[mt][0];
+          ol[mt][2] *= al[mt][1];
 #pragma unroll
           for (int ot = 0; ot < C::kOT; ++ot) {
             o[mt][ot][0] *= al[mt][0];
@@ -650,6 +651,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             o[mt][ot][2] *= al[mt][1];
             o[mt][ot][3] *= al[mt][1];
           }
+        }
       }
       // ---- O += P V, 16 keys at a time
 #pragma unroll
@@ -662,6 +664,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           pf[mt][2] = __float_as_uint(x[mt][2 * t2 + 1][0]);
           pf[mt][3] = __float_as_uint(x[mt][2 * t2 + 1][2]);
         }
+        // The sums: P times ones, so of the rounded P, and the weights add up to 1.
+        constexpr uint32_t kOnes = kE4M3 ? 0x3C003C00u : 0x3F803F80u;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) mma16816<kE4M3>(ol[mt], pf[mt], kOnes, kOnes);
         // Keys that no row sees may hold anything: their V counts as 0.
         const uint32_t vis = seen_bits >> (t2 * 4);
         if (!kE4M3) {
@@ -729,12 +735,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float s = l[mt][e];
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
         if (c == 0) {
           sm_m[cw * R + mt * 16 + e * 8 + g] = m[mt][e];
-          sm_l[cw * R + mt * 16 + e * 8 + g] = s;
+          sm_l[cw * R + mt * 16 + e * 8 + g] = ol[mt][2 * e];
         }
       }
     consumer_sync();
@@ -817,30 +820,36 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
     }
     if (!whole_unit) {
-      // ---- the unit's parts joined by the CTA that finishes last, in the order of their keys
-      // (the loop above ended with the CTA's barrier: thread 0's release covers every thread's stores)
-      if (tid == 0) {
-        int before;
-        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(a.counters + cf) : "memory");
-        s_last = before == parts - 1;
-        if (before == parts - 1) a.counters[cf] = 0;
-      }
-      consumer_sync();
-      if (s_last) {
+      // ---- the unit's parts joined by the CTA that finishes last, in the order of their keys.  More than 16 parts
+      // (one sequence with few K/V heads over all SMs) are joined in groups first, each by its last CTA, then the groups.
+      // The loop above ended with the CTA's barrier: thread 0's release covers every thread's stores.
+      auto last_of = [&](int32_t* counter, int n_parts) {
+        if (tid == 0) {
+          int before;
+          asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+          s_last = before == n_parts - 1;
+          if (s_last) *counter = 0;
+        }
+        consumer_sync();
+        return s_last != 0;
+      };
+      // Parts slot_of(0) .. slot_of(count - 1) into `to`, or the output where `to` is negative.
+      auto join = [&](int count, auto slot_of, int to) {
         constexpr int kAhead = 4;   // parts whose loads are in flight together
         for (int i = tid; i < live * (D / 4); i += kFewConsumers) {
           const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
           float mm = -INFINITY, ll = 0.0f;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int q0 = 0; q0 < parts; q0 += kAhead) {
+#pragma unroll 1
+          for (int q0 = 0; q0 < count; q0 += kAhead) {
             float2 ml[kAhead];
             float4 x[kAhead];
 #pragma unroll
             for (int q = 0; q < kAhead; ++q) {
               ml[q] = make_float2(-INFINITY, 0.0f);
               x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (q0 + q < parts) {
-                const int sl = (cf + q0 + q) * 2 + (q0 + q == 0 ? 1 : 0);
+              if (q0 + q < count) {
+                const int sl = slot_of(q0 + q);
                 ml[q] = __ldcg(a.part_ml + sl * R + r);
                 x[q] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (static_cast<int64_t>(sl) * R + r) * D + d4));
               }
@@ -858,8 +867,28 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               mm = mn;
             }
           }
-          store4(r, d4, ll > 0.0f ? vs / ll : 0.0f, v.x, v.y, v.z, v.w);
-          if (a.lse && d4 == 0) store_lse(r, mm, ll);
+          if (to >= 0) {
+            *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(to) * R + r) * D + d4) = v;
+            if (d4 == 0) a.part_ml[to * R + r] = make_float2(mm, ll);
+          } else {
+            store4(r, d4, ll > 0.0f ? vs / ll : 0.0f, v.x, v.y, v.z, v.w);
+            if (a.lse && d4 == 0) store_lse(r, mm, ll);
+          }
+        }
+      };
+      auto part_slot = [&](int q) { return (cf + q) * 2 + (q == 0 ? 1 : 0); };
+      if (parts <= 16) {
+        if (last_of(a.counters + cf, parts)) join(parts, part_slot, -1);
+      } else {
+        int per = 5;
+        while (per * per < parts) ++per;
+        const int group = (static_cast<int>(blockIdx.x) - cf) / per, first = group * per, groups = (parts + per - 1) / per;
+        const int size = min(per, parts - first);
+        if (last_of(a.counters + cf + first, size)) {
+          join(size, [&](int q) { return part_slot(first + q); }, kPagedSlots - 1 - cf - first);
+          consumer_sync();
+          if (last_of(a.counters + kPagedMaxCtas + cf, groups))
+            join(groups, [&](int q) { return kPagedSlots - 1 - cf - q * per; }, -1);
         }
       }
     }
@@ -888,7 +917,7 @@ cudaError_t launch_t(const PagedAttnArgs& a, const sage_paged_kv& kv, cudaStream
   if (err == cudaSuccess)
     err = cudaFuncSetAttribute(paged_few_kernel<D, kE4M3, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (err != cudaSuccess) return err;
-  paged_few_kernel<D, kE4M3, MT><<<std::min(sms, kPagedMaxCtas), kFewThreads, C::kSmem, s>>>(kmap, vmap, p);
+  paged_few_kernel<D, kE4M3, MT><<<std::min(sms, kFewMaxCtas), kFewThreads, C::kSmem, s>>>(kmap, vmap, p);
   return cudaGetLastError();
 }
 
