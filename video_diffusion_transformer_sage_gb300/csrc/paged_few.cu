@@ -120,6 +120,20 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, uint6
       "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
+// Draws a ticket with acquire and release at the GPU's scope; true for the last of n, which resets the counter.
+__device__ __forceinline__ int draw_ticket(int32_t* counter, int n) {
+  int before;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+  if (before != n - 1) return 0;
+  *counter = 0;
+  return 1;
+}
+// Parts of a group when more than 16 are joined: about the square root.
+__device__ __forceinline__ int group_size(int parts) {
+  int per = 5;
+  while (per * per < parts) ++per;
+  return per;
+}
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 struct FewParams {
@@ -166,14 +180,14 @@ template <int kRows, int kKeys>
 struct Walk {
   SeqWork w;
   int b;
-  int u;            // unit within the sequence (at most n_tokens * query heads / 16 + heads < 2^31)
-  int k;            // tile within the unit
-  int64_t at, end;  // even: flat tile index now, end of the CTA's share; aligned: 0, tiles of the share
-  int64_t quota;    // even: tiles per CTA; aligned: 0
-  int part, parts;  // aligned: this CTA's part of its unit
+  int u;                // unit within the sequence
+  int k;                // tile within the unit
+  uint32_t at, end;     // even: flat tile index now, end of the CTA's share; aligned: 0, tiles of the share
+  uint32_t quota;       // even: tiles per CTA; aligned: 0
+  int part, parts;      // aligned: this CTA's part of its unit
 
   // Units and tiles per unit of sequence b; (0, 1) past the last.
-  __device__ __forceinline__ void count(const FewParams& p, int b, int& units, int& nt) {
+  __device__ __forceinline__ void count(const FewParams& p, int b, uint32_t& units, uint32_t& nt) {
     units = 0;
     nt = 1;
     if (b < p.a.b.n_seqs) {
@@ -182,18 +196,29 @@ struct Walk {
       nt = s.nt;
     }
   }
-  // The sequence in which the running sum of f(units, nt) passes `target`, and the sum before it.
+  // Sum of f(units, nt) over the sequences; units, nt: this lane's sequence, where there are at most 32.
   template <typename F>
-  __device__ __forceinline__ bool locate(const FewParams& p, int64_t target, int units, int nt, F f, int64_t& before) {
+  __device__ __forceinline__ uint32_t sum(const FewParams& p, uint32_t units, uint32_t nt, F f) {
+    uint32_t total = 0;
+    for (int b0 = 0; b0 < p.a.b.n_seqs; b0 += 32) {
+      if (p.a.b.n_seqs > 32) count(p, b0 + (threadIdx.x & 31), units, nt);
+      total += f(units, nt);
+    }
+    return __reduce_add_sync(0xffffffffu, total);
+  }
+  // Sets b and w to the sequence in which the running sum of f passes `target`; `before`: the sum before it.
+  template <typename F>
+  __device__ __forceinline__ bool locate(const FewParams& p, uint32_t target, uint32_t units, uint32_t nt, F f,
+                                         uint32_t& before) {
     const int lane = threadIdx.x & 31;
-    int64_t base = 0;
+    uint32_t base = 0;
     for (int b0 = 0; b0 < p.a.b.n_seqs; b0 += 32) {
       if (p.a.b.n_seqs > 32) count(p, b0 + lane, units, nt);
-      const int64_t n = f(units, nt);
-      int64_t incl = n;
+      const uint32_t n = f(units, nt);
+      uint32_t incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+        const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += up;
       }
       const uint32_t past = __ballot_sync(0xffffffffu, base + incl > target);
@@ -208,47 +233,46 @@ struct Walk {
     }
     return false;
   }
-  // Sum of f(units, nt) over the sequences.
-  template <typename F>
-  __device__ __forceinline__ int64_t sum(const FewParams& p, int units, int nt, F f) {
-    const int lane = threadIdx.x & 31;
-    int64_t total = 0;
-    for (int b0 = 0; b0 < p.a.b.n_seqs; b0 += 32) {
-      if (p.a.b.n_seqs > 32) count(p, b0 + lane, units, nt);
-      total += f(units, nt);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    return total;
-  }
 
   // False if the CTA has no share.
   __device__ __forceinline__ bool init(const FewParams& p) {
-    const int grid = gridDim.x;
-    int units, nt;   // of this lane's sequence, where there are at most 32
+    const uint32_t grid = gridDim.x;
+    uint32_t units, nt, before;
     count(p, threadIdx.x & 31, units, nt);
-    const int64_t total = sum(p, units, nt, [](int u, int n) { return static_cast<int64_t>(u) * n; });
-    const int64_t all = sum(p, units, nt, [](int u, int) { return static_cast<int64_t>(u); });
-    const uint32_t even = static_cast<uint32_t>(min((total + grid - 1) / grid, static_cast<int64_t>(1 << 30)));
-    int64_t before;
+    // Tiles and units are counted in 32 bits: a batch of 2^31 tiles (each a 32 KB read) is refused.
+    uint64_t mine = 0;
+    for (int b0 = 0; b0 < p.a.b.n_seqs; b0 += 32) {
+      uint32_t x = units, y = nt;
+      if (p.a.b.n_seqs > 32) count(p, b0 + (threadIdx.x & 31), x, y);
+      mine += static_cast<uint64_t>(x) * y;
+    }
+    if (__any_sync(0xffffffffu, mine >= (1ull << 26))) {
+      uint64_t all = mine;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      if (all >= (1ull << 31)) {
+        record_bad_index(p.a.status, kWhereLength);
+        return false;
+      }
+    }
+    const uint32_t total = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(mine));
+    const uint32_t even = (total + grid - 1) / grid;
     part = parts = 0;
-    if (all <= grid) {
-      // At q = the largest nt the parts are the units, which the grid holds: the search ends.
+    if (sum(p, units, nt, [](uint32_t u, uint32_t) { return u; }) <= grid) {
+      // At q = the largest nt the parts are the units, which the grid holds.
       uint32_t q = max(even, 4u);
       const uint32_t most = even + 4;
-      while (q <= most && sum(p, units, nt, [q](int u, int n) { return static_cast<int64_t>(u) * ((n + q - 1) / q); }) > grid)
-        q += max(1u, q / 8);
+      while (q <= most && sum(p, units, nt, [q](uint32_t u, uint32_t n) { return u * ((n + q - 1) / q); }) > grid) ++q;
       if (q <= most) {
-        if (!locate(p, blockIdx.x, units, nt, [q](int u, int n) { return static_cast<int64_t>(u) * ((n + q - 1) / q); },
-                    before))
-          return false;
+        if (!locate(p, blockIdx.x, units, nt, [q](uint32_t u, uint32_t n) { return u * ((n + q - 1) / q); }, before)) return false;
         const int off = static_cast<int>(blockIdx.x - before);
-        parts = (w.nt + q - 1) / q;
+        parts = static_cast<int>((w.nt + q - 1) / q);
         u = off / parts;
         part = off - u * parts;
-        k = static_cast<int>(static_cast<int64_t>(w.nt) * part / parts);
+        // parts <= 152 and nt < 2^24: the products stay below 2^32
+        k = static_cast<int>(static_cast<uint32_t>(w.nt) * part / parts);
         at = 0;
-        end = static_cast<int>(static_cast<int64_t>(w.nt) * (part + 1) / parts) - k;
+        end = static_cast<uint32_t>(w.nt) * (part + 1) / parts - k;
         quota = 0;
         return true;
       }
@@ -256,14 +280,14 @@ struct Walk {
     quota = even;
     at = quota * blockIdx.x;
     end = min(total, at + quota);
-    if (at >= end || !locate(p, at, units, nt, [](int u, int n) { return static_cast<int64_t>(u) * n; }, before)) return false;
-    const int64_t off = at - before;
+    if (at >= end || !locate(p, at, units, nt, [](uint32_t u, uint32_t n) { return u * n; }, before)) return false;
+    const uint32_t off = at - before;
     u = static_cast<int>(off / w.nt);
-    k = static_cast<int>(off - static_cast<int64_t>(u) * w.nt);
+    k = static_cast<int>(off - u * w.nt);
     return true;
   }
   __device__ __forceinline__ int seg_tiles() const {
-    return quota ? static_cast<int>(min(static_cast<int64_t>(w.nt - k), end - at)) : static_cast<int>(end);
+    return quota ? static_cast<int>(min(static_cast<uint32_t>(w.nt - k), end - at)) : static_cast<int>(end);
   }
   // The CTAs that hold parts of the current unit: n of them from the first.
   __device__ __forceinline__ void unit_parts(int& first, int& n) const {
@@ -293,6 +317,12 @@ struct Walk {
   }
 };
 
+// A part left in the workspace, its ticket drawn: joined at the CTA's end if it was its unit's last.
+struct Pending {
+  int counter, count;                   // the ticket's counter and value that makes it the last
+  int cf, parts, start, rows, h, qi;
+};
+
 template <int D, bool kE4M3, int MT>
 __global__ void __launch_bounds__(kFewThreads, 1)
     paged_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -301,7 +331,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   constexpr int R = C::kRows, KT = C::kKeys;
   extern __shared__ uint8_t smem_raw[];
   __shared__ volatile int s_abort;
-  __shared__ int s_last, s_skip;
+  __shared__ int s_last[2], s_skip;
+  __shared__ Pending s_pending[2];   // of the CTA's first and last segment
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* empty = full + C::kStages;
@@ -311,9 +342,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PagedAttnArgs& a = p.a;
 
+  grid_dep_wait();     // launched as a dependent: nothing is read before the kernel ahead is done
+  grid_dep_launch();
   if (threadIdx.x == 0) {
     s_skip = *reinterpret_cast<volatile int32_t*>(a.status) == kStatusTimeout;
     s_abort = 0;
+    s_last[0] = s_last[1] = 0;
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(full + s, 1);
       mbar_init(empty + s, 4);
@@ -373,11 +407,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       token_keys(a, wk.w, (qi * R) / p.group, ulo, unused);
       token_keys(a, wk.w, (min(qi * R + R, wk.w.rows) - 1) / p.group, unused, uhi);
       if (lane == 0 && __ldg(a.b.kv_len + wk.b) > a.b.cap) record_bad_index(a.status, kWhereLength);
+      const int32_t* row = a.b.table + wk.b * a.b.table_stride;
+      const int first0 = (wk.w.t_lo + wk.k) * KT + (lane << p.box_shift);
+      auto needed = [&](int i) { return i < n && lane < boxes && first0 + i * KT < uhi && first0 + i * KT + box > ulo; };
+      int next = needed(0) ? __ldg(row + (first0 >> a.b.page_shift)) : -1;
       for (int i = 0; i < n; ++i, ++it) {
-        const int key0 = (wk.w.t_lo + wk.k + i) * KT + (lane << p.box_shift);
-        const bool need = lane < boxes && key0 < uhi && key0 + box > ulo;
-        int page = -1;
-        if (need) page = __ldg(a.b.table + wk.b * a.b.table_stride + (key0 >> a.b.page_shift));
+        // The next tile's table entries are on their way while this one waits for its stage.
+        const int key0 = first0 + i * KT, page = next;
+        const bool need = needed(i);
+        next = needed(i + 1) ? __ldg(row + ((key0 + KT) >> a.b.page_shift)) : -1;
         const bool good = need && page >= 0 && page < a.b.n_pages;
         if (need && !good) record_bad_index(a.status, kWherePage);
         const uint32_t bits = __ballot_sync(0xffffffffu, good);
@@ -427,6 +465,18 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   float* sm_m = reinterpret_cast<float*>(smem + C::kMlOff);   // [8][R]
   float* sm_l = sm_m + 8 * R;
   float* q_exp = reinterpret_cast<float*>(smem + C::kScaleOff);
+  // Row r of the unit (its sequence's first q row, K/V head, row tile): four channels of the output, its lse.
+  auto store4 = [&](int start, int h, int qi, int r, int d, float inv, float v0, float v1, float v2, float v3) {
+    const int rr = qi * R + r, tok = rr / p.group, hq = h * p.group + rr % p.group;
+    uint2 w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(v1 * inv), "f"(v0 * inv));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(v3 * inv), "f"(v2 * inv));
+    *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(start + tok) * a.ost + static_cast<int64_t>(hq) * a.osh + d) = w;
+  };
+  auto store_lse = [&](int start, int h, int qi, int r, float mm, float ll) {
+    const int rr = qi * R + r, tok = rr / p.group, hq = h * p.group + rr % p.group;
+    a.lse[static_cast<int64_t>(start + tok) * a.hq + hq] = ll > 0.0f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+  };
   int it = 0;
   for (int seg = 0; wk.at < wk.end; ++seg) {
     const int n = wk.seg_tiles();
@@ -747,19 +797,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const int slot = blockIdx.x * 2 + (wk.k == 0 ? 1 : 0);
     const int live = min(R, wk.w.rows - qi * R);        // rows of the tile that exist
     const float vs = kE4M3 ? __ldg(a.v_scale + h) : 1.0f;
-    auto store4 = [&](int r, int d, float inv, float v0, float v1, float v2, float v3) {
-      const int rr = qi * R + r, tok = rr / p.group, hq = h * p.group + rr % p.group;
-      uint16_t* dst = a.out + static_cast<int64_t>(wk.w.start + tok) * a.ost + static_cast<int64_t>(hq) * a.osh + d;
-      uint2 w;
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(v1 * inv), "f"(v0 * inv));
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(v3 * inv), "f"(v2 * inv));
-      *reinterpret_cast<uint2*>(dst) = w;
-    };
-    auto store_lse = [&](int r, float mm, float ll) {
-      const int rr = qi * R + r, tok = rr / p.group, hq = h * p.group + rr % p.group;
-      a.lse[static_cast<int64_t>(wk.w.start + tok) * a.hq + hq] =
-          ll > 0.0f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
-    };
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       float fac[2];
@@ -809,8 +846,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             if (mm != -INFINITY) ll += sm_l[w * R + r] * ex2_approx(sm_m[w * R + r] - mm);
           }
           if (whole_unit) {
-            store4(r, half * 64 + d4, ll > 0.0f ? vs / ll : 0.0f, v.x, v.y, v.z, v.w);
-            if (a.lse && half == 0 && d4 == 0) store_lse(r, mm, ll);
+            store4(wk.w.start, h, qi, r, half * 64 + d4, ll > 0.0f ? vs / ll : 0.0f, v.x, v.y, v.z, v.w);
+            if (a.lse && half == 0 && d4 == 0) store_lse(wk.w.start, h, qi, r, mm, ll);
           } else {
             *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(slot) * R + r) * D + half * 64 + d4) = v;
             if (half == 0 && d4 == 0) a.part_ml[slot * R + r] = make_float2(mm, ll);
@@ -820,79 +857,90 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
     }
     if (!whole_unit) {
-      // ---- the unit's parts joined by the CTA that finishes last, in the order of their keys.  More than 16 parts
-      // (one sequence with few K/V heads over all SMs) are joined in groups first, each by its last CTA, then the groups.
-      // The loop above ended with the CTA's barrier: thread 0's release covers every thread's stores.
-      auto last_of = [&](int32_t* counter, int n_parts) {
-        if (tid == 0) {
-          int before;
-          asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
-          s_last = before == n_parts - 1;
-          if (s_last) *counter = 0;
-        }
-        consumer_sync();
-        return s_last != 0;
-      };
-      // Parts slot_of(0) .. slot_of(count - 1) into `to`, or the output where `to` is negative.
-      auto join = [&](int count, auto slot_of, int to) {
-        constexpr int kAhead = 4;   // parts whose loads are in flight together
-        for (int i = tid; i < live * (D / 4); i += kFewConsumers) {
-          const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
-          float mm = -INFINITY, ll = 0.0f;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-          for (int q0 = 0; q0 < count; q0 += kAhead) {
-            float2 ml[kAhead];
-            float4 x[kAhead];
-#pragma unroll
-            for (int q = 0; q < kAhead; ++q) {
-              ml[q] = make_float2(-INFINITY, 0.0f);
-              x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (q0 + q < count) {
-                const int sl = slot_of(q0 + q);
-                ml[q] = __ldcg(a.part_ml + sl * R + r);
-                x[q] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (static_cast<int64_t>(sl) * R + r) * D + d4));
-              }
-            }
-#pragma unroll
-            for (int q = 0; q < kAhead; ++q) {
-              const float mn = fmaxf(mm, ml[q].x);
-              if (mn == -INFINITY) continue;        // no key so far
-              const float f0 = ex2_approx(mm - mn), f1 = ex2_approx(ml[q].x - mn);
-              ll = ll * f0 + ml[q].y * f1;
-              v.x = v.x * f0 + x[q].x * f1;
-              v.y = v.y * f0 + x[q].y * f1;
-              v.z = v.z * f0 + x[q].z * f1;
-              v.w = v.w * f0 + x[q].w * f1;
-              mm = mn;
-            }
-          }
-          if (to >= 0) {
-            *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(to) * R + r) * D + d4) = v;
-            if (d4 == 0) a.part_ml[to * R + r] = make_float2(mm, ll);
-          } else {
-            store4(r, d4, ll > 0.0f ? vs / ll : 0.0f, v.x, v.y, v.z, v.w);
-            if (a.lse && d4 == 0) store_lse(r, mm, ll);
-          }
-        }
-      };
-      auto part_slot = [&](int q) { return (cf + q) * 2 + (q == 0 ? 1 : 0); };
-      if (parts <= 16) {
-        if (last_of(a.counters + cf, parts)) join(parts, part_slot, -1);
-      } else {
-        int per = 5;
-        while (per * per < parts) ++per;
-        const int group = (static_cast<int>(blockIdx.x) - cf) / per, first = group * per, groups = (parts + per - 1) / per;
-        const int size = min(per, parts - first);
-        if (last_of(a.counters + cf + first, size)) {
-          join(size, [&](int q) { return part_slot(first + q); }, kPagedSlots - 1 - cf - first);
-          consumer_sync();
-          if (last_of(a.counters + kPagedMaxCtas + cf, groups))
-            join(groups, [&](int q) { return kPagedSlots - 1 - cf - q * per; }, -1);
-        }
+      // The loop above ended with the CTA's barrier: thread 0's release covers every thread's stores.  Whether the part
+      // was the last is looked at when the CTA's tiles are done, so its next unit does not wait for the ticket.
+      if (tid == 0) {
+        // More than 16 parts (one sequence with few K/V heads over all SMs) are joined in groups first.
+        const int per = parts <= 16 ? parts : group_size(parts);
+        const int first = (static_cast<int>(blockIdx.x) - cf) / per * per;
+        Pending& d = s_pending[wk.k == 0 ? 1 : 0];
+        d.counter = cf + first;
+        d.count = min(per, parts - first);
+        d.cf = cf;
+        d.parts = parts;
+        d.start = wk.w.start;
+        d.rows = wk.w.rows;
+        d.h = h;
+        d.qi = qi;
+        s_last[wk.k == 0 ? 1 : 0] = draw_ticket(a.counters + d.counter, d.count);
       }
     }
     wk.next(p, n);
+  }
+
+  // ---- units whose last part was this CTA's: the parts joined in the order of their keys
+#pragma unroll 1
+  for (int d = 0; d < 2; ++d) {
+    consumer_sync();
+    if (!s_last[d]) continue;
+    const Pending& e = s_pending[d];
+    const int cf = e.cf, parts = e.parts, live = min(R, e.rows - e.qi * R);
+    const float vs = kE4M3 ? __ldg(a.v_scale + e.h) : 1.0f;
+    // Parts slot_of(0) .. slot_of(count - 1) into `to`, or the output where `to` is negative.
+    auto join = [&](int count, auto slot_of, int to) {
+      constexpr int kAhead = 4;   // parts whose loads are in flight together
+      for (int i = tid; i < live * (D / 4); i += kFewConsumers) {
+        const int r = i / (D / 4), d4 = (i % (D / 4)) * 4;
+        float mm = -INFINITY, ll = 0.0f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int q0 = 0; q0 < count; q0 += kAhead) {
+          float2 ml[kAhead];
+          float4 x[kAhead];
+#pragma unroll
+          for (int q = 0; q < kAhead; ++q) {
+            ml[q] = make_float2(-INFINITY, 0.0f);
+            x[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (q0 + q < count) {
+              const int sl = slot_of(q0 + q);
+              ml[q] = __ldcg(a.part_ml + sl * R + r);
+              x[q] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (static_cast<int64_t>(sl) * R + r) * D + d4));
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < kAhead; ++q) {
+            const float mn = fmaxf(mm, ml[q].x);
+            if (mn == -INFINITY) continue;        // no key so far
+            const float f0 = ex2_approx(mm - mn), f1 = ex2_approx(ml[q].x - mn);
+            ll = ll * f0 + ml[q].y * f1;
+            v.x = v.x * f0 + x[q].x * f1;
+            v.y = v.y * f0 + x[q].y * f1;
+            v.z = v.z * f0 + x[q].z * f1;
+            v.w = v.w * f0 + x[q].w * f1;
+            mm = mn;
+          }
+        }
+        if (to >= 0) {
+          *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(to) * R + r) * D + d4) = v;
+          if (d4 == 0) a.part_ml[to * R + r] = make_float2(mm, ll);
+        } else {
+          store4(e.start, e.h, e.qi, r, d4, ll > 0.0f ? vs / ll : 0.0f, v.x, v.y, v.z, v.w);
+          if (a.lse && d4 == 0) store_lse(e.start, e.h, e.qi, r, mm, ll);
+        }
+      }
+    };
+    auto part_slot = [&](int q) { return (cf + q) * 2 + (q == 0 ? 1 : 0); };
+    if (parts <= 16) {
+      join(parts, part_slot, -1);
+    } else {
+      // The group's parts into a slot of the group's; then, if that was the last group, the groups.
+      const int per = group_size(parts), first = e.counter - cf, groups = (parts + per - 1) / per;
+      join(e.count, [&](int q) { return part_slot(first + q); }, kPagedSlots - 1 - e.counter);
+      consumer_sync();
+      if (tid == 0) s_last[d] = draw_ticket(a.counters + kPagedMaxCtas + cf, groups);
+      consumer_sync();
+      if (s_last[d]) join(groups, [&](int q) { return kPagedSlots - 1 - cf - q * per; }, -1);
+    }
   }
 }
 
@@ -917,8 +965,8 @@ cudaError_t launch_t(const PagedAttnArgs& a, const sage_paged_kv& kv, cudaStream
   if (err == cudaSuccess)
     err = cudaFuncSetAttribute(paged_few_kernel<D, kE4M3, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (err != cudaSuccess) return err;
-  paged_few_kernel<D, kE4M3, MT><<<std::min(sms, kFewMaxCtas), kFewThreads, C::kSmem, s>>>(kmap, vmap, p);
-  return cudaGetLastError();
+  return launch_dependent(true, paged_few_kernel<D, kE4M3, MT>, dim3(std::min(sms, kFewMaxCtas)), dim3(kFewThreads), C::kSmem,
+                          s, kmap, vmap, p);
 }
 
 template <int D, bool kE4M3>
