@@ -19,7 +19,7 @@
 // E4M3 cache: the codes come by TMA into a staging tile and one warpgroup widens them to fp16 (exact) in
 // the swizzled tiles; Q is held as fp16 times a power of two per row and P as fp16.
 //
-// Warp roles: warp 0 page table and TMA, warp 1 MMA issue (one thread), warp 2 tensor memory; warps 4-7 and
+// Warp roles: warp 0 (and 3) page table and TMA, warp 1 MMA issue (one thread), warp 2 tensor memory; warps 4-7 and
 // 8-11 softmax and epilogue of tile 0 and 1; with E4M3 warps 12-15 widen.  Every wait is bounded.
 //
 // What bounds it: 4 rows keys D FLOPs at the 16-bit tensor rate (for few rows the cache's bytes).  The key axis
@@ -360,6 +360,8 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
                                             ChunkShared& sh, uint8_t* smem) {
   using C = ChunkCfg<D, kE4M3>;
   constexpr int kStages = kOne ? C::kStages1 : C::kStages;
+  // K and V with barriers of their own have a loading warp each: pages of 16 tokens are 32 copies a tile.
+  constexpr bool kTwoLoaders = C::kSplitKV || kE4M3;
   const PagedAttnArgs& a = p.a;
   const Unit& u = sh.unit;
   uint8_t* sQ = smem;
@@ -382,11 +384,12 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
 
   if (warp < 4) {
     regs_dec<C::kRegsRoles>();
-    if (warp == 0) {
+    if (warp == 0 || (kTwoLoaders && warp == 3)) {
       // ------------------------------------------------------------ page table and TMA
+      const int kv0 = warp == 0 ? 0 : 1, kv1 = kTwoLoaders && warp == 0 ? 1 : 2;   // K, V or both
       tma_prefetch_desc(&kmap);
       tma_prefetch_desc(&vmap);
-      if (lane == 0 && __ldg(a.b.kv_len + u.b) > a.b.cap) record_bad_index(a.status, kWhereLength);
+      if (warp == 0 && lane == 0 && __ldg(a.b.kv_len + u.b) > a.b.cap) record_bad_index(a.status, kWhereLength);
       const int box = 1 << p.box_shift;
       const uint32_t box_bytes = static_cast<uint32_t>(box) * D * (kE4M3 ? 1 : 2);
       const int32_t* row = a.b.table + u.b * a.b.table_stride;
@@ -403,7 +406,7 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
         const uint32_t bits = __ballot_sync(0xffffffffu, good);
         const int slot_in_page = key0 & ((1 << a.b.page_shift) - 1);
         const int s = j % kStages;
-        for (kv = 0; kv < 2; ++kv) {
+        for (kv = kv0; kv < kv1; ++kv) {
           const CUtensorMap* map = kv ? &vmap : &kmap;
           const bool own_bar = C::kSplitKV || kv == 0;   // V shares K's barriers otherwise
           uint64_t* full = kE4M3 ? raw_full + kv : (kv && own_bar ? v_full : k_full) + s;
@@ -437,14 +440,15 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
         if (!ok) break;
       }
       if (!ok) {
-        // After a timeout: the copies issued (K tiles up to nk, V tiles up to j) have landed before the CTA ends.
-        const int nk = j + (kv > 0 ? 1 : 0);   // (without split barriers kv is 0 here)
+        // After a timeout: the copies issued have landed before the CTA ends (tiles up to j, and K of tile j where this
+        // warp loads both and gave up at V).
+        const int nk = kv0 == 0 ? j + (kv > 0 ? 1 : 0) : 0, nv = kv1 == 2 ? j : 0;
         if (kE4M3) {
           if (nk > 0) mbar_wait(raw_full, (nk - 1) & 1, kChunkWaitNs);
-          if (j > 0) mbar_wait(raw_full + 1, (j - 1) & 1, kChunkWaitNs);
+          if (nv > 0) mbar_wait(raw_full + 1, (nv - 1) & 1, kChunkWaitNs);
         } else {
           for (int i = max(0, nk - kStages); i < nk; ++i) mbar_wait(k_full + i % kStages, (i / kStages) & 1, kChunkWaitNs);
-          for (int i = max(0, j - kStages); C::kSplitKV && i < j; ++i)
+          for (int i = max(0, nv - kStages); C::kSplitKV && i < nv; ++i)
             mbar_wait(v_full + i % kStages, (i / kStages) & 1, kChunkWaitNs);
         }
       }
