@@ -396,11 +396,17 @@ class PagedKV:
                 raise ValueError(f"expected contiguous fp32 scales of shape ({h},) on the pages' device")
         self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
         self.n_pages, self.page_size, self.n_heads, self.head_dim = n, ps, h, d
-        self.device, self.status = k_pages.device, status_block(k_pages.device)
+        self.device, self._status = k_pages.device, None
         self._c = SagePagedKVC(k_pages.data_ptr(), v_pages.data_ptr(), n, ps, h, d, *k_pages.stride()[:3],
                                *v_pages.stride()[:3], 1 if e4m3 else 0, k_scale.data_ptr() if e4m3 else None,
                                v_scale.data_ptr() if e4m3 else None)
         self._ref = ctypes.byref(self._c)
+
+    @property
+    def status(self) -> torch.Tensor:
+        if self._status is None:
+            self._status = status_block(self.device)
+        return self._status
 
 
 class PagedBatch:
@@ -435,11 +441,17 @@ def paged_workspace(head_dim: int, device="cuda") -> torch.Tensor:
     return ws
 
 
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
 def _paged_view(t: torch.Tensor, d: int, device, what: str) -> SageView:
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[2] != d or stride[2] != 1 or t.dtype is not torch.bfloat16 or t.device != device:
+    if t.dim() != 3:
+        raise ValueError(f"{what}: expected a bf16 [N, H, {d}] tensor")
+    n, h, channels = t.shape
+    token, head, unit = t.stride()
+    if channels != d or unit != 1 or t.dtype is not _BF16 or t.device != device:
         raise ValueError(f"{what}: expected a bf16 [N, H, {d}] tensor with unit channel stride on the cache's device")
-    return SageView(t.data_ptr(), shape[0], shape[1], d, stride[0], stride[1])
+    return SageView(t.data_ptr(), n, h, d, token, head)
 
 
 def _paged_call(device, stream, fn, args) -> int:
@@ -455,7 +467,7 @@ def _paged_call(device, stream, fn, args) -> int:
 def _fp32_table(t: Optional[torch.Tensor], shape: tuple, device, what: str):
     if t is None:
         return None
-    if t.dtype is not torch.float32 or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not _F32 or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous fp32 tensor of shape {shape} on the cache's device")
     return t.data_ptr()
 
@@ -485,20 +497,20 @@ def sage_paged_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKV, batch: P
         oargs = (vo.data, vo.stride_token, vo.stride_head)
     elif q_out is not None or gamma_q is not None:
         raise ValueError("q_out and gamma_q belong to q")
-    rows = rope_cos.shape[0] if rope_cos is not None else 0
-    if positions is not None and (positions.dtype is not torch.int32 or tuple(positions.shape) != (k.shape[0],)
+    if positions is not None and (positions.dtype is not _I32 or positions.shape != (k.shape[0],)
                                   or not positions.is_contiguous() or positions.device != dev):
         raise ValueError("positions: expected a contiguous int32 tensor [N] on the cache's device")
-    status = cache.status if status is None else status
-    if status.device != dev or status.numel() * status.element_size() < 256:
+    if status is None:
+        status = cache.status
+    elif status.device != dev or status.nbytes < 256:
         raise ValueError("status: expected a zeroed block of 256 bytes on the cache's device")
-    by = ctypes.byref
+    rows = rope_cos.shape[0] if rope_cos is not None else 0
+    table, weight, by = (rows, d // 2), (d,), ctypes.byref
     _check(_paged_call(dev, stream, lib().sage_paged_append, (
-        None if vq is None else by(vq), by(vk), by(vv), _fp32_table(gamma_q, (d,), dev, "gamma_q"),
-        _fp32_table(gamma_k, (d,), dev, "gamma_k"), _fp32_table(rope_cos, (rows, d // 2), dev, "rope_cos"),
-        _fp32_table(rope_sin, (rows, d // 2), dev, "rope_sin"), rows,
-        None if positions is None else positions.data_ptr(), eps, cache._ref, batch._ref, *oargs, status.data_ptr())),
-        "sage_paged_append")
+        None if vq is None else by(vq), by(vk), by(vv), _fp32_table(gamma_q, weight, dev, "gamma_q"),
+        _fp32_table(gamma_k, weight, dev, "gamma_k"), _fp32_table(rope_cos, table, dev, "rope_cos"),
+        _fp32_table(rope_sin, table, dev, "rope_sin"), rows, None if positions is None else positions.data_ptr(), eps,
+        cache._ref, batch._ref, *oargs, status.data_ptr())), "sage_paged_append")
     return q_out
 
 
@@ -517,7 +529,7 @@ def sage_paged_attn(q: torch.Tensor, cache: PagedKV, batch: PagedBatch, sm_scale
     vo = _paged_view(out, d, dev, "out")
     if vo.n_tokens != vq.n_tokens or vo.n_heads != vq.n_heads:
         raise ValueError("out must have q's shape")
-    if lse is not None and (lse.dtype is not torch.float32 or tuple(lse.shape) != tuple(q.shape[:2])
+    if lse is not None and (lse.dtype is not _F32 or lse.shape != q.shape[:2]
                             or not lse.is_contiguous() or lse.device != dev):
         raise ValueError("lse: expected a contiguous fp32 tensor [N, Hq] on the cache's device")
     if ws is None:
@@ -527,6 +539,6 @@ def sage_paged_attn(q: torch.Tensor, cache: PagedKV, batch: PagedBatch, sm_scale
     sm_scale = 1.0 / math.sqrt(d) if sm_scale is None else sm_scale
     _check(_paged_call(dev, stream, lib().sage_paged_attn, (
         ctypes.byref(vq), cache._ref, batch._ref, sm_scale, 1 if causal else 0, window or 0, vo.data, vo.stride_token,
-        vo.stride_head, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())),
+        vo.stride_head, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes)),
         "sage_paged_attn")
     return out

@@ -58,14 +58,15 @@ struct FewCfg {
   static constexpr int kNT = kWarpKeys / 8;                   // 8-key score tiles per warp
   static constexpr int kOT = D / 8;                           // 8-channel O tiles
   static constexpr int kQRow = D * 2 + 16;                    // padded Q row
-  static constexpr int kMergeRow = 72;                        // padded merge row: 64 channels
+  static constexpr int kMergeRow = D + 8;                     // padded merge row
   static constexpr int kQOff = kStages * kStageBytes;
   static constexpr int kMergeOff = kQOff + 2 * kRows * kQRow;
   static constexpr int kMlOff = kMergeOff + 8 * 16 * kMergeRow * 4;
-  static constexpr int kScaleOff = kMlOff + 2 * 8 * kRows * 4;   // 2^e of each Q row (E4M3), per buffer
+  static constexpr int kScaleOff = kMlOff + 2 * 8 * 16 * 4;   // 2^e of each Q row (E4M3), per buffer
   static constexpr int kBarOff = kScaleOff + 2 * kRows * 4;
   static constexpr int kNumBars = 2 * kStages + 4;
   static constexpr int kSmem = kBarOff + kNumBars * 8 + kStages * 4 + 16 + 1024;
+  static_assert(kSmem <= 232448 - 512, "shared memory");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t r[4], uint32_t a) {
@@ -462,8 +463,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int tid = threadIdx.x - 128, cw = warp - 4;   // among the consumers
   const int team = cw >> 2, kw0 = (cw & 3) * C::kWarpKeys;
   float* merge = reinterpret_cast<float*>(smem + C::kMergeOff);
-  float* sm_m = reinterpret_cast<float*>(smem + C::kMlOff);   // [8][R]
-  float* sm_l = sm_m + 8 * R;
+  float* sm_m = reinterpret_cast<float*>(smem + C::kMlOff);   // [8][16]
+  float* sm_l = sm_m + 8 * 16;
   float* q_exp = reinterpret_cast<float*>(smem + C::kScaleOff);
   // Row r of the unit (its sequence's first q row, K/V head, row tile): four channels of the output, its lse.
   auto store4 = [&](int start, int h, int qi, int r, int d, float inv, float v0, float v1, float v2, float v3) {
@@ -781,16 +782,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // ---- the eight warps' results joined
     __syncwarp();
     if (lane == 0) mbar_arrive(q_empty + buf);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (c == 0) {
-          sm_m[cw * R + mt * 16 + e * 8 + g] = m[mt][e];
-          sm_l[cw * R + mt * 16 + e * 8 + g] = ol[mt][2 * e];
-        }
-      }
-    consumer_sync();
     const bool whole_unit = wk.k == 0 && n == wk.w.nt;
     int cf = 0, parts = 1;
     if (!whole_unit) wk.unit_parts(cf, parts);
@@ -799,62 +790,67 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const float vs = kE4M3 ? __ldg(a.v_scale + h) : 1.0f;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      float fac[2];
+      // Each warp leaves its maxima, sums and O of 16 rows; the readers bring them to a common maximum.
+      if (c == 0) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float mm = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) mm = fmaxf(mm, sm_m[w * R + mt * 16 + e * 8 + g]);
-        fac[e] = mm == -INFINITY ? 0.0f : ex2_approx(m[mt][e] - mm);
-      }
-#pragma unroll
-      for (int half = 0; half < D / 64; ++half) {
-        float* mine = merge + cw * 16 * C::kMergeRow;
-        if (!kE4M3) {
-#pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            const float* v = o[mt][half * 8 + t];
-            *reinterpret_cast<float2*>(mine + g * C::kMergeRow + t * 8 + 2 * c) = make_float2(v[0] * fac[0], v[1] * fac[0]);
-            *reinterpret_cast<float2*>(mine + (g + 8) * C::kMergeRow + t * 8 + 2 * c) =
-                make_float2(v[2] * fac[1], v[3] * fac[1]);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < C::kOT; ++j) {
-            if (D == 128) {
-              mine[g * C::kMergeRow + 16 * c + j] = o[mt][j][half] * fac[0];
-              mine[(g + 8) * C::kMergeRow + 16 * c + j] = o[mt][j][2 + half] * fac[1];
-            } else {
-              mine[g * C::kMergeRow + 16 * c + j] = o[mt][j][0] * fac[0];
-              mine[g * C::kMergeRow + 16 * c + 8 + j] = o[mt][j][1] * fac[0];
-              mine[(g + 8) * C::kMergeRow + 16 * c + j] = o[mt][j][2] * fac[1];
-              mine[(g + 8) * C::kMergeRow + 16 * c + 8 + j] = o[mt][j][3] * fac[1];
-            }
-          }
+        for (int e = 0; e < 2; ++e) {
+          sm_m[cw * 16 + e * 8 + g] = m[mt][e];
+          sm_l[cw * 16 + e * 8 + g] = ol[mt][2 * e];
         }
-        consumer_sync();
-        const int r16 = tid >> 4, d4 = (tid & 15) * 4, r = mt * 16 + r16;
-        if (r < live) {
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          float mm = -INFINITY, ll = 0.0f;
+      }
+      float* mine = merge + cw * 16 * C::kMergeRow;
+      if (!kE4M3) {
 #pragma unroll
-          for (int w = 0; w < 8; ++w) mm = fmaxf(mm, sm_m[w * R + r]);
+        for (int t = 0; t < C::kOT; ++t) {
+          const float* v = o[mt][t];
+          *reinterpret_cast<float2*>(mine + g * C::kMergeRow + t * 8 + 2 * c) = make_float2(v[0], v[1]);
+          *reinterpret_cast<float2*>(mine + (g + 8) * C::kMergeRow + t * 8 + 2 * c) = make_float2(v[2], v[3]);
+        }
+      } else {
+        // Columns 2 c and 2 c + 1 of O tile j are channels 16 c + j and kUp further: 64 (D = 128) or 8.
+        constexpr int kUp = D == 128 ? 64 : 8;
+        float* at = mine + g * C::kMergeRow + 16 * c;
+#pragma unroll
+        for (int j = 0; j < C::kOT; ++j) {
+          at[j] = o[mt][j][0];
+          at[kUp + j] = o[mt][j][1];
+          at[8 * C::kMergeRow + j] = o[mt][j][2];
+          at[8 * C::kMergeRow + kUp + j] = o[mt][j][3];
+        }
+      }
+      consumer_sync();
+      const int r16 = tid >> 4, r = mt * 16 + r16;
+      if (r < live) {
+        float f[8], mm = -INFINITY, ll = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) mm = fmaxf(mm, sm_m[w * 16 + r16]);
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          f[w] = mm == -INFINITY ? 0.0f : ex2_approx(sm_m[w * 16 + r16] - mm);
+          ll = fmaf(sm_l[w * 16 + r16], f[w], ll);
+        }
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half) {
+          const int d4 = half * 64 + (tid & 15) * 4;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int w = 0; w < 8; ++w) {
-            const float4 q = *reinterpret_cast<const float4*>(merge + (w * 16 + r16) * C::kMergeRow + d4);
-            v.x += q.x; v.y += q.y; v.z += q.z; v.w += q.w;
-            if (mm != -INFINITY) ll += sm_l[w * R + r] * ex2_approx(sm_m[w * R + r] - mm);
+            const float4 y = *reinterpret_cast<const float4*>(merge + (w * 16 + r16) * C::kMergeRow + d4);
+            v.x = fmaf(y.x, f[w], v.x);
+            v.y = fmaf(y.y, f[w], v.y);
+            v.z = fmaf(y.z, f[w], v.z);
+            v.w = fmaf(y.w, f[w], v.w);
           }
           if (whole_unit) {
-            store4(wk.w.start, h, qi, r, half * 64 + d4, ll > 0.0f ? vs / ll : 0.0f, v.x, v.y, v.z, v.w);
-            if (a.lse && half == 0 && d4 == 0) store_lse(wk.w.start, h, qi, r, mm, ll);
+            store4(wk.w.start, h, qi, r, d4, ll > 0.0f ? vs / ll : 0.0f, v.x, v.y, v.z, v.w);
+            if (a.lse && d4 == 0) store_lse(wk.w.start, h, qi, r, mm, ll);
           } else {
-            *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(slot) * R + r) * D + half * 64 + d4) = v;
-            if (half == 0 && d4 == 0) a.part_ml[slot * R + r] = make_float2(mm, ll);
+            *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(slot) * R + r) * D + d4) = v;
+            if (d4 == 0) a.part_ml[slot * R + r] = make_float2(mm, ll);
           }
         }
-        consumer_sync();
       }
+      consumer_sync();
     }
     if (!whole_unit) {
       // The loop above ended with the CTA's barrier: thread 0's release covers every thread's stores.  Whether the part
