@@ -318,10 +318,11 @@ sage_status sage_debug_wait_timeout(void* status_block, int64_t limit_ns, void* 
 sage_status sage_measure_mma_rate(int64_t mode, int64_t iters, int64_t ctas, void* status_block, void* stream);
 
 /* Waits for `stream`, reads the status block (device pointer) and returns SAGE_OK,
- * SAGE_ERR_DEVICE_TIMEOUT (a bounded wait expired; the block is then cleared) or
- * SAGE_ERR_CUDA.  If where != NULL (host), *where receives the code of the wait that
+ * SAGE_ERR_DEVICE_TIMEOUT (a bounded wait expired; the block is then cleared),
+ * SAGE_ERR_INVALID_ARG (a call of sage_paged.h met an index out of range in device memory; the
+ * block is then cleared) or SAGE_ERR_CUDA.  If where != NULL (host), *where receives the code of the wait that
  * expired: 1 Q tile, 2 K/V tile loaded, 3 K/V slot free, 4 S ready, 5 P ready, 6 P.V done,
- * 7/8 the S-tile hook's load / MMA, 10 the timeout hook; 0 if none.  This is the one call that
+ * 7/8 the S-tile hook's load / MMA, 10 the timeout hook, 16 and up those of sage_paged.h; 0 if none.  This is the one call that
  * synchronises. */
 sage_status sage_check_device_status(void* status_block, void* stream, int32_t* where);
 

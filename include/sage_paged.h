@@ -15,7 +15,8 @@
  * check every index before they use it.  An index that is out of range is never followed; the call
  * goes on with the rest as each entry point says, and the status block records SAGE_ERR_INVALID_ARG
  * with where = 16 (page table entry), 17 (length) or 18 (row of the rotary table), which
- * sage_check_device_status returns.  Since lengths are read on the device, a captured CUDA graph
+ * sage_check_device_status returns; the first one recorded stays until it is read.  A device wait that
+ * expires is recorded as in sage.h (where = 19, 20 or 21).  Since lengths are read on the device, a captured CUDA graph
  * may be replayed after they changed, as long as the buffers and n_tokens, n_seqs stay.
  */
 #ifndef SAGE_GB300_PAGED_H
@@ -99,7 +100,8 @@ typedef struct sage_paged_batch {
  * A token with no place (left padding, a position past max_pages * page_size, a page or table row
  * out of range) is not stored and its q_out row becomes 0; left padding is no error.  No two tokens
  * of a call may have the same slot of the same page.  Views need 16-byte aligned data and strides of
- * multiples of 8 elements; n_tokens may be 0.  One launch. */
+ * multiples of 8 elements; n_tokens may be 0 (nothing is launched), n_tokens at most 2^22 and
+ * n_tokens * (n_heads_q + 2 n_heads) at most 2^31.  One launch. */
 sage_status sage_paged_append(const sage_view* q, const sage_view* k, const sage_view* v, const float* gamma_q,
                               const float* gamma_k, const float* rope_cos, const float* rope_sin, int64_t rope_rows,
                               const int32_t* positions, float eps, const sage_paged_kv* cache,
@@ -120,22 +122,27 @@ size_t sage_paged_workspace_bytes(int64_t head_dim);
  *   causal 0: all of [0, kv_len);   causal 1: those up to the token's own position pos;
  *   window > 0 (with causal 1 only): of those the last `window`, j > pos - window.
  * A row that sees no key becomes 0, its lse -infinity.  Scores, maxima, sums and accumulators are fp32;
- * p is rounded to bf16 (fp16 with an E4M3 cache and few rows) for the product with V, as in
- * sage_attn_dense_bf16_tc.  Stored K and V of a sequence's visible range must be finite (a NaN in a
+ * p is rounded to bf16 for the product with V, as in sage_attn_dense_bf16_tc, or to fp16 with an E4M3
+ * cache (whose codes fp16 holds exactly; q is then held as fp16 times a power of two per row).  Against a running
+ * maximum that may lag by 2^8, p lies in [0, 2^8].  Per element, |out - exact| <= 2^-7 sum_j w_j |v_j| + 2^-8 |out|
+ * plus fp32 rounding, w the exact weights.  Stored K and V of a sequence's visible range must be finite (a NaN in a
  * value that only some of the rows see may reach the others).  Key positions whose page entry is out of
  * range are left out, as masked ones.
  *   q            bf16 [n_tokens, n_heads_q, head_dim] view; n_heads_q a multiple of the cache's
  *                n_heads, at most 128 times as many.
  *   out          bf16, element (t, h, c) at out[t * out_stride_token + h * out_stride_head + c],
- *                16-byte aligned, strides multiples of 8 elements, not overlapping the inputs.
+ *                16-byte aligned, strides multiples of 8 elements and not 0 where there are several rows, not
+ *                overlapping the inputs.
  *   lse          NULL, or device fp32 [n_tokens][n_heads_q] contiguous: ln sum_j exp(sm_scale q . k_j).
- *   sm_scale     positive and finite.
+ *   sm_scale     positive, finite also when multiplied by log2 e.
  *   ws           256-byte aligned, >= sage_paged_workspace_bytes; its first SAGE_PAGED_WS_HEADER bytes
  *                zeroed once by the caller before its first use (and again after a recorded timeout);
  *                it begins with the status block.  Calls that may overlap on the GPU need workspaces of
  *                their own.
  * The result does not depend on what else runs: partial results are joined in a fixed order.
- * One launch. */
+ * A batch whose mean query rows per K/V head and sequence (new tokens times n_heads_q / n_heads) are at most 32 takes
+ * one launch of the kernel for few rows (a batch of 2^31 or more key tiles of 16 KB of K is recorded as where =
+ * 17 and not computed), any other the tensor-core kernel for many rows, one launch or two. */
 sage_status sage_paged_attn(const sage_view* q, const sage_paged_kv* cache, const sage_paged_batch* batch,
                             float sm_scale, int64_t causal, int64_t window, void* out, int64_t out_stride_token,
                             int64_t out_stride_head, float* lse, void* ws, size_t ws_bytes, void* stream);

@@ -171,6 +171,21 @@ def test_append_bad_index_is_recorded_not_followed(what, where):
     assert changed.sum() >= len(stored) - 1
 
 
+def test_append_special_values_into_an_8_bit_cache():
+    """Infinities saturate, NaN stays NaN, the largest code is 448, zeros keep their sign."""
+    p = Problem([1, 1], [1, 1], 2, 2, 64, 8, "e4m3", seed=31)
+    cache, batch = _handles(p)
+    v = p.v.clone()
+    s = p.v_scale.double()
+    v[0, 0, :6] = torch.tensor([float("inf"), float("-inf"), float("nan"), 0.0, -0.0, 1e30], dtype=torch.bfloat16)
+    sage.sage_paged_append(p.k, v, cache, batch)
+    got = p.v_pages[int(p.table[0, 0]), 0, 0]
+    assert got[:2].double().tolist() == [448.0, -448.0] and bool(got[2].double().isnan())
+    assert got.view(torch.uint8)[3:6].tolist() == [0x00, 0x80, 0x7E]
+    want = (v[0, 0, 6:].double() / s[0]).clamp(-448, 448)
+    assert ((got[6:].double() - want).abs() <= want.abs() * 2.0 ** -4 + 2.0 ** -10).all()
+
+
 def test_append_nothing():
     p = Problem([0, 0], [0, 5], 2, 2, 64, 8, seed=8)
     cache, batch = _handles(p)
@@ -259,6 +274,69 @@ def test_attention_of_a_long_ragged_batch(fmt):
     for _ in range(10):
         assert torch.equal(_bits(sage.sage_paged_attn(p.q, cache, batch, ws=ws)), _bits(out))
     assert sage.sage_check_device_status(ws) == (0, 0)
+
+
+SPLIT = [
+    # few units over many keys: the key axis of the many-row kernel is split and joined
+    ([65], [9001], 8, 2, 128, 64, "bf16", True, 0),
+    ([40], [7777], 8, 1, 128, 16, "e4m3", True, 0),
+    ([300], [6000], 1, 1, 64, 32, "bf16", False, 0),
+    ([129], [5000], 2, 2, 64, 8, "e4m3", True, 3000),
+    ([128, 1], [8000, 70], 4, 2, 128, 256, "bf16", True, 2500),
+]
+
+
+@pytest.mark.parametrize("case", SPLIT, ids=lambda c: f"q{max(c[0])}-kv{max(c[1])}-{c[2]}-{c[3]}-{c[4]}-{c[6]}-w{c[8]}")
+def test_attention_of_a_chunk_behind_a_long_context(case):
+    q_lens, kv_lens, hq, hkv, d, page, fmt, causal, window = case
+    p = Problem(q_lens, kv_lens, hq, hkv, d, page, fmt, seed=32 + hq)
+    cache, batch = _handles(p)
+    ws = sage.paged_workspace(d)
+    lse = torch.empty((p.n, hq), dtype=torch.float32, device="cuda")
+    out = sage.sage_paged_attn(p.q, cache, batch, causal=causal, window=window, lse=lse, ws=ws)
+    ref = paged_ref.attention(p, p.q, causal, window)
+    paged_ref.check_attention(p, out, ref)
+    lim = p.d * 2.0 ** -23 * ref[3] / math.sqrt(d) + 1.01 * 2.0 ** -8 + 1e-5 * (1 + ref[1].abs())
+    assert ((lse.double() - ref[1]).abs() <= lim).all()
+    assert torch.equal(_bits(sage.sage_paged_attn(p.q, cache, batch, causal=causal, window=window, ws=ws)), _bits(out))
+    assert sage.sage_check_device_status(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("fmt,d", [("bf16", 128), ("e4m3", 64)])
+def test_attention_of_many_sequences_of_mixed_lengths(fmt, d):
+    """More sequences than a warp has lanes, prompts among single tokens and empty ones."""
+    q_lens = [(1, 0, 90, 3, 260)[i % 5] for i in range(45)]
+    kv_lens = [n + (37 * i) % 500 if n else 0 for i, n in enumerate(q_lens)]
+    p = Problem(q_lens, kv_lens, 4, 2, d, 16, fmt, seed=33)
+    cache, batch = _handles(p)
+    out = sage.sage_paged_attn(p.q, cache, batch)
+    paged_ref.check_attention(p, out, paged_ref.attention(p, p.q, True))
+
+
+@pytest.mark.parametrize("q_len", [1, 70])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_attention_of_rows_of_very_different_size(q_len, fmt):
+    """Query rows scaled by 2^-90 .. 2^10, and the scores' scale with them: relative accuracy is kept."""
+    p = Problem([q_len], [400], 4, 2, 64, 16, fmt, seed=34)
+    cache, batch = _handles(p)
+    for shift in (-90, 10):
+        q = (p.q.float() * 2.0 ** shift).to(torch.bfloat16)
+        sm = 2.0 ** -shift / 8
+        out = sage.sage_paged_attn(q, cache, batch, sm_scale=sm)
+        paged_ref.check_attention(p, out, paged_ref.attention(p, q, True, sm_scale=sm), sm_scale=sm)
+    q = p.q.contiguous().clone()
+    q[:, 1] = 0                       # a head of zeros: uniform weights
+    out = sage.sage_paged_attn(q, cache, batch)
+    paged_ref.check_attention(p, out, paged_ref.attention(p, q, True))
+
+
+def test_attention_of_an_expanded_query():
+    """One query row for all heads (stride 0)."""
+    p = Problem([3, 60], [50, 200], 6, 2, 128, 16, seed=35)
+    cache, batch = _handles(p)
+    q = p.q[:, :1].expand(-1, 6, -1)
+    out = sage.sage_paged_attn(q, cache, batch)
+    paged_ref.check_attention(p, out, paged_ref.attention(p, q, True))
 
 
 def test_attention_shared_prefix_and_strided_views():

@@ -106,6 +106,8 @@ def test_append_refusals(L):
     assert _append(L, q=q, q_out=None) == 1
     assert _append(L, q=q, q_out=4104) == 2
     assert _append(L, q=q, ost=12) == 2
+    assert _append(L, q=q, ost=0) == 1 and _append(L, q=q, osh=0) == 1      # rows that coincide
+    assert _append(L, q=_view(n=1 << 20, h=2500), k=_view(n=1 << 20), v=_view(n=1 << 20)) == 3   # over 2^31 rows
     assert _append(L, q=_view(h=5000)) == 3
     assert _append(L, cos=4096) == 1 and _append(L, sin=4096) == 1
     assert _append(L, cos=4096, sin=4096, rows=0) == 1
@@ -132,8 +134,9 @@ def test_attention_refusals(L):
     assert _attn(L, q=_view(ptr=4100, h=8)) == 2
     assert _attn(L, causal=2) == 1 and _attn(L, window=-1) == 1
     assert _attn(L, causal=0, window=5) == 1                  # a window needs causal attention
-    for sm in (0.0, -1.0, float("nan"), float("inf")):
+    for sm in (0.0, -1.0, float("nan"), float("inf"), 3e38):
         assert _attn(L, sm=sm) == 1
+    assert _attn(L, ost=0) == 1 and _attn(L, osh=0) == 1
     assert _attn(L, out=None) == 1 and _attn(L, out=4100) == 2 and _attn(L, osh=20) == 2 and _attn(L, ost=-8) == 1
     assert _attn(L, lse=4098) == 2
     need = int(L.sage_paged_workspace_bytes(128))

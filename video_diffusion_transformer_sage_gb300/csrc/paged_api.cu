@@ -10,6 +10,7 @@
 namespace {
 
 constexpr size_t kStatusBytes = 256;
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr int64_t kMaxRows = int64_t(1) << 22, kMaxHeads = 4096, kMaxSeqs = 65536;
 
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -57,8 +58,9 @@ sage_status check_batch(const sage_paged_batch* b, int64_t page_size) {
   return SAGE_OK;
 }
 
-sage_status check_target(const void* out, int64_t ost, int64_t osh) {
-  if (!out || ost < 0 || osh < 0) return SAGE_ERR_INVALID_ARG;
+// An output of the view's shape; rows that coincide (a zero stride) are refused.
+sage_status check_target(const void* out, int64_t ost, int64_t osh, const sage_view* v) {
+  if (!out || ost < 0 || osh < 0 || (ost == 0 && v->n_tokens > 1) || (osh == 0 && v->n_heads > 1)) return SAGE_ERR_INVALID_ARG;
   if (!aligned(out, 16) || (ost % 8) != 0 || (osh % 8) != 0) return SAGE_ERR_ALIGNMENT;
   return SAGE_OK;
 }
@@ -103,7 +105,7 @@ sage_status sage_paged_append(const sage_view* q, const sage_view* k, const sage
   if (k->n_heads != cache->n_heads || v->n_heads != cache->n_heads) return SAGE_ERR_INVALID_ARG;
   if (q) {
     if ((st = check_rows(q, n, d)) != SAGE_OK) return st;
-    if (n > 0 && (st = check_target(q_out, q_out_stride_token, q_out_stride_head)) != SAGE_OK) return st;
+    if (n > 0 && (st = check_target(q_out, q_out_stride_token, q_out_stride_head, q)) != SAGE_OK) return st;
   }
   if ((rope_cos == nullptr) != (rope_sin == nullptr) || (rope_cos && rope_rows <= 0)) return SAGE_ERR_INVALID_ARG;
   if (!(eps >= 0.0f) || !(eps < INFINITY)) return SAGE_ERR_INVALID_ARG;
@@ -111,6 +113,7 @@ sage_status sage_paged_append(const sage_view* q, const sage_view* k, const sage
       !aligned(positions, 4) || !aligned(status_block, 4))
     return SAGE_ERR_ALIGNMENT;
   if (!status_block) return SAGE_ERR_INVALID_ARG;
+  if (n * ((q ? q->n_heads : 0) + 2 * cache->n_heads) > (int64_t(1) << 31)) return SAGE_ERR_UNSUPPORTED;   // rows
   if (n == 0 || batch->n_seqs == 0) return SAGE_OK;
   const int64_t e = cache->format == 1 ? 1 : 2;
   sage::PagedAppendArgs a;
@@ -168,8 +171,8 @@ sage_status sage_paged_attn(const sage_view* q, const sage_paged_kv* cache, cons
   if (q->n_heads % cache->n_heads != 0) return SAGE_ERR_INVALID_ARG;
   if (q->n_heads / cache->n_heads > 128) return SAGE_ERR_UNSUPPORTED;
   if ((causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal)) return SAGE_ERR_INVALID_ARG;
-  if (!(sm_scale > 0.0f) || !(sm_scale < INFINITY)) return SAGE_ERR_INVALID_ARG;
-  if (n > 0 && (st = check_target(out, out_stride_token, out_stride_head)) != SAGE_OK) return st;
+  if (!(sm_scale > 0.0f) || !(sm_scale * kLog2e < INFINITY)) return SAGE_ERR_INVALID_ARG;
+  if (n > 0 && (st = check_target(out, out_stride_token, out_stride_head, q)) != SAGE_OK) return st;
   if (!aligned(lse, 4)) return SAGE_ERR_ALIGNMENT;
   if (!ws) return SAGE_ERR_WORKSPACE;
   if (!aligned(ws, 256)) return SAGE_ERR_ALIGNMENT;
@@ -184,7 +187,7 @@ sage_status sage_paged_attn(const sage_view* q, const sage_paged_kv* cache, cons
   a.hkv = static_cast<int>(cache->n_heads);
   a.causal = static_cast<int>(causal);
   a.window = window > (int64_t(1) << 30) ? 0 : static_cast<int>(window);   // longer than any sequence: none
-  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.scale_log2 = sm_scale * kLog2e;
   a.k_scale = cache->k_scale;
   a.v_scale = cache->v_scale;
   a.out = static_cast<uint16_t*>(out);
