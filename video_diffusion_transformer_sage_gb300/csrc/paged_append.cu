@@ -1,17 +1,18 @@
 // paged_append.cu -- new tokens into the paged K/V cache: RMSNorm and rotation of Q and K rows (the
 // row arithmetic of qk_row.cuh), K and V stored to their pages as bf16 or E4M3 codes.
 //
-// A warp takes up to 4 kSteps rows (8 kSteps at D = 64) of one token: its Q heads, then its K heads,
-// then its V heads.  D/16 lanes hold a row, each the 8-channel groups g and g + D/16, which are the first two that the
-// row's sum of squares adds: the fold over the lanes is then the same butterfly as with a lane per group,
-// and the root, the division and the address of a row are paid by half as many threads.  The rows are loaded first;
-// the chain cu_q -> kv_len -> page table -> rotary row hides under them.  Warps do not wait for one another.
+// A warp takes up to 4 kSteps heads (8 kSteps at D = 64) of one token, all of Q, of K or of V, so what a row needs is the
+// same for all its lanes.  D/16 lanes hold a row, each the 8-channel groups g and g + D/16, which are the first two that
+// the row's sum of squares adds: the fold over the lanes is then the same butterfly as with a lane per group, and the
+// root, the division and the address of a row are paid by half as many threads.  Products go two to an
+// instruction.  The rows are loaded first; the chain cu_q -> kv_len -> page table -> rotary row hides under them.  Warps do
+// not wait for one another.
 //
-// What bounds it: HBM for many tokens, each row read once and written once: 4.77 TB/s at 3024 tokens of 168 rows of
-// D = 128 (54.9 us), 3.9 TB/s at 11927 tokens of 72 rows of D = 64 into E4M3 (47.6 us), where the instructions of
-// the norm weigh as much as the bytes; for few tokens the chain of dependent loads.  A warp takes three steps of rows
-// where the batch fills the GPU (two: 55.9 and 51.3 us, one: 64.0 and 58.0), two where three would leave
-// lanes of a token's last warp idle, one where spreading the rows over more SMs shortens the chain.
+// What bounds it: HBM for many tokens, each row read once and written once, with about as much issue time: 5.23 TB/s at
+// 3024 tokens of 168 rows of D = 128 (50.1 us), 4.09 TB/s at 11927 tokens of 72 rows of D = 64 into E4M3 (45.5 us); for few
+// tokens the chain of dependent loads.  A warp takes two steps of heads where the batch fills the GPU (one: 57.1 and
+// 53.6 us), three where that leaves fewer lanes idle (24 heads of D = 64: 54.2 us with two), one where spreading the rows
+// over more SMs shortens the chain.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -41,28 +42,40 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return w;
 }
 
+// Segments (runs of kSteps * kPer heads, one warp each) of a token's Q, and of its K or V.
+struct AppendSegs {
+  uint32_t q, kv;
+};
+
 template <int D, bool kE4M3, int kSteps>
-__global__ void __launch_bounds__(256, kSteps == 3 ? 3 : 4) paged_append_kernel(const PagedAppendArgs a, const uint32_t segs) {
+__global__ void __launch_bounds__(256, kSteps == 1 ? 5 : 4) paged_append_kernel(const PagedAppendArgs a, const AppendSegs segs) {
   constexpr int kLanes = D / 16, kPer = 32 / kLanes;   // lanes of a row, rows of a step
   const int lane = threadIdx.x & 31, g = lane % kLanes;
-  const int rows = a.hq + 2 * a.hkv;
-  const uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int t = static_cast<int>(unit / segs);
+  const uint32_t unit = blockIdx.x * 8 + (threadIdx.x >> 5), per_token = segs.q + 2 * segs.kv;
+  const int t = static_cast<int>(unit / per_token);
   if (t >= a.b.n_tokens) return;
-  const int r0 = static_cast<int>(unit - t * segs) * (kSteps * kPer) + lane / kLanes;
+  uint32_t seg = unit - t * per_token;
+  const bool first = seg == 0;
+  // What the warp's rows are: all Q, all K or all V.
+  const bool is_q = seg < segs.q, is_v = seg >= segs.q + segs.kv;
+  seg -= is_q ? 0u : is_v ? segs.q + segs.kv : segs.q;
+  const int heads = is_q ? a.hq : a.hkv;
+  const int64_t sh = is_q ? a.qsh : is_v ? a.vsh : a.ksh;
+  const int h0 = static_cast<int>(seg) * (kSteps * kPer) + lane / kLanes;
+  const uint16_t* src = (is_q ? a.q + t * a.qst : is_v ? a.v + t * a.vst : a.k + t * a.kst) + h0 * sh + g * 8;
   uint4 x[kSteps][2];
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
-    const int r = r0 + i * kPer, h = r - a.hq;
     x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-    if (r < a.hq) {
-      const uint16_t* p = a.q + t * a.qst + r * a.qsh + g * 8;
-      x[i][0] = ld_row8<true>(p);
-      x[i][1] = ld_row8<true>(p + D / 2);
-    } else if (r < rows) {
-      const uint16_t* p = (h < a.hkv ? a.k + t * a.kst + h * a.ksh : a.v + t * a.vst + (h - a.hkv) * a.vsh) + g * 8;
-      x[i][0] = ld_row8<false>(p);
-      x[i][1] = ld_row8<false>(p + D / 2);
+    if (h0 + i * kPer < heads) {
+      const uint16_t* p = src + i * kPer * sh;
+      if (is_q) {
+        x[i][0] = ld_row8<true>(p);
+        x[i][1] = ld_row8<true>(p + D / 2);
+      } else {
+        x[i][0] = ld_row8<false>(p);
+        x[i][1] = ld_row8<false>(p + D / 2);
+      }
     }
   }
   const int b = find_seq(a.b, t);
@@ -74,9 +87,45 @@ __global__ void __launch_bounds__(256, kSteps == 3 ? 3 : 4) paged_append_kernel(
   int page = -1;
   if (pos >= 0 && pos < a.b.cap) page = __ldg(a.b.table + b * a.b.table_stride + (pos >> a.b.page_shift));
   const bool row_ok = !a.rope_cos || (row >= 0 && row < a.rope_rows);
+  const bool placed = page >= 0 && page < a.b.n_pages && row_ok;
+  if (!placed && pos >= 0 && first && lane == 0)
+    record_bad_index(a.status, pos >= a.b.cap ? kWhereLength : row_ok ? kWherePage : kWhereRopeRow);
+  if (!placed) {
+    // Nothing stored; a Q row becomes 0.
+    if (is_q) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        uint16_t* dst = a.q_out + t * a.ost + (h0 + i * kPer) * a.osh + g * 8;
+        if (h0 + i * kPer < heads) {
+          *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(dst + D / 2) = make_uint4(0, 0, 0, 0);
+        }
+      }
+    }
+    return;
+  }
+  const int64_t slot = pos & ((1 << a.b.page_shift) - 1);
+  // Row h goes to dst + h * dh (bytes).
+  uint8_t* dst = is_q ? reinterpret_cast<uint8_t*>(a.q_out + t * a.ost)
+                 : is_v ? a.v_pages + page * a.vp + slot * a.vt : a.k_pages + page * a.kp + slot * a.kt;
+  const int64_t dh = is_q ? a.osh * 2 : is_v ? a.vh : a.kh;
+  dst += h0 * dh;
+  if (is_v && !kE4M3) {
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      if (h0 + i * kPer < heads) {
+        uint16_t* o = reinterpret_cast<uint16_t*>(dst + i * kPer * dh) + g * 8;
+        *reinterpret_cast<uint4*>(o) = x[i][0];
+        *reinterpret_cast<uint4*>(o + D / 2) = x[i][1];
+      }
+    }
+    return;
+  }
+  const float* gamma = is_q ? a.gamma_q : is_v ? nullptr : a.gamma_k;
+  const bool turn = a.rope_cos && !is_v;
   float4 cs[2], sn[2];
   cs[0] = cs[1] = sn[0] = sn[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (a.rope_cos && row_ok) {
+  if (turn) {
     const int64_t at = row * (D / 2) + g * 4;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -84,93 +133,93 @@ __global__ void __launch_bounds__(256, kSteps == 3 ? 3 : 4) paged_append_kernel(
       sn[k] = __ldg(reinterpret_cast<const float4*>(a.rope_sin + at + k * (D / 4)));
     }
   }
-  const bool placed = page >= 0 && page < a.b.n_pages && row_ok;
-  if (!placed && pos >= 0 && r0 == 0)
-    record_bad_index(a.status, pos >= a.b.cap ? kWhereLength : row_ok ? kWherePage : kWhereRopeRow);
-  const int64_t slot = pos & ((1 << a.b.page_shift) - 1);
-  uint8_t* k_at = a.k_pages + page * a.kp + slot * a.kt;
-  uint8_t* v_at = a.v_pages + page * a.vp + slot * a.vt;
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
-    const int r = r0 + i * kPer;
-    const bool is_q = r < a.hq, is_v = r >= a.hq + a.hkv;
-    const float* gamma = is_q ? a.gamma_q : is_v ? nullptr : a.gamma_k;
-    float f[2][8];
-    unpack_bf16x8(x[i][0], f[0]);
-    unpack_bf16x8(x[i][1], f[1]);
-    if (__any_sync(0xffffffffu, gamma != nullptr && r < rows)) {
-      // sum of squares: 8 channels in order per group, groups g and g + D/16 first, then the butterfly.
-      float acc[2] = {0.0f, 0.0f};
+    // The 16 channels as pairs (2 j, 2 j + 1): a packed multiply is two separately rounded products.  Sums stay scalar.
+    uint64_t f[2][4];
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t w[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[k] = __fadd_rn(acc[k], __fmul_rn(f[k][j], f[k][j]));
+      for (int j = 0; j < 4; ++j) f[k][j] = f2_pack(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+    }
+    if (gamma) {
+      // Sum of squares: 8 channels in order per group, groups g and g + D/16 first, then the butterfly.
+      float acc[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        acc[k] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float lo, hi;
+          f2_unpack(f2_mul(f[k][j], f[k][j]), lo, hi);
+          acc[k] = __fadd_rn(__fadd_rn(acc[k], lo), hi);
+        }
+      }
       float ss = __fadd_rn(acc[0], acc[1]);
 #pragma unroll
       for (int s = kLanes / 2; s > 0; s >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, s));
-      if (gamma) {
-        const float rs = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(ss, 1.0f / D), a.eps)));   // = fl32(1 / root)
+      const float rs = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(ss, 1.0f / D), a.eps)));   // = fl32(1 / root)
+      const uint64_t rs2 = f2_pack(rs, rs);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float gm[8];
-          load_gamma8(gamma, g + k * kLanes, gm);
+      for (int k = 0; k < 2; ++k) {
+        float gm[8];
+        load_gamma8(gamma, g + k * kLanes, gm);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f[k][j] = __fmul_rn(__fmul_rn(f[k][j], rs), gm[j]);
-        }
+        for (int j = 0; j < 4; ++j) f[k][j] = f2_mul(f2_mul(f[k][j], rs2), f2_pack(gm[2 * j], gm[2 * j + 1]));
       }
     }
-    if (r >= rows) continue;
-    if (a.rope_cos && !is_v) {
+    if (turn) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const float cc[4] = {cs[k].x, cs[k].y, cs[k].z, cs[k].w}, sc[4] = {sn[k].x, sn[k].y, sn[k].z, sn[k].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float y0 = f[k][2 * j], y1 = f[k][2 * j + 1];
-          f[k][2 * j] = __fsub_rn(__fmul_rn(y0, cc[j]), __fmul_rn(y1, sc[j]));
-          f[k][2 * j + 1] = __fadd_rn(__fmul_rn(y0, sc[j]), __fmul_rn(y1, cc[j]));
+          float y0c, y1c, y0s, y1s;
+          f2_unpack(f2_mul(f[k][j], f2_pack(cc[j], cc[j])), y0c, y1c);
+          f2_unpack(f2_mul(f[k][j], f2_pack(sc[j], sc[j])), y0s, y1s);
+          f[k][j] = f2_pack(__fsub_rn(y0c, y1s), __fadd_rn(y0s, y1c));
         }
       }
     }
+    if (h0 + i * kPer >= heads) continue;
+    uint8_t* out = dst + i * kPer * dh;
     if (kE4M3 && !is_q) {
-      if (!placed) continue;
-      const int h = is_v ? r - a.hq - a.hkv : r - a.hq;
-      uint8_t* dst = is_v ? v_at + h * a.vh : k_at + h * a.kh;
-      const float rs = __frcp_rn(__ldg((is_v ? a.v_scale : a.k_scale) + h));
+      const float rs = __frcp_rn(__ldg((is_v ? a.v_scale : a.k_scale) + h0 + i * kPer));
+      const uint64_t rs2 = f2_pack(rs, rs);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         uint16_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = e4m3x2(__fmul_rn(f[k][2 * j], rs), __fmul_rn(f[k][2 * j + 1], rs));
-        *reinterpret_cast<uint2*>(dst + (g + k * kLanes) * 8) = make_uint2(pack_h2(w[0], w[1]), pack_h2(w[2], w[3]));
+        for (int j = 0; j < 4; ++j) {
+          float lo, hi;
+          f2_unpack(f2_mul(f[k][j], rs2), lo, hi);
+          w[j] = e4m3x2(lo, hi);
+        }
+        *reinterpret_cast<uint2*>(out + (g + k * kLanes) * 8) = make_uint2(pack_h2(w[0], w[1]), pack_h2(w[2], w[3]));
       }
-      continue;
-    }
-    uint4 o[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      o[k] = is_v ? x[i][k]
-                  : make_uint4(bf16x2(f[k][0], f[k][1]), bf16x2(f[k][2], f[k][3]), bf16x2(f[k][4], f[k][5]),
-                               bf16x2(f[k][6], f[k][7]));
-    uint16_t* dst;
-    if (is_q) {
-      dst = a.q_out + t * a.ost + r * a.osh;
-      if (!placed) o[0] = o[1] = make_uint4(0, 0, 0, 0);
     } else {
-      if (!placed) continue;
-      dst = reinterpret_cast<uint16_t*>(is_v ? v_at + (r - a.hq - a.hkv) * a.vh : k_at + (r - a.hq) * a.kh);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float lo, hi;
+          f2_unpack(f[k][j], lo, hi);
+          w[j] = bf16x2(lo, hi);
+        }
+        *reinterpret_cast<uint4*>(out + (g + k * kLanes) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
-    *reinterpret_cast<uint4*>(dst + g * 8) = o[0];
-    *reinterpret_cast<uint4*>(dst + g * 8 + D / 2) = o[1];
   }
 }
 
 template <int D, bool kE4M3, int kSteps>
 cudaError_t launch_steps(const PagedAppendArgs& a, cudaStream_t s) {
-  constexpr int kRows = kSteps * 32 / (D / 16);
-  const int64_t segs = (a.hq + 2 * a.hkv + kRows - 1) / kRows, units = segs * a.b.n_tokens;
-  paged_append_kernel<D, kE4M3, kSteps><<<static_cast<unsigned>((units + 7) / 8), 256, 0, s>>>(a, static_cast<uint32_t>(segs));
+  constexpr uint32_t kRows = kSteps * 512 / D;
+  const AppendSegs segs{(a.hq + kRows - 1) / kRows, (a.hkv + kRows - 1) / kRows};
+  const int64_t units = static_cast<int64_t>(segs.q + 2 * segs.kv) * a.b.n_tokens;
+  paged_append_kernel<D, kE4M3, kSteps><<<static_cast<unsigned>((units + 7) / 8), 256, 0, s>>>(a, segs);
   return cudaGetLastError();
 }
 
@@ -182,9 +231,13 @@ cudaError_t launch_t(const PagedAppendArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   constexpr int kPer = 512 / D;                             // rows of a step
   const int64_t rows = a.hq + 2 * a.hkv;
-  if (rows * a.b.n_tokens < int64_t(sms) * 24 * kPer) return launch_steps<D, kE4M3, 1>(a, s);
-  const int64_t lanes2 = (rows + 2 * kPer - 1) / (2 * kPer) * 2, lanes3 = (rows + 3 * kPer - 1) / (3 * kPer) * 3;
-  return lanes3 <= lanes2 + lanes2 / 8 ? launch_steps<D, kE4M3, 3>(a, s) : launch_steps<D, kE4M3, 2>(a, s);
+  if (rows * a.b.n_tokens < int64_t(sms) * 32 * kPer) return launch_steps<D, kE4M3, 1>(a, s);
+  // The rows that the warps' runs cover, idle ones included.
+  auto covered = [&](int steps) {
+    const int64_t run = int64_t(steps) * kPer;
+    return (a.hq + run - 1) / run * run + 2 * ((a.hkv + run - 1) / run * run);
+  };
+  return covered(3) < covered(2) ? launch_steps<D, kE4M3, 3>(a, s) : launch_steps<D, kE4M3, 2>(a, s);
 }
 
 }  // namespace
