@@ -202,9 +202,12 @@ __device__ __forceinline__ uint32_t vdesc_lo(uint32_t saddr) {
   return ((saddr & 0x3FFFFu) >> 4) | ((128u * 128u >> 4) << 16);
 }
 
+// Descriptors are added up at each instruction: kept in registers from step to step they spilled (window_e4m3 189 ->
+// 182 us, 2048 rows over 8192 E4M3 keys of 16 heads 133 -> 120).
 template <int D, bool kE4M3>
 __device__ __forceinline__ void issue_qk(uint32_t s_tmem, uint32_t ql, uint32_t kl) {
   constexpr uint32_t idesc = idesc_f32acc(kBM, kBN) | (kE4M3 ? 0u : kIdescBf16);
+  asm volatile("" : "+r"(s_tmem), "+r"(ql), "+r"(kl));
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
     const uint32_t off = ((kk >> 2) * ChunkCfg<D, kE4M3>::kPanelBytes + (kk & 3) * 32) >> 4;
@@ -215,6 +218,7 @@ __device__ __forceinline__ void issue_qk(uint32_t s_tmem, uint32_t ql, uint32_t 
 template <int D, bool kE4M3>
 __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint32_t vl, bool first) {
   constexpr uint32_t idesc = idesc_f32acc(kBM, D) | kIdescBmn | (kE4M3 ? 0u : kIdescBf16);
+  asm volatile("" : "+r"(o_tmem), "+r"(p_tmem), "+r"(vl));
 #pragma unroll
   for (int kk = 0; kk < kBN / 16; ++kk)
     mma_f16_ts(o_tmem, p_tmem + kk * 8, sdesc_of_lo(vl + kk * (2048 >> 4)), idesc, (first && kk == 0) ? 0u : 1u);
