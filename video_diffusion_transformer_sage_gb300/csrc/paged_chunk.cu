@@ -3,7 +3,7 @@
 //
 // A unit is (sequence, K/V head, 256 query rows): the rows of a K/V head are the sequence's new tokens
 // times the query heads that share it, so grouped heads fill the 128-row tiles and every K and V
-// tile that is loaded serves all of them.  Two 128-row tiles t = 0, 1 per CTA and 128-key tiles:
+// tile that is loaded serves all of them.  Two 128-row tiles t = 0, 1 per unit and 128-key tiles:
 //   S_t = Q_t K^T    tcgen05.mma 128 x 128 x 16, fp32 in tensor memory
 //   online softmax   one thread per row: fp32 maximum and sum; P_t in 16 bits over S_t's columns
 //                    (its own columns at D = 64)
@@ -19,12 +19,18 @@
 // E4M3 cache: the codes come by TMA into a staging tile and one warpgroup widens them to fp16 (exact) in
 // the swizzled tiles; Q is held as fp16 times a power of two per row and P as fp16.
 //
-// Warp roles: warp 0 (and 3) page table and TMA, warp 1 MMA issue (one thread), warp 2 tensor memory; warps 4-7 and
-// 8-11 softmax and epilogue of tile 0 and 1; with E4M3 warps 12-15 widen.  Every wait is bounded.
+// One CTA per SM works through the items (units, or shares of a unit's keys), drawn from a counter; the pipeline does
+// not drain between them: the next unit's Q, K and V are loaded and its first S formed while O of the last one leaves.
+// Against a CTA per item, whose start and end take 7.6 us of a unit: prompts_causal 371 -> 345 us, window_e4m3
+// 180 -> 168, 2048 rows over 16384 bf16 keys of 16 heads 207 -> 201; a call of one short unit per SM takes 0.8 us
+// more (13.2 -> 14.0).
 //
-// What bounds it: 4 rows keys D FLOPs at the 16-bit tensor rate (for few rows the cache's bytes).  The key axis
-// is split over several CTAs for the units that do not fill the SMs a last time; each then leaves (maximum, sum, O) in the
-// workspace, and paged_join_kernel adds the parts in the order of their keys.
+// Warp roles: warp 0 (and 3) page table and TMA, warp 1 MMA issue (one thread), warp 2 draws the items and finds their
+// units; warps 4-7 and 8-11 softmax and epilogue of tile 0 and 1; with E4M3 warps 12-15 widen.  Every wait is bounded.
+//
+// What bounds it: 4 rows keys D FLOPs at the 16-bit tensor rate (for few rows the cache's bytes), and the softmax warps,
+// which take about as long: D = 64 has half the FLOPs for the same exponentials.  The key axis is split over several
+// items for the units that do not fill the SMs a last time; each then leaves (maximum, sum, O) in the workspace, and paged_join_kernel adds the parts in the order of their keys.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -39,6 +45,7 @@ namespace {
 
 constexpr int kBM = 128, kBN = 128;
 constexpr uint64_t kChunkWaitNs = 2000000000ull;
+constexpr int kItemWaits = 64;   // such waits for all of an item's key tiles
 constexpr float kRise = 8.0f;   // log2 of how far a maximum may fall behind before O is rescaled
 
 template <int D, bool kE4M3>
@@ -49,10 +56,7 @@ struct ChunkCfg {
   static constexpr int kQTileBytes = kBM * D * 2;
   static constexpr int kTileBytes = kBN * D * 2;              // a K or V tile in 16 bits
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = D == 128 ? 2 : 4;            // with two row tiles
-  // With one row tile the second Q tile's shared memory holds another stage (D = 128, bf16).
-  static constexpr int kStages1 = D == 128 ? (kE4M3 ? 2 : 3) : 4;
-  static constexpr int kMaxStages = kStages1;
+  static constexpr int kStages = D == 128 ? 2 : 4;
   // K and V of a tile have barriers of their own where the ring is short (D = 128): a K stage is free again once
   // Q K^T has read it, a softmax before P V is done with V (chunk_frames 2358 -> 2236 us).  The four stages at
   // D = 64 hide the loads anyway, and there the extra waits of the issuing thread cost 5 %.
@@ -63,29 +67,35 @@ struct ChunkCfg {
   static constexpr int kColO0 = 256;
   static constexpr bool kSepP = D == 64;
   static constexpr int kColP0 = kSepP ? 384 : 0, kStepP = kSepP ? 64 : 128;
-  static constexpr int kKvOff = 2 * kQTileBytes, kKvOff1 = kStages1 > kStages ? kQTileBytes : kKvOff;
-  static constexpr int kKvEnd = kKvOff + kStages * kStageBytes > kKvOff1 + kStages1 * kStageBytes
-                                    ? kKvOff + kStages * kStageBytes : kKvOff1 + kStages1 * kStageBytes;
-  static constexpr int kRawOff = kKvEnd;
-  static constexpr int kExpOff = kRawOff + kRawBytes;         // 2^e of each Q row (E4M3)
-  static constexpr int kBarOff = kExpOff + (kE4M3 ? 1024 : 0);
-  // q_full, k_full[S], v_full[S], k_empty[S], v_empty[S], s_full[2], p_full[2], pv_done[2], s_free[2], mma_final,
-  // raw_full[2] (K, V), raw_empty[2]
-  static constexpr int kNumBars = 1 + 4 * kMaxStages + 8 + 5;
+  // K and V with barriers of their own, and the two staging tiles, have a loading warp each: pages of 16 tokens are 32
+  // copies a tile.
+  static constexpr bool kTwoLoaders = kSplitKV || kE4M3;
+  // Results leave through 16 KB of shared memory per slot while the next unit's Q is loaded; with E4M3 at D = 128 there
+  // is no room for both, and they leave through the slot's Q tile first.
+  static constexpr bool kEarlyQ = !(kE4M3 && D == 128);
+  static constexpr int kKvOff = 2 * kQTileBytes;
+  static constexpr int kRawOff = kKvOff + kStages * kStageBytes;
+  static constexpr int kOutOff = kRawOff + kRawBytes;
+  static constexpr int kExpOff = kOutOff + (kEarlyQ ? 2 * 16384 : 0);   // biased exponent of each Q row (E4M3)
+  static constexpr int kBarOff = kExpOff + (kE4M3 ? 256 : 0);
+  // q_full[2], k_full[S], v_full[S], k_empty[S], v_empty[S], s_full[2], p_full[2], pv_done[2], s_free[2], o_free[2],
+  // ml_full, ml_empty, mma_final, raw_full[2] (K, V), raw_empty[2], unit_full[2], unit_empty[2], draw
+  static constexpr int kNumBars = 4 * kStages + 24;
   static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;
   // Registers a thread: launched at 168 (384 threads) or 128 (512).
   static constexpr int kRegsRoles = kE4M3 ? 56 : 72, kRegsSoftmax = kE4M3 ? 192 : 216, kRegsWiden = 72;
   static_assert(128 * kRegsRoles + 256 * kRegsSoftmax + (kE4M3 ? 128 * kRegsWiden : 0) <= (kE4M3 ? 512 * 128 : 384 * 168),
                 "register split exceeds launch");
-  static_assert(kSmem <= 232448 - 256, "shared memory");
+  static_assert(kSmem <= 232448 - 1408, "shared memory");
 };
 
 struct ChunkParams {
   PagedAttnArgs a;
   int group;
   int box_shift;   // log2 of the slots per TMA box (a page, or 128)
-  int whole;       // units below this number are one CTA's; each of the rest is `splits` CTAs'
+  int whole;       // units below this number are one item; each of the rest is `splits` items
   int splits;
+  uint32_t items;
 };
 
 __device__ __forceinline__ void record_timeout(int32_t* status, int32_t where, volatile int* abort_flag) {
@@ -109,9 +119,12 @@ struct Unit {
   int b, h;
   int start, n_new, len;    // first row of q, new tokens, tokens in the cache
   int row0, rows;           // first row (token x group) of the unit, rows it has (at most 256)
-  int t0, nt;               // its key tiles (this CTA's share of them)
+  int t0, nt;               // its key tiles (the item's share of them); nt < 0: no more items
   int ulo, uhi;             // keys that some row sees
-  int slot;                 // of its partial result; -1: the unit is one CTA's
+  int slot;                 // of its partial result; -1: the unit is one item
+  // For the softmax: keys that every row of tile t sees; this CTA's key tiles, slot t's and units of one row tile so far.
+  int alo[2], ahi[2];
+  uint32_t ct, mine[2], ones;
 };
 
 __device__ __forceinline__ void token_keys(const PagedAttnArgs& a, int len, int n_new, int j, int& lo, int& hi) {
@@ -203,7 +216,7 @@ __device__ __forceinline__ uint32_t vdesc_lo(uint32_t saddr) {
 }
 
 // Descriptors are added up at each instruction: kept in registers from step to step they spilled (window_e4m3 189 ->
-// 182 us, 2048 rows over 8192 E4M3 keys of 16 heads 133 -> 120).
+// 181 us, 2048 rows over 8192 E4M3 keys of 16 heads 133 -> 120).
 template <int D, bool kE4M3>
 __device__ __forceinline__ void issue_qk(uint32_t s_tmem, uint32_t ql, uint32_t kl) {
   constexpr uint32_t idesc = idesc_f32acc(kBM, kBN) | (kE4M3 ? 0u : kIdescBf16);
@@ -350,110 +363,248 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 
 // What the roles of a CTA share.
 struct ChunkShared {
-  Unit unit;
+  Unit unit[2];                    // the items in work and next
   int skip;
   volatile int abort;
   uint32_t bits[8], raw_bits[2];   // boxes loaded: of the last key tiles, and of the staging K and V tile
   uint32_t tmem;
+  float2 ml[128];                  // slot 1's maxima and sums (units of one row tile)
 };
 
-// The roles of one CTA on its unit.  kOne: at most 128 rows, key tile j is slot j & 1's; otherwise both slots
-// (row tiles) take every key tile.
-template <int D, bool kE4M3, bool kOne>
-__device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUtensorMap& vmap, const ChunkParams& p,
-                                            ChunkShared& sh, uint8_t* smem) {
+template <int T>
+struct Slot {   // a row tile's number, as a constant
+  static constexpr int v = T;
+};
+
+template <int D, bool kE4M3>
+__global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                       const __grid_constant__ ChunkParams p) {
   using C = ChunkCfg<D, kE4M3>;
-  constexpr int kStages = kOne ? C::kStages1 : C::kStages;
-  // K and V with barriers of their own have a loading warp each: pages of 16 tokens are 32 copies a tile.
-  constexpr bool kTwoLoaders = C::kSplitKV || kE4M3;
-  const PagedAttnArgs& a = p.a;
-  const Unit& u = sh.unit;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ ChunkShared sh;
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sQ = smem;
-  uint8_t* sKV = smem + (kOne ? C::kKvOff1 : C::kKvOff);
+  uint8_t* sKV = smem + C::kKvOff;
+  uint8_t* q_exp = smem + C::kExpOff;
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-  uint64_t* k_full = q_full + 1;
-  uint64_t* v_full = k_full + C::kMaxStages;
-  uint64_t* k_empty = v_full + C::kMaxStages;
-  uint64_t* v_empty = k_empty + C::kMaxStages;
-  uint64_t* s_full = v_empty + C::kMaxStages;
+  uint64_t* k_full = q_full + 2;
+  uint64_t* v_full = k_full + S;
+  uint64_t* k_empty = v_full + S;
+  uint64_t* v_empty = k_empty + S;
+  uint64_t* s_full = v_empty + S;
   uint64_t* p_full = s_full + 2;
   uint64_t* pv_done = p_full + 2;
   uint64_t* s_free = pv_done + 2;
-  uint64_t* mma_final = s_free + 2;
+  uint64_t* o_free = s_free + 2;
+  uint64_t* ml_full = o_free + 2;
+  uint64_t* ml_empty = ml_full + 1;
+  uint64_t* mma_final = ml_empty + 1;
   uint64_t* raw_full = mma_final + 1;
   uint64_t* raw_empty = raw_full + 2;
+  uint64_t* unit_full = raw_empty + 2;
+  uint64_t* unit_empty = unit_full + 2;
+  uint64_t* draw = unit_empty + 2;
+  const PagedAttnArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ntiles = u.nt, boxes = kBN >> p.box_shift;
+
+  if (threadIdx.x == 0) {
+    sh.skip = *reinterpret_cast<volatile int32_t*>(a.status) == kStatusTimeout;
+    sh.abort = 0;
+    for (int i = 0; i < 2 * S; ++i) mbar_init(k_full + i, kE4M3 ? 128 : 1);        // and v_full
+    for (int i = 0; i < 2 * S; ++i) mbar_init(k_empty + i, 1);                     // and v_empty
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + i, 128);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 128);
+      mbar_init(pv_done + i, 1);
+      mbar_init(s_free + i, 4);
+      mbar_init(o_free + i, 128);
+      mbar_init(raw_full + i, 1);
+      mbar_init(raw_empty + i, 128);
+      mbar_init(unit_full + i, 1);
+      // The loading warps, the issuing thread, the softmax and the widening warps.
+      mbar_init(unit_empty + i, (C::kTwoLoaders ? 2 : 1) + 1 + 8 + (kE4M3 ? 4 : 0));
+    }
+    mbar_init(ml_full, 128);
+    mbar_init(ml_empty, 128);
+    mbar_init(mma_final, 1);
+    mbar_init(draw, 1);
+    fence_mbar_init();
+  }
+  // Warp 2 finds an item's unit and its share of the unit's key tiles (which may be empty when there are few).
+  auto take = [&](uint32_t item, Unit& u) {
+    const bool split = item >= static_cast<uint32_t>(p.whole);
+    const int rest = static_cast<int>(item) - p.whole;
+    if (!find_unit(a, p.group, split ? p.whole + rest / p.splits : static_cast<int>(item), u)) return false;
+    if (lane == 0 && __ldg(a.b.kv_len + u.b) > a.b.cap) record_bad_index(a.status, kWhereLength);
+    u.slot = -1;
+    if (split) {
+      const int per = (u.nt + p.splits - 1) / p.splits, from = min(u.nt, per * (rest % p.splits));
+      u.t0 += from;
+      u.nt = min(per, u.nt - from);
+      u.slot = rest;
+    }
+    if (u.nt > 0) {
+      for (int t = 0; t < 2; ++t) {
+        int unused;
+        const int from = u.rows > 128 ? t * 128 : 0, last = min(u.rows, from + 128) - 1;
+        token_keys(a, u.len, u.n_new, (u.row0 + from) / p.group, unused, u.ahi[t]);
+        token_keys(a, u.len, u.n_new, (u.row0 + last) / p.group, u.alo[t], unused);
+      }
+      return true;
+    }
+    for (int r = lane; r < u.rows; r += 32) a.part_ml[u.slot * kPagedChunkRows + r] = make_float2(-INFINITY, 0.0f);
+    return false;
+  };
+  Unit u{};
+  bool have = false, first = true;
+  // Item k for the other roles, with the CTA's counts up to it.
+  auto publish = [&](int k, bool end) {
+    if (end) u.nt = -1;
+    if (lane == 0) {
+      sh.unit[k & 1] = u;
+      mbar_arrive(unit_full + (k & 1));
+    }
+    __syncwarp();
+    u.ct += u.nt;
+    u.ones += u.rows <= 128;
+    for (int t = 0; t < 2; ++t) u.mine[t] += u.rows > 128 ? u.nt : (u.nt + 1 - t) / 2;
+  };
+  if (warp == 2) have = take(blockIdx.x, u);
+  __syncthreads();
+  if (sh.skip) return;   // an earlier wait ran out: no work until the status has been read
+  if (warp == 2 && have) publish(0, false);
+  if (warp == 3) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  const int boxes = kBN >> p.box_shift;
+  // A bounded wait by a whole warp; records the first timeout.  False once anything timed out.
+  auto wait = [&](uint64_t* bar, uint32_t parity, int where) {
+    if (warp_wait(bar, parity)) return true;
+    if (lane == 0) record_timeout(a.status, where, &sh.abort);
+    __syncwarp();
+    return false;
+  };
+  // Item k's entry has been copied by the whole warp and may be replaced.
+  auto release_unit = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(unit_empty + (k & 1));
+  };
 
   if (warp < 4) {
     regs_dec<C::kRegsRoles>();
-    if (warp == 0 || (kTwoLoaders && warp == 3)) {
-      // ------------------------------------------------------------ page table and TMA
-      const int kv0 = warp == 0 ? 0 : 1, kv1 = kTwoLoaders && warp == 0 ? 1 : 2;   // K, V or both
-      tma_prefetch_desc(&kmap);
-      tma_prefetch_desc(&vmap);
-      if (warp == 0 && lane == 0 && __ldg(a.b.kv_len + u.b) > a.b.cap) record_bad_index(a.status, kWhereLength);
-      const int box = 1 << p.box_shift;
-      const uint32_t box_bytes = static_cast<uint32_t>(box) * D * (kE4M3 ? 1 : 2);
-      const int32_t* row = a.b.table + u.b * a.b.table_stride;
-      const int h = u.h, t0 = u.t0, ulo = u.ulo, uhi = u.uhi;
-      bool ok = true;
-      int j = 0, kv = 0;
-      for (; j < ntiles && ok; ++j) {
-        const int key0 = (t0 + j) * kBN + (lane << p.box_shift);
-        const bool need = lane < boxes && key0 < uhi && key0 + box > ulo;
-        int page = -1;
-        if (need) page = __ldg(row + (key0 >> a.b.page_shift));
-        const bool good = need && page >= 0 && page < a.b.n_pages;
-        if (need && !good) record_bad_index(a.status, kWherePage);
-        const uint32_t bits = __ballot_sync(0xffffffffu, good);
-        const int slot_in_page = key0 & ((1 << a.b.page_shift) - 1);
-        const int s = j % kStages;
-        for (kv = kv0; kv < kv1; ++kv) {
-          const CUtensorMap* map = kv ? &vmap : &kmap;
-          const bool own_bar = C::kSplitKV || kv == 0;   // V shares K's barriers otherwise
-          uint64_t* full = kE4M3 ? raw_full + kv : (kv && own_bar ? v_full : k_full) + s;
-          if (kE4M3) {
-            if (j >= 1) ok = warp_wait(raw_empty + kv, (j - 1) & 1);
-          } else if (own_bar && j >= kStages) {
-            ok = warp_wait((kv || !C::kSplitKV ? v_empty : k_empty) + s, (j / kStages - 1) & 1);
-          }
-          if (!ok) record_timeout(a.status, kWherePagedEmpty, &sh.abort);
-          ok = !__any_sync(0xffffffffu, !ok || sh.abort);
-          if (!ok) break;
-          if (lane == 0) {
-            if (kE4M3) sh.raw_bits[kv] = bits;
-            else if (kv == 0) sh.bits[j % (2 * kStages)] = bits;
-            if (kE4M3 || own_bar)
-              mbar_arrive_expect_tx(full, __popc(bits) * box_bytes * (kE4M3 || C::kSplitKV ? 1u : 2u));
-          }
-          __syncwarp();
-          if (good) {
-            if (kE4M3) {
-              tma_load_4d(smem_u32(smem + C::kRawOff) + kv * C::kRawTile + (lane << p.box_shift) * D, map, full, 0, h,
-                          slot_in_page, page);
-            } else {
-              const uint32_t dst = smem_u32(sKV + s * C::kStageBytes) + kv * C::kTileBytes + (lane << p.box_shift) * 128;
-#pragma unroll
-              for (int pn = 0; pn < C::kPanels; ++pn)
-                tma_load_4d(dst + pn * C::kPanelBytes, map, full, pn * 64, h, slot_in_page, page);
-            }
+    if (warp == 2) {
+      // ------------------------------------------------------------ items, one ahead
+      uint32_t item = blockIdx.x;
+      for (int k = have ? 1 : 0;;) {
+        const bool end = item >= p.items;
+        if (!first) {
+          have = !end && take(item, u);
+          if (have || end) {
+            if (k >= 2 && !wait(unit_empty + (k & 1), ((k >> 1) - 1) & 1, kWherePagedEmpty)) break;
+            publish(k++, end);
           }
         }
+        first = false;
+        if (end || __any_sync(0xffffffffu, sh.abort)) break;
+        // The next item is drawn when the loads of this one are about to end: late enough that a CTA with a long item
+        // holds no other, early enough that finding the unit costs no time.
+        if (p.items <= gridDim.x) {
+          item = p.items;
+          continue;
+        }
+        if (have) {
+          bool ready = false;
+          for (int n = 0; n < kItemWaits && !ready && !sh.abort; ++n) ready = warp_wait(draw, (k - 1) & 1);
+          if (!ready) {
+            if (lane == 0) record_timeout(a.status, kWherePagedEmpty, &sh.abort);
+            __syncwarp();
+            break;
+          }
+        }
+        // Items are handed out one by one; whoever draws the last number, past the end, resets the counter.
+        uint32_t drawn = 0;
+        if (lane == 0) {
+          drawn = static_cast<uint32_t>(atomicAdd(a.counters + 2 * kPagedMaxCtas, 1));
+          if (drawn == p.items - 1) a.counters[2 * kPagedMaxCtas] = 0;
+        }
+        item = gridDim.x + __shfl_sync(0xffffffffu, drawn, 0);
+      }
+    } else if (warp == 0 || (C::kTwoLoaders && warp == 3)) {
+      // ------------------------------------------------------------ page table and TMA
+      const int kv0 = warp == 0 ? 0 : 1, kv1 = C::kTwoLoaders && warp == 0 ? 1 : 2;   // K, V or both
+      tma_prefetch_desc(&kmap);
+      tma_prefetch_desc(&vmap);
+      const int box = 1 << p.box_shift;
+      const uint32_t box_bytes = static_cast<uint32_t>(box) * D * (kE4M3 ? 1 : 2);
+      uint32_t ct = 0, issued = 0;   // tiles so far; those whose copies were issued (of K, or of this warp's)
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        ok = wait(unit_full + (k & 1), (k >> 1) & 1, kWherePagedEmpty);
         if (!ok) break;
+        const Unit& e = sh.unit[k & 1];
+        const int ntiles = e.nt, h = e.h, ulo = e.ulo, uhi = e.uhi, key00 = e.t0 * kBN + (lane << p.box_shift);
+        const int32_t* row = a.b.table + e.b * a.b.table_stride;
+        release_unit(k);
+        if (ntiles < 0) break;
+        for (int j = 0; j < ntiles && ok; ++j, ++ct) {
+          const int key0 = key00 + j * kBN;
+          if (warp == 0 && lane == 0 && j == max(0, ntiles - 3)) mbar_arrive(draw);
+          const bool need = lane < boxes && key0 < uhi && key0 + box > ulo;
+          int page = -1;
+          if (need) page = __ldg(row + (key0 >> a.b.page_shift));
+          const bool good = need && page >= 0 && page < a.b.n_pages;
+          if (need && !good) record_bad_index(a.status, kWherePage);
+          const uint32_t bits = __ballot_sync(0xffffffffu, good);
+          const int slot_in_page = key0 & ((1 << a.b.page_shift) - 1);
+          const uint32_t s = ct % S;
+          for (int kv = kv0; kv < kv1; ++kv) {
+            const CUtensorMap* map = kv ? &vmap : &kmap;
+            const bool own_bar = C::kSplitKV || kv == 0;   // V shares K's barriers otherwise
+            uint64_t* full = kE4M3 ? raw_full + kv : (kv && own_bar ? v_full : k_full) + s;
+            if (kE4M3) {
+              if (ct >= 1) ok = wait(raw_empty + kv, (ct - 1) & 1, kWherePagedEmpty);
+            } else if (own_bar && ct >= S) {
+              ok = wait((kv || !C::kSplitKV ? v_empty : k_empty) + s, (ct / S - 1) & 1, kWherePagedEmpty);
+            }
+            ok = !__any_sync(0xffffffffu, !ok || sh.abort);
+            if (!ok) break;
+            if (lane == 0) {
+              if (kE4M3) sh.raw_bits[kv] = bits;
+              else if (kv == 0) sh.bits[ct % (2 * S)] = bits;
+              if (kE4M3 || own_bar)
+                mbar_arrive_expect_tx(full, __popc(bits) * box_bytes * (kE4M3 || C::kSplitKV ? 1u : 2u));
+            }
+            __syncwarp();
+            if (good) {
+              if (kE4M3) {
+                tma_load_4d(smem_u32(smem + C::kRawOff) + kv * C::kRawTile + (lane << p.box_shift) * D, map, full, 0, h,
+                            slot_in_page, page);
+              } else {
+                const uint32_t dst = smem_u32(sKV + s * C::kStageBytes) + kv * C::kTileBytes + (lane << p.box_shift) * 128;
+#pragma unroll
+                for (int pn = 0; pn < C::kPanels; ++pn)
+                  tma_load_4d(dst + pn * C::kPanelBytes, map, full, pn * 64, h, slot_in_page, page);
+              }
+            }
+            issued = ct + 1;
+          }
+        }
       }
       if (!ok) {
-        // After a timeout: the copies issued have landed before the CTA ends (tiles up to j, and K of tile j where this
-        // warp loads both and gave up at V).
-        const int nk = kv0 == 0 ? j + (kv > 0 ? 1 : 0) : 0, nv = kv1 == 2 ? j : 0;
+        // After a timeout: the copies issued have landed before the CTA ends.
         if (kE4M3) {
-          if (nk > 0) mbar_wait(raw_full, (nk - 1) & 1, kChunkWaitNs);
-          if (nv > 0) mbar_wait(raw_full + 1, (nv - 1) & 1, kChunkWaitNs);
+          if (issued > 0) mbar_wait(raw_full + kv0, (issued - 1) & 1, kChunkWaitNs);
         } else {
-          for (int i = max(0, nk - kStages); i < nk; ++i) mbar_wait(k_full + i % kStages, (i / kStages) & 1, kChunkWaitNs);
-          for (int i = max(0, nv - kStages); C::kSplitKV && i < nv; ++i)
-            mbar_wait(v_full + i % kStages, (i / kStages) & 1, kChunkWaitNs);
+          for (uint32_t i = issued > S ? issued - S : 0; i < issued; ++i)
+            mbar_wait((kv0 ? v_full : k_full) + i % S, (i / S) & 1, kChunkWaitNs);
         }
       }
     } else if (warp == 1 && lane == 0) {
@@ -462,111 +613,144 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
       const uint32_t q_lo = sdesc_lo(smem_u32(sQ)), k_lo = sdesc_lo(smem_u32(sKV)),
                      v_lo = vdesc_lo(smem_u32(sKV) + C::kTileBytes);
       constexpr uint32_t kQLo = C::kQTileBytes >> 4, kStageLo = C::kStageBytes >> 4;
-      bool ok = mbar_wait(q_full, 0, kChunkWaitNs);
-      // The ring stage and phase of the next K tile and of the next V tile.
+      // The ring stage and phase of the next K tile and of the next V tile; per slot the S, P V, units and Q tiles so
+      // far.
       int sk = 0, sv = 0;
-      uint32_t phk = 0, phv = 0;
+      uint32_t phk = 0, phv = 0, ns[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0}, nq[2] = {0, 0};
+      bool ok = true;
+      auto mwait = [&](uint64_t* x, uint32_t parity) { return mbar_wait(x, parity, kChunkWaitNs); };
       auto step_k = [&]() {
         if (C::kSplitKV) tc_commit(k_empty + sk);
-        if (++sk == kStages) {
+        if (++sk == S) {
           sk = 0;
           phk ^= 1u;
         }
       };
       auto step_v = [&]() {
         tc_commit(v_empty + sv);
-        if (++sv == kStages) {
+        if (++sv == S) {
           sv = 0;
           phv ^= 1u;
         }
       };
-      auto v_ready = [&]() { return !C::kSplitKV || mbar_wait(v_full + sv, phv, kChunkWaitNs); };
-      auto qk = [&](int t) {
-        tc_fence_after();
-        issue_qk<D, kE4M3>(colS + t * kBN, q_lo + (kOne ? 0 : t * kQLo), k_lo + sk * kStageLo);
-        tc_commit(s_full + t);
+      auto k_ready = [&]() { return mwait(k_full + sk, phk); };
+      auto v_ready = [&]() { return !C::kSplitKV || mwait(v_full + sv, phv); };
+      // S of slot T from Q tile `tile` and the current K stage, once the slot's S columns are free: read, or (P in S's
+      // columns) its last P V done.
+      auto s_ready = [&](auto T) {
+        constexpr int t = decltype(T)::v;
+        return mwait((C::kSepP ? s_free : pv_done) + t, (ns[t] - 1) & 1);
       };
-      auto pv = [&](int t, bool first) {
+      auto qk = [&](auto T, int tile) {
+        constexpr int t = decltype(T)::v;
+        tc_fence_after();
+        issue_qk<D, kE4M3>(colS + t * kBN, q_lo + tile * kQLo, k_lo + sk * kStageLo);
+        tc_commit(s_full + t);
+        ++ns[t];
+      };
+      auto p_ready = [&](auto T) {
+        constexpr int t = decltype(T)::v;
+        return mwait(p_full + t, np[t] & 1);
+      };
+      auto pv = [&](auto T, bool first) {
+        constexpr int t = decltype(T)::v;
         tc_fence_after();
         issue_pv<D, kE4M3>(colO + t * D, colP + t * C::kStepP, v_lo + sv * kStageLo, first);
         tc_commit(pv_done + t);
+        ++np[t];
       };
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, kChunkWaitNs); };
-      if (kOne) {
-        for (int j = 0; j < 2 && j < ntiles && ok; ++j) {
-          ok = wait(k_full + sk, phk);
-          if (!ok) break;
-          qk(j);
+      // A unit's first S of a slot; its first P V waits until the last unit's O was read.
+      auto begin = [&](auto T, int tile) {
+        constexpr int t = decltype(T)::v;
+        if (ns[t] > 0 && !s_ready(T)) return false;
+        qk(T, tile);
+        return true;
+      };
+      auto o_ready = [&](auto T) {
+        constexpr int t = decltype(T)::v;
+        return no[t]++ == 0 || mwait(o_free + t, (no[t] - 2) & 1);
+      };
+      // One key tile of a unit of one row tile, in slot T.
+      auto one_tile = [&](auto T, bool first, bool more) {
+        if (C::kSepP && more) {
+          if (!k_ready() || !s_ready(T)) return false;
+          qk(T, 0);
           step_k();
         }
-        for (int j = 0; j < ntiles && ok; ++j) {
-          const int t = j & 1;
-          const uint32_t phase = (j >> 1) & 1;
-          const bool more = j + 2 < ntiles;
-          if (C::kSepP && more) {
-            // S_t of the slot's next tile as soon as S_t is read.
-            ok = wait(k_full + sk, phk) && wait(s_free + t, phase);
-            if (!ok) break;
-            qk(t);
-            step_k();
-          }
-          ok = wait(p_full + t, phase) && v_ready();
-          if (!ok) break;
-          pv(t, j < 2);
-          step_v();
-          if (!C::kSepP && more) {
-            // P_t lies in S_t's columns: the next S_t only once P_t.V is done.
-            ok = wait(k_full + sk, phk) && wait(pv_done + t, phase);
-            if (!ok) break;
-            qk(t);
-            step_k();
-          }
-        }
-      } else {
-        ok = ok && wait(k_full, 0);
-        if (ok) {
-          qk(0);
-          qk(1);
+        if (!p_ready(T) || !v_ready()) return false;
+        pv(T, first);
+        step_v();
+        if (!C::kSepP && more) {
+          if (!k_ready() || !s_ready(T)) return false;
+          qk(T, 0);
           step_k();
         }
-        for (int j = 0; j < ntiles && ok; ++j) {
-          const uint32_t phase = j & 1;
-          const bool more = j + 1 < ntiles;
-          if (C::kSepP) {
-            if (more) {
-              ok = wait(k_full + sk, phk) && wait(s_free, phase);
+        return true;
+      };
+      const Slot<0> s0;
+      const Slot<1> s1;
+      for (int k = 0; ok; ++k) {
+        ok = mwait(unit_full + (k & 1), (k >> 1) & 1);
+        if (!ok) break;
+        const int ntiles = sh.unit[k & 1].nt;
+        const bool one = sh.unit[k & 1].rows <= 128;
+        mbar_arrive(unit_empty + (k & 1));
+        if (ntiles < 0) break;
+        ok = k_ready() && mwait(q_full, nq[0]++ & 1) && begin(s0, 0);
+        if (one) {
+          if (ok) step_k();
+          if (ok && ntiles > 1) {
+            ok = k_ready() && begin(s1, 0);
+            if (ok) step_k();
+          }
+          ok = ok && o_ready(s0) && (ntiles == 1 || o_ready(s1));
+          for (int j = 0; j < ntiles && ok; j += 2) {
+            ok = one_tile(s0, j == 0, j + 2 < ntiles);
+            if (ok && j + 1 < ntiles) ok = one_tile(s1, j == 0, j + 3 < ntiles);
+          }
+        } else {
+          ok = ok && mwait(q_full + 1, nq[1]++ & 1) && begin(s1, 1);
+          if (ok) step_k();
+          ok = ok && o_ready(s0) && o_ready(s1);
+          for (int j = 0; j < ntiles && ok; ++j) {
+            const bool more = j + 1 < ntiles;
+            if (C::kSepP) {
+              // S of the next tile as soon as S is read, P V once P is written.
+              if (more) {
+                ok = k_ready() && s_ready(s0);
+                if (!ok) break;
+                qk(s0, 0);
+                ok = s_ready(s1);
+                if (!ok) break;
+                qk(s1, 1);
+                step_k();
+              }
+              ok = p_ready(s0) && v_ready();
               if (!ok) break;
-              qk(0);
-              ok = wait(s_free + 1, phase);
+              pv(s0, j == 0);
+              ok = p_ready(s1);
               if (!ok) break;
-              qk(1);
-              step_k();
-            }
-            ok = wait(p_full, phase) && v_ready();
-            if (!ok) break;
-            pv(0, j == 0);
-            ok = wait(p_full + 1, phase);
-            if (!ok) break;
-            pv(1, j == 0);
-            step_v();
-          } else {
-            ok = wait(p_full, phase) && v_ready();
-            if (!ok) break;
-            pv(0, j == 0);
-            if (more) {
-              ok = wait(k_full + sk, phk) && wait(pv_done, phase);
+              pv(s1, j == 0);
+              step_v();
+            } else {
+              ok = p_ready(s0) && v_ready();
               if (!ok) break;
-              qk(0);
-            }
-            ok = wait(p_full + 1, phase);
-            if (!ok) break;
-            pv(1, j == 0);
-            step_v();
-            if (more) {
-              ok = wait(pv_done + 1, phase);
+              pv(s0, j == 0);
+              if (more) {
+                ok = k_ready() && s_ready(s0);
+                if (!ok) break;
+                qk(s0, 0);
+              }
+              ok = p_ready(s1);
               if (!ok) break;
-              qk(1);
-              step_k();
+              pv(s1, j == 0);
+              step_v();
+              if (more) {
+                ok = s_ready(s1);
+                if (!ok) break;
+                qk(s1, 1);
+                step_k();
+              }
             }
           }
         }
@@ -582,61 +766,72 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
     const int r = threadIdx.x - 384;   // the key of the tile
     const uint32_t raw = smem_u32(smem + C::kRawOff) + r * D;
     const uint32_t rsw = D == 128 ? (r & 7) : ((r >> 1) & 3);
-    const int key_r = u.t0 * kBN + r, ulo = u.ulo, uhi = u.uhi;
-    for (int j = 0; j < ntiles; ++j) {
-      const int s = j % kStages;
-      uint8_t* tile = sKV + s * C::kStageBytes;
-      bool ok = true;
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        if (j >= kStages && (C::kSplitKV || kv == 0))
-          ok = warp_wait((kv || !C::kSplitKV ? v_empty : k_empty) + s, (j / kStages - 1) & 1);
-        ok = ok && warp_wait(raw_full + kv, j & 1);
-        if (!ok) record_timeout(a.status, kWherePagedFull, &sh.abort);
-        ok = !__any_sync(0xffffffffu, !ok || sh.abort);
-        if (!ok) break;
-        const uint32_t bits = sh.raw_bits[kv];
-        const int key = key_r + j * kBN;
-        // Keys that no row sees count as zeros, whatever their slots hold.
-        const bool live = ((bits >> (r >> p.box_shift)) & 1u) && key >= ulo && key < uhi;
-        uint4 v[D / 16];
-#pragma unroll
-        for (int ch = 0; ch < D / 16; ++ch)
-          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(v[ch].x), "=r"(v[ch].y), "=r"(v[ch].z), "=r"(v[ch].w)
-                       : "r"(raw + kv * C::kRawTile + ((ch ^ rsw) << 4)));
-        if (r == 0 && kv == 0) sh.bits[j % (2 * kStages)] = bits;
-#pragma unroll
-        for (int ch = 0; ch < D / 16; ++ch) {
-          const uint32_t w[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
-          uint32_t f[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f[2 * i]) : "h"(static_cast<uint16_t>(live ? w[i] : 0u)));
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f[2 * i + 1]) : "h"(static_cast<uint16_t>(live ? w[i] >> 16 : 0u)));
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int c8 = ch * 2 + i;   // 8-channel chunk of the 16-bit row
-            *reinterpret_cast<uint4*>(tile + kv * C::kTileBytes + (c8 >> 3) * C::kPanelBytes + r * 128 +
-                                      (((c8 & 7) ^ (r & 7)) << 4)) =
-                make_uint4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-          }
-        }
-        mbar_arrive(raw_empty + kv);
-        fence_proxy_async_smem();
-        if (C::kSplitKV || kv == 1) mbar_arrive((kv && C::kSplitKV ? v_full : k_full) + s);
-      }
+    uint32_t ct = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      ok = wait(unit_full + (k & 1), (k >> 1) & 1, kWherePagedEmpty);
       if (!ok) break;
+      const Unit& e = sh.unit[k & 1];
+      const int ntiles = e.nt, ulo = e.ulo, uhi = e.uhi, key_r = e.t0 * kBN + r;
+      release_unit(k);
+      if (ntiles < 0) break;
+      for (int j = 0; j < ntiles && ok; ++j, ++ct) {
+        const uint32_t s = ct % S;
+        uint8_t* tile = sKV + s * C::kStageBytes;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          if (ct >= S && (C::kSplitKV || kv == 0))
+            ok = warp_wait((kv || !C::kSplitKV ? v_empty : k_empty) + s, (ct / S - 1) & 1);
+          ok = ok && warp_wait(raw_full + kv, ct & 1);
+          if (!ok) record_timeout(a.status, kWherePagedFull, &sh.abort);
+          ok = !__any_sync(0xffffffffu, !ok || sh.abort);
+          if (!ok) break;
+          const uint32_t bits = sh.raw_bits[kv];
+          const int key = key_r + j * kBN;
+          // Keys that no row sees count as zeros, whatever their slots hold.
+          const bool live = ((bits >> (r >> p.box_shift)) & 1u) && key >= ulo && key < uhi;
+          uint4 v[D / 16];
+#pragma unroll
+          for (int ch = 0; ch < D / 16; ++ch)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(v[ch].x), "=r"(v[ch].y), "=r"(v[ch].z), "=r"(v[ch].w)
+                         : "r"(raw + kv * C::kRawTile + ((ch ^ rsw) << 4)));
+          mbar_arrive(raw_empty + kv);
+          if (r == 0 && kv == 0) sh.bits[ct % (2 * S)] = bits;
+#pragma unroll
+          for (int ch = 0; ch < D / 16; ++ch) {
+            const uint32_t w[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
+            uint32_t f[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f[2 * i]) : "h"(static_cast<uint16_t>(live ? w[i] : 0u)));
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f[2 * i + 1]) : "h"(static_cast<uint16_t>(live ? w[i] >> 16 : 0u)));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int c8 = ch * 2 + i;   // 8-channel chunk of the 16-bit row
+              *reinterpret_cast<uint4*>(tile + kv * C::kTileBytes + (c8 >> 3) * C::kPanelBytes + r * 128 +
+                                        (((c8 & 7) ^ (r & 7)) << 4)) =
+                  make_uint4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+            }
+          }
+          fence_proxy_async_smem();
+          if (C::kSplitKV || kv == 1) mbar_arrive((kv && C::kSplitKV ? v_full : k_full) + s);
+        }
+      }
     }
   } else {
     // -------------------------------------------------------------- softmax and epilogue
     regs_inc<C::kRegsSoftmax>();
     const int t = (warp - 4) >> 2, wq = warp & 3, r = wq * 32 + lane;
-    float* q_exp = reinterpret_cast<float*>(smem + C::kExpOff);
-    const int steps = kOne ? (ntiles + 1 - t) / 2 : ntiles;   // key tiles of this slot
-    if (!kOne || t == 0) {
-      // ---- Q: each warp its 32 rows.  Lane i finds row i (one division), the others get it by shuffle.
+    const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_base + t * kBN, tO = tmem + lane_base + C::kColO0 + t * D;
+    const uint32_t tP = tmem + lane_base + C::kColP0 + t * C::kStepP;
+    const uint32_t all_boxes = (1u << boxes) - 1u;   // at most 16
+    // Slot t's Q tile of a unit, each warp its 32 rows: started here (bf16), finished and announced when the unit begins.
+    auto load_q = [&](const Unit& u) {
+      if (t == 1 && u.rows <= 128) return;
+      // Lane i finds row i (one division), the others get it by shuffle; rows past the last are zeros.
       uint8_t* tile = sQ + t * C::kQTileBytes;
       const int my = t * 128 + wq * 32 + lane, my_row = u.row0 + my;
       const int64_t my_at = my < u.rows ? static_cast<int64_t>(u.start + my_row / p.group) * a.qst +
@@ -644,7 +839,7 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
                                         : -1;
       const uint16_t* q = a.q;
       if (!kE4M3) {
-        // 8 lanes to a row's 128 bytes; rows past the last are zeros.
+        // 8 lanes to a row's 128 bytes.
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int rr = wq * 32 + i * 4 + (lane >> 3), ch = lane & 7;
@@ -655,9 +850,9 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
           for (int pn = 0; pn < C::kPanels; ++pn)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                              smem_u32(tile + pn * C::kPanelBytes + rr * 128 + ((ch ^ (rr & 7)) << 4))),
-                         "l"(src + pn * 64), "r"(n));
+                         "l"(src + pn * 64), "r"(n)
+                         : "memory");
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
       } else {
         // fp16 times a power of two that brings the row's largest value into [1, 2): exact but for values
         // 2^-14 below it, which keep an absolute error of 2^-25 of the row's largest.  D/8 lanes a row.
@@ -671,8 +866,8 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           float mx = 0.0f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
+          for (int x = 0; x < 4; ++x)
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[x] << 16)), fabsf(__uint_as_float(w[x] & 0xFFFF0000u))));
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
           int e = static_cast<int>((__float_as_uint(mx) >> 23) & 255) - 127;
@@ -680,52 +875,54 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
           const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
           uint32_t f[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            f[k] = pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xFFFF0000u) * down);
+          for (int x = 0; x < 4; ++x)
+            f[x] = pack2<true>(__uint_as_float(w[x] << 16) * down, __uint_as_float(w[x] & 0xFFFF0000u) * down);
           *reinterpret_cast<uint4*>(tile + (c8 >> 3) * C::kPanelBytes + rr * 128 + (((c8 & 7) ^ (rr & 7)) << 4)) =
               make_uint4(f[0], f[1], f[2], f[3]);
-          if (c8 == 0) q_exp[t * 128 + rr] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+          if (c8 == 0) q_exp[t * 128 + rr] = static_cast<uint8_t>(127 + e);
         }
-        __syncwarp();
       }
+    };
+    auto announce_q = [&](const Unit& u) {
+      if (t == 1 && u.rows <= 128) return;
+      if (!kE4M3) asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
-      mbar_arrive(q_full);
-    }
-    {
-      const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
-      const uint32_t tS = tmem + lane_base + t * kBN, tO = tmem + lane_base + C::kColO0 + t * D;
-      const uint32_t tP = tmem + lane_base + C::kColP0 + t * C::kStepP;
-      // This row's visible keys, and those that all rows of the tile see.
-      const int first = kOne ? 0 : t * 128;   // the slot's first row
-      const int last = min(u.rows, first + 128) - 1, mine = min(first + r, last);
-      int klo, khi, alo, ahi, unused;
-      token_keys(a, u.len, u.n_new, (u.row0 + mine) / p.group, klo, khi);
-      token_keys(a, u.len, u.n_new, (u.row0 + first) / p.group, unused, ahi);
-      token_keys(a, u.len, u.n_new, (u.row0 + last) / p.group, alo, unused);
-      const uint32_t all = boxes == 32 ? ~0u : (1u << boxes) - 1u;
+      mbar_arrive(q_full + t);
+    };
+    // One unit, of one row tile or of two.  (Runtime, not two copies: with them window_e4m3 took 195 us instead of 168,
+    // a third of the stalls for instructions.)
+    auto work = [&](int k) -> bool {
+      const Unit& u = sh.unit[k & 1];
+      const bool one = u.rows <= 128;
+      bool ok = true;
+      const int ntiles = u.nt, first = one ? 0 : t * 128;   // the slot's first row
+      const int steps = one ? (ntiles + 1 - t) / 2 : ntiles;
+      int klo, khi;   // this row's visible keys
+      token_keys(a, u.len, u.n_new, (u.row0 + min(first + r, u.rows - 1)) / p.group, klo, khi);
+      const int alo = u.alo[t], ahi = u.ahi[t];
       float c = a.scale_log2;
       if (kE4M3) {
-        if (kOne && t == 1) warp_wait(q_full, 0);   // the other warpgroup wrote the exponents
-        c *= __ldg(a.k_scale + u.h) * q_exp[first + r];
+        // (In a unit of one row tile slot 0's warps wrote the exponents.)
+        if (one && t == 1) ok = wait(q_full, k & 1, kWherePagedFull);
+        else __syncwarp();
+        c *= __ldg(a.k_scale + u.h) * __uint_as_float(static_cast<uint32_t>(q_exp[first + r]) << 23);
       }
       float m = -INFINITY, l = 0.0f;
-      bool ok = true;
-      const int t0 = u.t0;
-      for (int i = 0; i < steps; ++i) {
-        if (!warp_wait(s_full + t, i & 1)) {
-          if (lane == 0) record_timeout(a.status, kWherePagedMma, &sh.abort);
-          ok = false;
-          break;
-        }
+      const int key_t0 = u.t0 * kBN;
+      const uint32_t ct = u.ct, mine = u.mine[t];
+      for (int i = 0; i < steps && ok; ++i) {
+        ok = wait(s_full + t, (mine + i) & 1, kWherePagedMma);
+        if (!ok) break;
         tc_fence_after();
-        const int j = kOne ? 2 * i + t : i, kb = (t0 + j) * kBN, s = j % kStages;
-        const uint32_t bits = sh.bits[j % (2 * kStages)];
-        const bool masked = kb < alo || kb + kBN > ahi || bits != all;
-        const bool stepped = softmax_step<D, kE4M3>(tS, tO, tP, c, masked, [&](uint32_t mask[4]) {
+        const int j = one ? 2 * i + t : i, kb = key_t0 + j * kBN;
+        const uint32_t bits = sh.bits[(ct + j) % (2 * S)];
+        const bool masked = kb < alo || kb + kBN > ahi || bits != all_boxes;
+        ok = softmax_step<D, kE4M3>(tS, tO, tP, c, masked, [&](uint32_t mask[4]) {
           if (!kE4M3) {
             // Keys that no row of the unit sees may hold anything: their V counts as 0.
+            const uint32_t s = (ct + j) % S;
             const int key = kb + r;
-            if (C::kSplitKV && !warp_wait(v_full + s, (j / kStages) & 1)) record_timeout(a.status, kWherePagedFull, &sh.abort);
+            if (C::kSplitKV) wait(v_full + s, ((ct + j) / S) & 1, kWherePagedFull);
             if (!(((bits >> (r >> p.box_shift)) & 1u) && key >= u.ulo && key < u.uhi)) {
               uint8_t* v = sKV + s * C::kStageBytes + C::kTileBytes + r * 128;
 #pragma unroll
@@ -736,44 +933,29 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
           }
 #pragma unroll
           for (int w = 0; w < 4; ++w) mask[w] = key_mask(w, klo - kb, khi - kb, bits, p.box_shift);
-        }, i == 0, m, l, s_free + t, pv_done + t, i);
-        if (!stepped) {
+          __syncwarp();
+        }, i == 0, m, l, s_free + t, pv_done + t, static_cast<int>(mine) + i);
+        if (!ok) {
           if (lane == 0) record_timeout(a.status, kWherePagedMma, &sh.abort);
-          ok = false;
           break;
         }
         tc_fence_before();
         mbar_arrive(p_full + t);
       }
-      if (ok && steps > 0 && !warp_wait(pv_done + t, (steps - 1) & 1)) {
-        if (lane == 0) record_timeout(a.status, kWherePagedMma, &sh.abort);
-        ok = false;
-      }
-      tc_fence_after();
-      float own = 1.0f, other = 0.0f;   // factors of slot 0's and slot 1's O (kOne)
-      if (kOne) {
-        // Slot 1's maximum, sum and O go to slot 0 through the K / V ring, which nothing reads any more once
-        // both slots are past their last P.V.  Both warpgroups meet both barriers whatever happened.
-        float4* xo = reinterpret_cast<float4*>(sKV) + r * (D / 4);
-        float2* xml = reinterpret_cast<float2*>(sKV + 128 * D * 4) + r;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (ok && steps > 0) ok = wait(pv_done + t, (mine + steps - 1) & 1, kWherePagedMma);
+      float own = 1.0f, other = 0.0f;   // factors of slot 0's and slot 1's O (one row tile)
+      if (one && ok) {
+        const uint32_t ones = u.ones;
+        // Slot 1's maxima and sums to slot 0's warps, which read its O themselves: the same lanes of tensor memory.
         if (t == 1) {
-          if (steps > 0)
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-              uint32_t o[32];
-              SAGE_TMEM_LD32(tO + c0, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                xo[(c0 / 4 + i) ^ (r & 7)] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                                         __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-            }
-          *xml = make_float2(m, l);
-        }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (t == 0) {
-          const float2 x = *xml;
+          if (ones > 0) ok = wait(ml_empty, (ones - 1) & 1, kWherePagedMma);
+          if (ok) sh.ml[r] = make_float2(m, l);
+          mbar_arrive(ml_full);
+        } else {
+          ok = wait(ml_full, ones & 1, kWherePagedMma) &&
+               (ntiles == 1 || wait(pv_done + 1, (u.mine[1] + ntiles / 2 - 1) & 1, kWherePagedMma));
+          const float2 x = sh.ml[r];
+          mbar_arrive(ml_empty);
           const float mm = fmaxf(m, x.x);
           // A slot that saw no key counts nothing.
           own = m == -INFINITY ? 0.0f : ex2_approx(m - mm);
@@ -782,150 +964,112 @@ __device__ __forceinline__ void chunk_roles(const CUtensorMap& kmap, const CUten
           m = mm;
         }
       }
-      if (ok && (!kOne || t == 0)) {
+      // The next unit's Q comes under this one's epilogue (every S that reads the slot's Q tile is done).
+      const Unit& next = sh.unit[(k + 1) & 1];
+      ok = ok && wait(unit_full + ((k + 1) & 1), ((k + 1) >> 1) & 1, kWherePagedEmpty);
+      const bool has_next = ok && next.nt >= 0;
+      if (C::kEarlyQ && has_next) {
+        load_q(next);
+        if (kE4M3 || (one && t == 1)) announce_q(next);
+      }
+      if (ok && (!one || t == 0)) {
+        tc_fence_after();
         const int ur = first + r;
-        const bool live = ur < u.rows;
+        const bool live = ur < u.rows, whole = u.slot < 0;
         const int row = u.row0 + (live ? ur : 0);
         const int tok = u.start + row / p.group, hd = u.h * p.group + row % p.group;
-        const bool whole = u.slot < 0;
         const float vs = kE4M3 ? __ldg(a.v_scale + u.h) : 1.0f;
         // A row that saw no key (l = 0) becomes 0.
         const float inv = whole ? (l > 0.0f ? vs / l : l) : 1.0f;
-        // The rows leave through the slot's Q tile, which no MMA reads any more: each thread writes its own row
-        // there, 2 D bytes at a time (bf16 rows, or half an fp32 row of a partial result), and the warp
-        // stores whole rows.  Storing 16 bytes of 32 rows at a time took 2.0 us of a unit, this 0.9.
-        constexpr int kRowChunks = D / 8;
-        uint8_t* stage = sQ + t * C::kQTileBytes + wq * 32 * (2 * D);
+        const float f0 = own * inv, f1 = other * inv;
         const int64_t o_at = static_cast<int64_t>(tok) * a.ost + static_cast<int64_t>(hd) * a.osh;
         float* part = whole ? nullptr : a.part_o + (static_cast<int64_t>(u.slot) * kPagedChunkRows + first + wq * 32) * D;
         const int rows_here = u.rows - first - wq * 32;   // of this warp's 32
         uint16_t* out = a.out;
-#pragma unroll 1
-        for (int half = 0; half < (whole ? 1 : 2); ++half) {
-          const int c_end = whole ? D : (half + 1) * (D / 2);
-#pragma unroll 1
-          for (int c0 = half * (D / 2); c0 < c_end; c0 += 32) {
-            uint32_t o[32];
-            __syncwarp();
-            SAGE_TMEM_LD32(tO + c0, o);
-            tmem_wait_ld();
-            if (kOne) {
-              const float4* xo = reinterpret_cast<const float4*>(sKV) + r * (D / 4);
+        // 32 channels of the row, times the factors.
+        auto channels = [&](int c0, uint32_t o[32]) {
+          __syncwarp();
+          SAGE_TMEM_LD32(tO + c0, o);
+          tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (ntiles > 1) x = xo[(c0 / 4 + i) ^ (r & 7)];
-                o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * own + x.x * other);
-                o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * own + x.y * other);
-                o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * own + x.z * other);
-                o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * own + x.w * other);
-              }
-            }
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
+          if (one && ntiles > 1) {
+            uint32_t x[32];
+            SAGE_TMEM_LD32(tO + D + c0, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(fmaf(__uint_as_float(x[i]), f1, __uint_as_float(o[i])));
+          }
+        };
+        // Rows leave 128 bytes at a time through shared memory (64 bf16 channels, or 32 of a partial result), so that a
+        // warp stores whole lines; storing 16 bytes of 32 rows at a time took 2.0 us of a unit.
+        uint8_t* stage = (C::kEarlyQ ? smem + C::kOutOff + t * 16384 : sQ + t * C::kQTileBytes) + wq * 4096;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += whole ? 64 : 32) {
+          uint32_t o[32];
+#pragma unroll 1
+          for (int h2 = 0; h2 < (whole ? 2 : 1); ++h2) {
+            channels(c0 + h2 * 32, o);
             if (whole) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 uint32_t w[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  w[k] = pack2<false>(__uint_as_float(o[i * 8 + 2 * k]) * inv, __uint_as_float(o[i * 8 + 2 * k + 1]) * inv);
-                *reinterpret_cast<uint4*>(stage + lane * (2 * D) + (((c0 / 8 + i) ^ (lane & 7)) << 4)) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
+                for (int x = 0; x < 4; ++x)
+                  w[x] = pack2<false>(__uint_as_float(o[i * 8 + 2 * x]), __uint_as_float(o[i * 8 + 2 * x + 1]));
+                const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4*>(stage + lane * 128 + (((h2 * 4 + i) ^ (lane & 7)) << 4)) = v;
               }
             } else {
-              const int b = (c0 - half * (D / 2)) / 4;
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(stage + lane * (2 * D) + (((b + i) ^ (lane & 7)) << 4)) =
-                    make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              for (int i = 0; i < 8; ++i) {
+                const uint4 v = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) = v;
+              }
             }
           }
           __syncwarp();
-#pragma unroll 4
-          for (int i = 0; i < kRowChunks; ++i) {
-            const int rr = i * (32 / kRowChunks) + lane / kRowChunks, ch = lane % kRowChunks;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = i * 4 + (lane >> 3), ch = lane & 7;
             const int64_t at = __shfl_sync(0xffffffffu, o_at, rr);
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * (2 * D) + ((ch ^ (rr & 7)) << 4));
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
             if (rr < rows_here) {
-              if (whole) *reinterpret_cast<uint4*>(out + at + ch * 8) = v;
-              else *reinterpret_cast<uint4*>(part + rr * D + half * (D / 2) + ch * 4) = v;
+              if (whole) *reinterpret_cast<uint4*>(out + at + c0 + ch * 8) = v;
+              else *reinterpret_cast<uint4*>(part + rr * D + c0 + ch * 4) = v;
             }
           }
           __syncwarp();
+          if (C::kEarlyQ && !kE4M3 && c0 == 0 && has_next) announce_q(next);
         }
+        tc_fence_before();
+        mbar_arrive(o_free + t);
+        if (one && ntiles > 1) mbar_arrive(o_free + 1);
         if (live) {
           if (!whole) a.part_ml[u.slot * kPagedChunkRows + ur] = make_float2(m, l);
           else if (a.lse) a.lse[static_cast<int64_t>(tok) * a.hq + hd] = lse_of(m, l);
         }
       }
-    }
-  }
-}
-
-template <int D, bool kE4M3>
-__global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
-    paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                       const __grid_constant__ ChunkParams p) {
-  using C = ChunkCfg<D, kE4M3>;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ ChunkShared sh;
-  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  const PagedAttnArgs& a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  if (warp == 0) {
-    Unit u;
-    const int bx = blockIdx.x, split = bx >= p.whole;
-    const int part = split ? (bx - p.whole) % p.splits : 0;
-    const bool found = find_unit(a, p.group, split ? p.whole + (bx - p.whole) / p.splits : bx, u);
-    if (lane == 0) {
-      sh.skip = !found || *reinterpret_cast<volatile int32_t*>(a.status) == kStatusTimeout;
-      sh.abort = 0;
-      if (found) {
-        // This CTA's share of the unit's key tiles; a share may be empty when there are few.
-        u.slot = -1;
-        if (split) {
-          const int per = (u.nt + p.splits - 1) / p.splits;
-          const int from = min(u.nt, per * part);
-          u.t0 += from;
-          u.nt = min(per, u.nt - from);
-          u.slot = bx - p.whole;
-        }
-        sh.unit = u;
+      if (!C::kEarlyQ && has_next) {
+        load_q(next);
+        announce_q(next);
       }
-      uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-      mbar_init(bar++, found && u.rows > 128 ? 256 : 128);                                   // q_full
-      for (int s = 0; s < 2 * C::kMaxStages; ++s) mbar_init(bar++, kE4M3 ? 128 : 1);         // k_full, v_full
-      for (int s = 0; s < 2 * C::kMaxStages + 2; ++s) mbar_init(bar++, 1);                   // k_empty, v_empty, s_full
-      for (int t = 0; t < 2; ++t) mbar_init(bar++, 128);                                     // p_full
-      for (int t = 0; t < 2; ++t) mbar_init(bar++, 1);                                       // pv_done
-      for (int t = 0; t < 2; ++t) mbar_init(bar++, 4);                                       // s_free
-      mbar_init(bar++, 1);                                                                   // mma_final
-      for (int t = 0; t < 2; ++t) mbar_init(bar++, 1);                                       // raw_full
-      for (int t = 0; t < 2; ++t) mbar_init(bar++, 128);                                     // raw_empty
-      fence_mbar_init();
+      release_unit(k);
+      return ok;
+    };
+    bool ok = wait(unit_full, 0, kWherePagedEmpty);
+    if (ok && sh.unit[0].nt >= 0) {
+      load_q(sh.unit[0]);
+      announce_q(sh.unit[0]);
     }
-  }
-  __syncthreads();
-  if (sh.skip) return;
-  if (sh.unit.nt == 0) {   // an empty share of a split unit
-    for (int r = threadIdx.x; r < sh.unit.rows; r += C::kThreads)
-      a.part_ml[sh.unit.slot * kPagedChunkRows + r] = make_float2(-INFINITY, 0.0f);
-    return;
-  }
-  if (warp == 2) {
-    tmem_alloc(&sh.tmem, 512);
-    tmem_relinquish();
+    for (int k = 0; ok && sh.unit[k & 1].nt >= 0; ++k) ok = work(k);
+    if (!kE4M3) asm volatile("cp.async.wait_all;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  if (sh.unit.rows > 128) chunk_roles<D, kE4M3, false>(kmap, vmap, p, sh, smem);
-  else chunk_roles<D, kE4M3, true>(kmap, vmap, p, sh, smem);
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 2) {
+  if (warp == 3) {
     tc_fence_after();
-    tmem_dealloc(sh.tmem, 512);
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -1008,8 +1152,8 @@ cudaError_t launch_t(const PagedAttnArgs& a, const sage_paged_kv& kv, cudaStream
     if (last_wave(k) < last_wave(splits)) splits = k;
   p.splits = static_cast<int>(splits);
   p.whole = static_cast<int>(splits > 1 ? units - rest : units);
-  const unsigned grid = static_cast<unsigned>(p.whole + (units - p.whole) * splits);
-  paged_chunk_kernel<D, kE4M3><<<grid, C::kThreads, C::kSmem, s>>>(kmap, vmap, p);
+  p.items = static_cast<uint32_t>(p.whole + (units - p.whole) * splits);
+  paged_chunk_kernel<D, kE4M3><<<std::min<uint32_t>(p.items, sms), C::kThreads, C::kSmem, s>>>(kmap, vmap, p);
   err = cudaGetLastError();
   if (err == cudaSuccess && splits > 1)
     err = launch_dependent(true, paged_join_kernel<D>, dim3(static_cast<unsigned>(rest), kPagedChunkRows / 8), dim3(256), 0,
