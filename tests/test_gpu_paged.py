@@ -313,6 +313,24 @@ def test_attention_of_many_sequences_of_mixed_lengths(fmt, d):
     paged_ref.check_attention(p, out, paged_ref.attention(p, p.q, True))
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_of_more_chunks_than_sms(fmt, d):
+    """Several units to each SM, drawn as they end: of one row tile and of two, long and short, windows that begin
+    behind the first page; whichever SM takes which, the result is the same, and the next call starts anew."""
+    q_lens = [(70, 1, 0, 300, 33, 129, 256)[i % 7] for i in range(42)]
+    kv_lens = [q + (0, 1500, 3, 640, 127)[i % 5] for i, q in enumerate(q_lens)]
+    p = Problem(q_lens, kv_lens, 16, 8, d, 64, fmt, seed=50 + d)
+    cache, batch = _handles(p)
+    ws = sage.paged_workspace(d)
+    for window in (0, 200):
+        out = sage.sage_paged_attn(p.q, cache, batch, window=window, ws=ws)
+        paged_ref.check_attention(p, out, paged_ref.attention(p, p.q, True, window))
+        for _ in range(8):
+            assert torch.equal(_bits(sage.sage_paged_attn(p.q, cache, batch, window=window, ws=ws)[:p.n]), _bits(out[:p.n]))
+    assert sage.sage_check_device_status(ws) == (0, 0)
+
+
 @pytest.mark.parametrize("q_len", [1, 70])
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 def test_attention_of_rows_of_very_different_size(q_len, fmt):
