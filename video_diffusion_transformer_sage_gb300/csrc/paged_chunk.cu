@@ -25,7 +25,7 @@
 // 180 -> 168, 2048 rows over 16384 bf16 keys of 16 heads 207 -> 201; a call of one short unit per SM takes 0.8 us
 // more (13.2 -> 14.0).
 //
-// Warp roles: warp 0 (and 3) page table and TMA, warp 1 MMA issue (one thread), warp 2 draws the items and finds their
+// Warp roles: warp 0 (and 3) page table and TMA, warp 1 MMA issue, warp 2 draws the items and finds their
 // units; warps 4-7 and 8-11 softmax and epilogue of tile 0 and 1; with E4M3 warps 12-15 widen.  Every wait is bounded.
 //
 // What bounds it: 4 rows keys D FLOPs at the 16-bit tensor rate (for few rows the cache's bytes), and the softmax warps,
@@ -59,7 +59,7 @@ struct ChunkCfg {
   static constexpr int kStages = D == 128 ? 2 : 4;
   // K and V of a tile have barriers of their own where the ring is short (D = 128): a K stage is free again once
   // Q K^T has read it, a softmax before P V is done with V (chunk_frames 2358 -> 2236 us).  The four stages at
-  // D = 64 hide the loads anyway, and there the extra waits of the issuing thread cost 5 %.
+  // D = 64 hide the loads anyway, and there the extra waits of the issuing warp cost 5 %.
   static constexpr bool kSplitKV = D == 128;
   static constexpr int kRawTile = kBN * D;                    // a tile of codes
   static constexpr int kRawBytes = kE4M3 ? 2 * kRawTile : 0;
@@ -83,7 +83,7 @@ struct ChunkCfg {
   static constexpr int kNumBars = 4 * kStages + 24;
   static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;
   // Registers a thread: launched at 168 (384 threads) or 128 (512).
-  static constexpr int kRegsRoles = kE4M3 ? 56 : 72, kRegsSoftmax = kE4M3 ? 192 : 216, kRegsWiden = 72;
+  static constexpr int kRegsRoles = 72, kRegsSoftmax = kE4M3 ? 184 : 216, kRegsWiden = 72;
   static_assert(128 * kRegsRoles + 256 * kRegsSoftmax + (kE4M3 ? 128 * kRegsWiden : 0) <= (kE4M3 ? 512 * 128 : 384 * 168),
                 "register split exceeds launch");
   static_assert(kSmem <= 232448 - 1408, "shared memory");
@@ -215,26 +215,49 @@ __device__ __forceinline__ uint32_t vdesc_lo(uint32_t saddr) {
   return ((saddr & 0x3FFFFu) >> 4) | ((128u * 128u >> 4) << 16);
 }
 
-// Descriptors are added up at each instruction: kept in registers from step to step they spilled (window_e4m3 189 ->
-// 181 us, 2048 rows over 8192 E4M3 keys of 16 heads 133 -> 120).
+// MMA and commit on behalf of a converged warp: one thread of it, always the same, issues.  The whole warp computes the
+// operands, which are the same in all lanes and known to be so (the warp's number, shared-memory base, tile counts
+// come by shuffle), so they need not be moved to uniform registers for each MMA: one lane's code spent ~93 cycles on
+// each, this ~35 (D = 64, 2048 rows over 16384 bf16 keys of 16 heads 168 -> 149 us; prompts_causal 345 -> 329).
+__device__ __forceinline__ void warp_mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void warp_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void warp_tc_commit(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
 template <int D, bool kE4M3>
 __device__ __forceinline__ void issue_qk(uint32_t s_tmem, uint32_t ql, uint32_t kl) {
   constexpr uint32_t idesc = idesc_f32acc(kBM, kBN) | (kE4M3 ? 0u : kIdescBf16);
-  asm volatile("" : "+r"(s_tmem), "+r"(ql), "+r"(kl));
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
     const uint32_t off = ((kk >> 2) * ChunkCfg<D, kE4M3>::kPanelBytes + (kk & 3) * 32) >> 4;
-    mma_f16_ss(s_tmem, sdesc_of_lo(ql + off), sdesc_of_lo(kl + off), idesc, kk > 0 ? 1u : 0u);
+    warp_mma_f16_ss(s_tmem, sdesc_of_lo(ql + off), sdesc_of_lo(kl + off), idesc, kk > 0 ? 1u : 0u);
   }
 }
 // P: 16 keys in 8 tensor-memory columns; V: 16 keys are 2048 bytes.
 template <int D, bool kE4M3>
 __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint32_t vl, bool first) {
   constexpr uint32_t idesc = idesc_f32acc(kBM, D) | kIdescBmn | (kE4M3 ? 0u : kIdescBf16);
-  asm volatile("" : "+r"(o_tmem), "+r"(p_tmem), "+r"(vl));
 #pragma unroll
   for (int kk = 0; kk < kBN / 16; ++kk)
-    mma_f16_ts(o_tmem, p_tmem + kk * 8, sdesc_of_lo(vl + kk * (2048 >> 4)), idesc, (first && kk == 0) ? 0u : 1u);
+    warp_mma_f16_ts(o_tmem, p_tmem + kk * 8, sdesc_of_lo(vl + kk * (2048 >> 4)), idesc, (first && kk == 0) ? 0u : 1u);
 }
 
 template <bool kF16>
@@ -407,7 +430,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
   uint64_t* unit_empty = unit_full + 2;
   uint64_t* draw = unit_empty + 2;
   const PagedAttnArgs& a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     sh.skip = *reinterpret_cast<volatile int32_t*>(a.status) == kStatusTimeout;
@@ -424,7 +447,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
       mbar_init(raw_full + i, 1);
       mbar_init(raw_empty + i, 128);
       mbar_init(unit_full + i, 1);
-      // The loading warps, the issuing thread, the softmax and the widening warps.
+      // The loading warps, the issuing warp, the softmax and the widening warps.
       mbar_init(unit_empty + i, (C::kTwoLoaders ? 2 : 1) + 1 + 8 + (kE4M3 ? 4 : 0));
     }
     mbar_init(ml_full, 128);
@@ -483,7 +506,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   const int boxes = kBN >> p.box_shift;
   // A bounded wait by a whole warp; records the first timeout.  False once anything timed out.
   auto wait = [&](uint64_t* bar, uint32_t parity, int where) {
@@ -607,27 +630,28 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
             mbar_wait((kv0 ? v_full : k_full) + i % S, (i / S) & 1, kChunkWaitNs);
         }
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issue
       const uint32_t colS = tmem, colO = tmem + C::kColO0, colP = tmem + C::kColP0;
-      const uint32_t q_lo = sdesc_lo(smem_u32(sQ)), k_lo = sdesc_lo(smem_u32(sKV)),
-                     v_lo = vdesc_lo(smem_u32(sKV) + C::kTileBytes);
+      const uint32_t s_base = __shfl_sync(0xffffffffu, smem_u32(sQ), 0);
+      const uint32_t q_lo = sdesc_lo(s_base), k_lo = sdesc_lo(s_base + C::kKvOff),
+                     v_lo = vdesc_lo(s_base + C::kKvOff + C::kTileBytes);
       constexpr uint32_t kQLo = C::kQTileBytes >> 4, kStageLo = C::kStageBytes >> 4;
       // The ring stage and phase of the next K tile and of the next V tile; per slot the S, P V, units and Q tiles so
       // far.
       int sk = 0, sv = 0;
       uint32_t phk = 0, phv = 0, ns[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0}, nq[2] = {0, 0};
       bool ok = true;
-      auto mwait = [&](uint64_t* x, uint32_t parity) { return mbar_wait(x, parity, kChunkWaitNs); };
+      auto mwait = [&](uint64_t* x, uint32_t parity) { return warp_wait(x, parity); };
       auto step_k = [&]() {
-        if (C::kSplitKV) tc_commit(k_empty + sk);
+        if (C::kSplitKV) warp_tc_commit(k_empty + sk);
         if (++sk == S) {
           sk = 0;
           phk ^= 1u;
         }
       };
       auto step_v = [&]() {
-        tc_commit(v_empty + sv);
+        warp_tc_commit(v_empty + sv);
         if (++sv == S) {
           sv = 0;
           phv ^= 1u;
@@ -645,7 +669,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
         constexpr int t = decltype(T)::v;
         tc_fence_after();
         issue_qk<D, kE4M3>(colS + t * kBN, q_lo + tile * kQLo, k_lo + sk * kStageLo);
-        tc_commit(s_full + t);
+        warp_tc_commit(s_full + t);
         ++ns[t];
       };
       auto p_ready = [&](auto T) {
@@ -656,7 +680,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
         constexpr int t = decltype(T)::v;
         tc_fence_after();
         issue_pv<D, kE4M3>(colO + t * D, colP + t * C::kStepP, v_lo + sv * kStageLo, first);
-        tc_commit(pv_done + t);
+        warp_tc_commit(pv_done + t);
         ++np[t];
       };
       // A unit's first S of a slot; its first P V waits until the last unit's O was read.
@@ -692,9 +716,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
       for (int k = 0; ok; ++k) {
         ok = mwait(unit_full + (k & 1), (k >> 1) & 1);
         if (!ok) break;
-        const int ntiles = sh.unit[k & 1].nt;
-        const bool one = sh.unit[k & 1].rows <= 128;
-        mbar_arrive(unit_empty + (k & 1));
+        const int ntiles = __shfl_sync(0xffffffffu, sh.unit[k & 1].nt, 0);
+        const bool one = __shfl_sync(0xffffffffu, sh.unit[k & 1].rows, 0) <= 128;
+        release_unit(k);
         if (ntiles < 0) break;
         ok = k_ready() && mwait(q_full, nq[0]++ & 1) && begin(s0, 0);
         if (one) {
@@ -715,19 +739,23 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
           for (int j = 0; j < ntiles && ok; ++j) {
             const bool more = j + 1 < ntiles;
             if (C::kSepP) {
-              // S of the next tile as soon as S is read, P V once P is written.
+              // S of the next tile as soon as S is read, P V once P is written.  The slots in turn: with both S issued
+              // before both P V the two softmaxes ran in step and shared the exponential units (149 -> 135 us at the
+              // sizes above).
               if (more) {
                 ok = k_ready() && s_ready(s0);
                 if (!ok) break;
                 qk(s0, 0);
+              }
+              ok = p_ready(s0) && v_ready();
+              if (!ok) break;
+              pv(s0, j == 0);
+              if (more) {
                 ok = s_ready(s1);
                 if (!ok) break;
                 qk(s1, 1);
                 step_k();
               }
-              ok = p_ready(s0) && v_ready();
-              if (!ok) break;
-              pv(s0, j == 0);
               ok = p_ready(s1);
               if (!ok) break;
               pv(s1, j == 0);
@@ -755,9 +783,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
           }
         }
       }
-      if (!ok) record_timeout(a.status, kWherePagedMma, &sh.abort);
+      if (!ok && lane == 0) record_timeout(a.status, kWherePagedMma, &sh.abort);
+      __syncwarp();
       // Every MMA issued has finished before the tensor memory is freed.
-      tc_commit(mma_final);
+      warp_tc_commit(mma_final);
       mbar_wait(mma_final, 0, kChunkWaitNs);
     }
   } else if (kE4M3 && warp >= 12) {
