@@ -36,6 +36,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "paged_batch.cuh"
 #include "tensor_map.h"
@@ -95,6 +96,7 @@ struct ChunkParams {
   int box_shift;   // log2 of the slots per TMA box (a page, or 128)
   int whole;       // units below this number are one item; each of the rest is `splits` items
   int splits;
+  int halve;       // units of one row tile are split half as often
   uint32_t items;
 };
 
@@ -464,7 +466,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
     if (lane == 0 && __ldg(a.b.kv_len + u.b) > a.b.cap) record_bad_index(a.status, kWhereLength);
     u.slot = -1;
     if (split) {
-      const int per = (u.nt + p.splits - 1) / p.splits, from = min(u.nt, per * (rest % p.splits));
+      // A unit of one row tile takes half as long: among others it has half as many shares that are not empty.
+      const int parts = p.halve && u.rows <= 128 ? (p.splits + 1) / 2 : p.splits;
+      const int per = (u.nt + parts - 1) / parts, from = min(u.nt, per * (rest % p.splits));
       u.t0 += from;
       u.nt = min(per, u.nt - from);
       u.slot = rest;
@@ -1114,24 +1118,47 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
   const int ur = blockIdx.y * 8 + (threadIdx.x >> 5);
   if (ur >= u.rows) return;
   const float2* ml = a.part_ml + static_cast<int64_t>(blockIdx.x) * p.splits * kPagedChunkRows + ur;
-  float m = -INFINITY, l = 0.0f;
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, ml[s * kPagedChunkRows].x);
   constexpr int kC = D / 32;   // channels of a lane
+  using Channels = std::conditional_t<D == 128, float4, float2>;
+  const float* o = a.part_o + (static_cast<int64_t>(blockIdx.x) * p.splits * kPagedChunkRows + ur) * D + lane * kC;
+  const int64_t o_step = static_cast<int64_t>(kPagedChunkRows) * D;
+  float m = -INFINITY, l = 0.0f;
+  for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, ml[s * kPagedChunkRows].x);
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
   float v[kC];
 #pragma unroll
   for (int i = 0; i < kC; ++i) v[i] = 0.0f;
-  if (m != -INFINITY)
-    for (int s = 0; s < p.splits; ++s) {
-      const float2 x = ml[s * kPagedChunkRows];
-      if (x.x == -INFINITY) continue;     // saw no key: its O was not written, or counts nothing
-      const float f = ex2_approx(x.x - m);
-      const float* o = a.part_o + ((static_cast<int64_t>(blockIdx.x) * p.splits + s) * kPagedChunkRows + ur) * D + lane * kC;
+  for (int s0 = 0; s0 < p.splits; s0 += 32) {
+    // Lane i has part s0 + i's factor, 0 for one that saw no key: its O counts nothing (and may not have been written).
+    float f = 0.0f;
+    if (s0 + lane < p.splits) {
+      const float2 x = ml[(s0 + lane) * kPagedChunkRows];
+      if (x.x != -INFINITY) f = ex2_approx(x.x - m);
+      else if (x.y != 0.0f) f = x.y;   // scores that are no numbers: neither is the result
       l += x.y * f;
-#pragma unroll
-      for (int i = 0; i < kC; ++i) v[i] += o[i] * f;
     }
+    const int n = min(32, p.splits - s0);
+    for (int s = 0; s < n; s += 4) {
+      float part[4][kC], g[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        g[x] = __shfl_sync(0xffffffffu, f, s + x);
+        Channels c{};
+        if (g[x] != 0.0f) c = *reinterpret_cast<const Channels*>(o + (s0 + s + x) * o_step);
+#pragma unroll
+        for (int i = 0; i < kC; ++i) part[x][i] = reinterpret_cast<const float*>(&c)[i];
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int i = 0; i < kC; ++i) v[i] = fmaf(part[x][i], g[x], v[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 16; i > 0; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
   const int row = u.row0 + ur, tok = u.start + row / p.group, hd = u.h * p.group + row % p.group;
-  const float inv = m == -INFINITY ? 0.0f : (a.v_scale ? __ldg(a.v_scale + u.h) : 1.0f) / l;
+  const float inv = l > 0.0f ? (a.v_scale ? __ldg(a.v_scale + u.h) : 1.0f) / l : l;   // 0 for a row that saw no key
   uint16_t* dst = a.out + static_cast<int64_t>(tok) * a.ost + static_cast<int64_t>(hd) * a.osh + lane * kC;
 #pragma unroll
   for (int i = 0; i < kC; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = pack2<false>(v[i] * inv, v[i + 1] * inv);
@@ -1165,22 +1192,28 @@ cudaError_t launch_t(const PagedAttnArgs& a, const sage_paged_kv& kv, cudaStream
   const int64_t seqs = std::min<int64_t>(a.b.n_seqs, a.b.n_tokens);
   const int64_t units = (rows + 255 * seqs) / 256 * a.hkv;
   // Whole units fill the SMs as often as they can; those left over are split along the keys into the number of
-  // parts that ends them soonest, estimated in microseconds: a unit's key tiles (at most the table's) at 1.6 us for
-  // two row tiles of D = 128, 12 us for a part's start and end, and the parts' O written and read again at 2.5 TB/s
-  // with 4 us for the join.
-  const int64_t rest = units % sms, tiles = std::max(1, (a.b.cap + kBN - 1) / kBN);
+  // parts that ends them soonest.  Their number is estimated from the mean length of a sequence.  In microseconds: an
+  // item's key tiles (at most the table's) at 1.45 us for two row tiles of D = 128, 0.98 of D = 64, half for one row
+  // tile; 3 between items; the parts' O written and read again at 3.4 TB/s with 6 us for the join,
+  // 10 behind whole units (24 x 128 rows over 3000 keys of 8 heads: 71 us unsplit, 78 in three).
+  const int64_t mean = (rows + seqs - 1) / seqs, blocks = (mean + 255) / 256;
+  const bool one = mean <= 128, odd = mean - (blocks - 1) * 256 <= 128;   // units of one row tile: all, or the last ones
+  const int64_t likely = std::min(units, seqs * blocks * a.hkv), whole = likely / sms * sms, rest = units - whole;
+  const double count = static_cast<double>(likely - whole), tile_us = 0.51 + 0.94 * D / 128;
+  const int64_t tiles = std::max(1, (a.b.cap + kBN - 1) / kBN);
   const int64_t most = std::min<int64_t>({kPagedSlots / std::max<int64_t>(rest, 1), sms, std::max<int64_t>(1, tiles / 4)});
   auto last_wave = [&](int64_t k) {
-    const double waves = static_cast<double>((rest * k + sms - 1) / sms);
-    const double part_bytes = std::min<double>(static_cast<double>(rows), 256.0) * D * 4;
-    return waves * (1.6 * D / 128 * static_cast<double>((tiles + k - 1) / k) + 12.0) +
-           (k > 1 ? 4.0 + static_cast<double>(rest * k) * part_bytes * 2 / 2.5e6 : 0.0);
+    const double items = count * static_cast<double>(k) * (odd && !one ? 1.0 - 0.5 / static_cast<double>(blocks) : 1.0);
+    const double item = tile_us * (one ? 0.5 : 1.0) * static_cast<double>((tiles + k - 1) / k) + 3.0;
+    const double part_bytes = std::min<double>(static_cast<double>(mean), 256.0) * D * 4;
+    return std::ceil(items / sms) * item + (k > 1 ? (whole > 0 ? 10.0 : 6.0) + items * part_bytes * 2 / 3.4e6 : 0.0);
   };
   int64_t splits = 1;
   for (int64_t k = 2; k <= most; ++k)
     if (last_wave(k) < last_wave(splits)) splits = k;
   p.splits = static_cast<int>(splits);
-  p.whole = static_cast<int>(splits > 1 ? units - rest : units);
+  p.halve = !one;
+  p.whole = static_cast<int>(splits > 1 ? whole : units);
   p.items = static_cast<uint32_t>(p.whole + (units - p.whole) * splits);
   paged_chunk_kernel<D, kE4M3><<<std::min<uint32_t>(p.items, sms), C::kThreads, C::kSmem, s>>>(kmap, vmap, p);
   err = cudaGetLastError();
