@@ -60,7 +60,7 @@ struct ChunkCfg {
   static constexpr int kStages = D == 128 ? 2 : 4;
   // K and V of a tile have barriers of their own where the ring is short (D = 128): a K stage is free again once
   // Q K^T has read it, a softmax before P V is done with V (chunk_frames 2358 -> 2236 us).  The four stages at
-  // D = 64 hide the loads anyway, and there the extra waits of the issuing warp cost 5 %.
+  // D = 64 hide the loads anyway, and there the extra waits of the issuing warp cost 3 %.
   static constexpr bool kSplitKV = D == 128;
   static constexpr int kRawTile = kBN * D;                    // a tile of codes
   static constexpr int kRawBytes = kE4M3 ? 2 * kRawTile : 0;
