@@ -83,7 +83,7 @@ sage::PagedBatchDev batch_dev(const sage_paged_batch* b, const sage_paged_kv* c,
 // Workspace: status block | counters | (maximum, sum) of each partial row | partial O.
 constexpr size_t kCountersOff = kStatusBytes;
 constexpr size_t kMlOff = SAGE_PAGED_WS_HEADER;
-static_assert(kCountersOff + sizeof(int32_t) * (2 * sage::kPagedMaxCtas + 1) <= kMlOff, "counters exceed the workspace header");
+static_assert(kCountersOff + sizeof(int32_t) * (2 * sage::kPagedMaxCtas + 2) <= kMlOff, "counters exceed the workspace header");
 constexpr size_t kSlots = sage::kPagedSlots;
 constexpr size_t kPartOff = kMlOff + kSlots * sage::kPagedChunkRows * sizeof(float2);
 

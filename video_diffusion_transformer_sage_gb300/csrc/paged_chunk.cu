@@ -459,7 +459,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
     fence_mbar_init();
   }
   // Warp 2 finds an item's unit and its share of the unit's key tiles (which may be empty when there are few).
-  auto take = [&](uint32_t item, Unit& u) {
+  // False past the last unit, of which the number of items is an upper bound: no later item has one either.
+  auto take = [&](uint32_t item, Unit& u, bool& have) {
+    have = false;
     const bool split = item >= static_cast<uint32_t>(p.whole);
     const int rest = static_cast<int>(item) - p.whole;
     if (!find_unit(a, p.group, split ? p.whole + rest / p.splits : static_cast<int>(item), u)) return false;
@@ -480,15 +482,16 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
         token_keys(a, u.len, u.n_new, (u.row0 + from) / p.group, unused, u.ahi[t]);
         token_keys(a, u.len, u.n_new, (u.row0 + last) / p.group, u.alo[t], unused);
       }
+      have = true;
       return true;
     }
     for (int r = lane; r < u.rows; r += 32) a.part_ml[u.slot * kPagedChunkRows + r] = make_float2(-INFINITY, 0.0f);
-    return false;
+    return true;
   };
   Unit u{};
-  bool have = false, first = true;
+  bool have = false, end = false, first = true;
   // Item k for the other roles, with the CTA's counts up to it.
-  auto publish = [&](int k, bool end) {
+  auto publish = [&](int k) {
     if (end) u.nt = -1;
     if (lane == 0) {
       sh.unit[k & 1] = u;
@@ -499,10 +502,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
     u.ones += u.rows <= 128;
     for (int t = 0; t < 2; ++t) u.mine[t] += u.rows > 128 ? u.nt : (u.nt + 1 - t) / 2;
   };
-  if (warp == 2) have = take(blockIdx.x, u);
+  if (warp == 2) end = !take(blockIdx.x, u, have);
   __syncthreads();
   if (sh.skip) return;   // an earlier wait ran out: no work until the status has been read
-  if (warp == 2 && have) publish(0, false);
+  if (warp == 2 && (have || end)) publish(0);
   if (warp == 3) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
@@ -529,14 +532,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
     regs_dec<C::kRegsRoles>();
     if (warp == 2) {
       // ------------------------------------------------------------ items, one ahead
-      uint32_t item = blockIdx.x;
-      for (int k = have ? 1 : 0;;) {
-        const bool end = item >= p.items;
+      int32_t* next_item = a.counters + 2 * kPagedMaxCtas;   // and the number of CTAs that draw no more
+      uint32_t item = 0;
+      for (int k = have || end ? 1 : 0;;) {
         if (!first) {
-          have = !end && take(item, u);
+          end = item >= p.items || !take(item, u, have);
           if (have || end) {
             if (k >= 2 && !wait(unit_empty + (k & 1), ((k >> 1) - 1) & 1, kWherePagedEmpty)) break;
-            publish(k++, end);
+            publish(k++);
           }
         }
         first = false;
@@ -556,14 +559,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
             break;
           }
         }
-        // Items are handed out one by one; whoever draws the last number, past the end, resets the counter.
         uint32_t drawn = 0;
-        if (lane == 0) {
-          drawn = static_cast<uint32_t>(atomicAdd(a.counters + 2 * kPagedMaxCtas, 1));
-          if (drawn == p.items - 1) a.counters[2 * kPagedMaxCtas] = 0;
-        }
+        if (lane == 0) drawn = static_cast<uint32_t>(atomicAdd(next_item, 1));
         item = gridDim.x + __shfl_sync(0xffffffffu, drawn, 0);
       }
+      // The last CTA to draw no more leaves the counters at zero for the next call.
+      if (end && p.items > gridDim.x && lane == 0 && atomicAdd(next_item + 1, 1) == static_cast<int>(gridDim.x) - 1)
+        next_item[0] = next_item[1] = 0;
     } else if (warp == 0 || (C::kTwoLoaders && warp == 3)) {
       // ------------------------------------------------------------ page table and TMA
       const int kv0 = warp == 0 ? 0 : 1, kv1 = C::kTwoLoaders && warp == 0 ? 1 : 2;   // K, V or both

@@ -63,7 +63,7 @@ struct PagedAttnArgs {
   int64_t ost, osh;
   float* lse;
   int32_t* status;
-  int32_t* counters;           // [2 kPagedMaxCtas + 1], zero between calls
+  int32_t* counters;           // [2 kPagedMaxCtas + 2], zero between calls
   float2* part_ml;             // [slots][rows]: running maximum (log2 units) and sum
   float* part_o;               // [slots][rows][D]
 };
