@@ -542,6 +542,31 @@ def test_on_another_stream():
     assert torch.equal(out, out2)
 
 
+def test_buffers_that_a_call_makes_belong_to_its_stream():
+    """Output, status block and workspace made by a call on a given stream, while the current stream is busy: zeroed
+    before the kernel, and not given away before it is done."""
+    p = Problem([1, 5, 60], [4000, 77, 900], 8, 2, 128, 32, seed=23)
+    cache, batch = _handles(p)
+    ref_q = sage.sage_paged_append(p.k, p.v, *_handles(p), q=p.q, rope_cos=p.cos, rope_sin=p.sin)
+    want = sage.sage_paged_attn(ref_q, cache, batch).clone()
+    busy = torch.randn((6000, 6000), device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for given in (side, side.cuda_stream):
+        cache, batch = _handles(p)
+        for _ in range(8):
+            busy = busy @ busy * 1e-4
+        q = sage.sage_paged_append(p.k, p.v, cache, batch, q=p.q, rope_cos=p.cos, rope_sin=p.sin, stream=given)
+        outs = [sage.sage_paged_attn(q, cache, batch, stream=given) for _ in range(3)]
+        for _ in range(4):
+            torch.full((1 << 22,), 255, dtype=torch.uint8, device="cuda")   # what was freed on the current stream
+        side.synchronize()
+        assert sage.sage_check_device_status(cache.status, stream=side) == (0, 0)
+        assert torch.equal(_bits(q), _bits(ref_q))
+        assert all(torch.equal(_bits(o), _bits(want)) for o in outs)
+    torch.cuda.synchronize()
+
+
 def test_two_calls_at_once_on_their_own_workspaces():
     ps = [Problem([1], [20000 + 999 * i], 8, 2, 128, 64, seed=20 + i) for i in range(2)]
     hs = [_handles(p) for p in ps]

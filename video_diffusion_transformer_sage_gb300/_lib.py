@@ -7,6 +7,7 @@ missing the import of any op raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -464,6 +465,15 @@ def _paged_call(device, stream, fn, args) -> int:
         return fn(*args, raw)
 
 
+def _made_on(stream, device):
+    """Where a call makes a buffer: on its own stream, so that zeroing comes before the kernel and the memory's next
+    use after it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream")
+                             else torch.cuda.ExternalStream(int(stream), device=device))
+
+
 def _fp32_table(t: Optional[torch.Tensor], shape: tuple, device, what: str):
     if t is None:
         return None
@@ -490,7 +500,8 @@ def sage_paged_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKV, batch: P
     if q is not None:
         vq = _paged_view(q, d, dev, "q")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+            with _made_on(stream, dev):
+                q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
         vo = _paged_view(q_out, d, dev, "q_out")
         if vo.n_tokens != vq.n_tokens or vo.n_heads != vq.n_heads:
             raise ValueError("q_out must have q's shape")
@@ -501,7 +512,10 @@ def sage_paged_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKV, batch: P
                                   or not positions.is_contiguous() or positions.device != dev):
         raise ValueError("positions: expected a contiguous int32 tensor [N] on the cache's device")
     if status is None:
-        status = cache.status
+        status = cache._status
+        if status is None:
+            with _made_on(stream, dev):
+                status = cache.status
     elif status.device != dev or status.nbytes < 256:
         raise ValueError("status: expected a zeroed block of 256 bytes on the cache's device")
     rows = rope_cos.shape[0] if rope_cos is not None else 0
@@ -525,7 +539,8 @@ def sage_paged_attn(q: torch.Tensor, cache: PagedKV, batch: PagedBatch, sm_scale
     if batch.device != dev:
         raise ValueError("the batch lies on another device than the cache")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        with _made_on(stream, dev):
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
     vo = _paged_view(out, d, dev, "out")
     if vo.n_tokens != vq.n_tokens or vo.n_heads != vq.n_heads:
         raise ValueError("out must have q's shape")
@@ -533,7 +548,8 @@ def sage_paged_attn(q: torch.Tensor, cache: PagedKV, batch: PagedBatch, sm_scale
                             or not lse.is_contiguous() or lse.device != dev):
         raise ValueError("lse: expected a contiguous fp32 tensor [N, Hq] on the cache's device")
     if ws is None:
-        ws = paged_workspace(d, dev)
+        with _made_on(stream, dev):
+            ws = paged_workspace(d, dev)
     elif ws.device != dev:
         raise ValueError("ws lies on another device than the cache")
     sm_scale = 1.0 / math.sqrt(d) if sm_scale is None else sm_scale
