@@ -14,7 +14,7 @@
 // there.  Otherwise each CTA leaves (maximum, sum, O) of its part in the workspace and takes a ticket; the last
 // one joins the parts in the order of their keys, so the result does not depend on which CTA came last.
 //
-// Inside a CTA: one producer warp (page table entries by lane, one TMA box per page) and two teams of
+// Inside a CTA: two or four loading warps (page table entries by lane, one TMA box per page) and two teams of
 // four consumer warps that take the tiles in turn, a quarter of a tile's keys to each warp.  Each warp
 // keeps a running maximum, sum and O of its own keys (online softmax in fp32); the eight are
 // joined through shared memory at the end of a segment.
@@ -30,7 +30,7 @@
 namespace sage {
 namespace {
 
-// Warps 0-3: the producer warp and three that only give up their registers; warps 4-11: consumers.
+// Warps 0-3: loads (two of them may only give up their registers); warps 4-11: consumers.
 // 384 threads launch with 168 registers each; 40 / 232 after the split (128 * 40 + 256 * 232 =
 // 384 * 168), which holds two row tiles' accumulators.
 constexpr int kFewConsumers = 256, kFewThreads = 384;
@@ -54,6 +54,11 @@ struct FewCfg {
   // barrier could take a phase two back, of the same parity, for the one it waits for.
   static constexpr int kStages = 4;
   static_assert(kStages % 2 == 0, "a ring stage must stay with one team");
+  // K and V have a loading warp each, even and odd tiles too: a tile's load is a chain of waits (~400 cycles) that one
+  // warp did not repeat fast enough (one / two / four warps: decode_e4m3 69.4 / 64.0 / 61.6 us, 16 single tokens over
+  // 500-4000 keys 40.6 / 34.2 / 32.4).  Rows of 64 bytes share lines between heads, which are best read in order
+  // (24 heads: 191 / 179 / 205 us), and with two row tiles the arithmetic is the limit (E4M3: 71.5 / 72 / 73.5).
+  static constexpr int kTurns = MT == 1 && kRowBytes >= 128 ? 2 : 1;
   static constexpr int kWarpKeys = kKeys / 4;
   static constexpr int kNT = kWarpKeys / 8;                   // 8-key score tiles per warp
   static constexpr int kOT = D / 8;                           // 8-channel O tiles
@@ -356,7 +361,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     s_abort = 0;
     s_last[0] = s_last[1] = 0;
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(full + s, 1);
+      mbar_init(full + s, 2);
       mbar_init(empty + s, 4);
     }
     for (int s = 0; s < 2; ++s) {
@@ -375,59 +380,64 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
   Walk<R, KT> wk;
   if (warp < 4) {
-    // ------------------------------------------------------------------ producer
+    // ------------------------------------------------------------------ loads
     regs_dec<kFewRegsProducer>();
-    if (warp != 0 || !wk.init(p)) return;
-    tma_prefetch_desc(&kmap);
-    tma_prefetch_desc(&vmap);
+    // Warps 0 and 1 load K and V, of the even tiles where 2 and 3 load those of the odd ones; warp 0 Q.
+    if (warp >= 2 * C::kTurns || !wk.init(p)) return;
+    const int kv = warp & 1, turn = warp >> 1;
+    const CUtensorMap* map = kv ? &vmap : &kmap;
+    tma_prefetch_desc(map);
     const int box = 1 << p.box_shift, boxes = KT >> p.box_shift;   // boxes per stage, at most 32
-    const uint32_t box_bytes = 2u * static_cast<uint32_t>(box) * C::kRowBytes;
-    int it = 0;
+    const uint32_t box_bytes = static_cast<uint32_t>(box) * C::kRowBytes;
+    int it = 0, issued = 0;
     bool ok = true;
     for (int seg = 0; wk.at < wk.end && ok; ++seg) {
       const int n = wk.seg_tiles();
       const int h = wk.u / wk.w.qt * p.lock + col, qi = wk.u % wk.w.qt;
       const int buf = seg & 1;
-      if (seg >= 2 && !mbar_wait(q_empty + buf, ((seg >> 1) - 1) & 1, kFewWaitNs)) {
+      if (warp == 0 && seg >= 2 && !mbar_wait(q_empty + buf, ((seg >> 1) - 1) & 1, kFewWaitNs)) {
         fail(kWherePagedEmpty);
         ok = false;
       }
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok || s_abort) break;
-      const uint32_t sq = smem_u32(smem + C::kQOff + buf * R * C::kQRow);
-      // Lane i finds row i (one division), the others get it by shuffle; rows past the last are zeros.
-      const int my = qi * R + lane;
-      const int64_t my_at = lane < R && my < wk.w.rows
-                                ? static_cast<int64_t>(wk.w.start + my / p.group) * a.qst +
-                                      static_cast<int64_t>(h * p.group + my % p.group) * a.qsh
-                                : -1;
-      constexpr int kLanes = D / 8;   // lanes to a row
+      ok = __all_sync(0xffffffffu, ok && !s_abort);
+      if (!ok) break;
+      if (warp == 0) {
+        const uint32_t sq = smem_u32(smem + C::kQOff + buf * R * C::kQRow);
+        // Lane i finds row i (one division), the others get it by shuffle; rows past the last are zeros.
+        const int my = qi * R + lane;
+        const int64_t my_at = lane < R && my < wk.w.rows
+                                  ? static_cast<int64_t>(wk.w.start + my / p.group) * a.qst +
+                                        static_cast<int64_t>(h * p.group + my % p.group) * a.qsh
+                                  : -1;
+        constexpr int kLanes = D / 8;   // lanes to a row
 #pragma unroll
-      for (int i = 0; i < R * kLanes / 32; ++i) {
-        const int r = i * (32 / kLanes) + lane / kLanes, c = lane % kLanes;
-        const int64_t at = __shfl_sync(0xffffffffu, my_at, r);
-        cp_async16(sq + r * C::kQRow + c * 16, a.q + (at >= 0 ? at : 0) + c * 8, at >= 0);
+        for (int i = 0; i < R * kLanes / 32; ++i) {
+          const int r = i * (32 / kLanes) + lane / kLanes, c = lane % kLanes;
+          const int64_t at = __shfl_sync(0xffffffffu, my_at, r);
+          cp_async16(sq + r * C::kQRow + c * 16, a.q + (at >= 0 ? at : 0) + c * 8, at >= 0);
+        }
+        cp_async_arrive(q_full + buf);
       }
-      cp_async_arrive(q_full + buf);
       // The keys any row of this tile sees.
       int ulo, uhi, unused;
       token_keys(a, wk.w, (qi * R) / p.group, ulo, unused);
       token_keys(a, wk.w, (min(qi * R + R, wk.w.rows) - 1) / p.group, unused, uhi);
-      if (lane == 0 && __ldg(a.b.kv_len + wk.b) > a.b.cap) record_bad_index(a.status, kWhereLength);
+      if (threadIdx.x == 0 && __ldg(a.b.kv_len + wk.b) > a.b.cap) record_bad_index(a.status, kWhereLength);
       const int32_t* row = a.b.table + wk.b * a.b.table_stride;
       const int first0 = (wk.w.t_lo + wk.k) * KT + (lane << p.box_shift);
       auto needed = [&](int i) { return i < n && lane < boxes && first0 + i * KT < uhi && first0 + i * KT + box > ulo; };
-      int next = needed(0) ? __ldg(row + (first0 >> a.b.page_shift)) : -1;
-      for (int i = 0; i < n; ++i, ++it) {
+      const int i0 = it % C::kTurns != turn;
+      int next = needed(i0) ? __ldg(row + ((first0 + i0 * KT) >> a.b.page_shift)) : -1;
+      for (int i = i0; i < n; i += C::kTurns) {
         // The next tile's table entries are on their way while this one waits for its stage.
-        const int key0 = first0 + i * KT, page = next;
+        const int key0 = first0 + i * KT, page = next, at = it + i;
         const bool need = needed(i);
-        next = needed(i + 1) ? __ldg(row + ((key0 + KT) >> a.b.page_shift)) : -1;
+        next = needed(i + C::kTurns) ? __ldg(row + ((key0 + C::kTurns * KT) >> a.b.page_shift)) : -1;
         const bool good = need && page >= 0 && page < a.b.n_pages;
         if (need && !good) record_bad_index(a.status, kWherePage);
         const uint32_t bits = __ballot_sync(0xffffffffu, good);
-        const int s = it % C::kStages;
-        if (it >= C::kStages && !mbar_wait(empty + s, (it / C::kStages - 1) & 1, kFewWaitNs)) {
+        const int s = at % C::kStages;
+        if (at >= C::kStages && !mbar_wait(empty + s, (at / C::kStages - 1) & 1, kFewWaitNs)) {
           fail(kWherePagedEmpty);
           ok = false;
         }
@@ -437,26 +447,25 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           break;
         }
         if (lane == 0) {
-          page_bits[s] = bits;
+          if (kv == 0) page_bits[s] = bits;
           mbar_arrive_expect_tx(full + s, __popc(bits) * box_bytes);
         }
         __syncwarp();
         if (good) {
-          const uint32_t sk = smem_u32(smem + s * C::kStageBytes) + (lane << p.box_shift) * C::kPanelRow;
+          const uint32_t dst = smem_u32(smem + s * C::kStageBytes) + kv * 16384 + (lane << p.box_shift) * C::kPanelRow;
           const int slot = key0 & ((1 << a.b.page_shift) - 1);
 #pragma unroll
-          for (int pn = 0; pn < C::kPanels; ++pn) {
-            tma_load_4d(sk + pn * C::kPanelBytes, &kmap, full + s, pn * 64, h, slot, page);
-            tma_load_4d(sk + 16384 + pn * C::kPanelBytes, &vmap, full + s, pn * 64, h, slot, page);
-          }
+          for (int pn = 0; pn < C::kPanels; ++pn) tma_load_4d(dst + pn * C::kPanelBytes, map, full + s, pn * 64, h, slot, page);
         }
+        issued = at + 1;
       }
+      if (ok) it += n;
       wk.next(p, n);
     }
     if (!ok) {
       // Every copy issued has landed before the CTA ends.
-      for (int j = max(0, it - C::kStages); j < it; ++j)
-        mbar_wait(full + j % C::kStages, (j / C::kStages) & 1, kFewWaitNs);
+      for (int j = max(0, issued - C::kStages); j < issued; ++j)
+        if (j % C::kTurns == turn) mbar_wait(full + j % C::kStages, (j / C::kStages) & 1, kFewWaitNs);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     return;
