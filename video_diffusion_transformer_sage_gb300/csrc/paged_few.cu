@@ -436,27 +436,29 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         const bool good = need && page >= 0 && page < a.b.n_pages;
         if (need && !good) record_bad_index(a.status, kWherePage);
         const uint32_t bits = __ballot_sync(0xffffffffu, good);
+        // All that can be is done before the stage is free, and the copies go ahead of the bytes announced for them (the
+        // phase cannot end before this warp's arrival).
         const int s = at % C::kStages;
+        const uint32_t dst = smem_u32(smem + s * C::kStageBytes) + kv * 16384 + (lane << p.box_shift) * C::kPanelRow;
+        const uint32_t bytes = __popc(bits) * box_bytes;
+        const int slot = key0 & ((1 << a.b.page_shift) - 1);
+        const bool go = !s_abort;
         if (at >= C::kStages && !mbar_wait(empty + s, (at / C::kStages - 1) & 1, kFewWaitNs)) {
           fail(kWherePagedEmpty);
           ok = false;
         }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok || s_abort) {
-          ok = false;
-          break;
+        ok = __all_sync(0xffffffffu, ok && go);
+        if (!ok) break;
+        if (good) {
+#pragma unroll
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            tma_load_4d(dst + pn * C::kPanelBytes, map, full + s, pn * 64, h, slot, page);
         }
         if (lane == 0) {
           if (kv == 0) page_bits[s] = bits;
-          mbar_arrive_expect_tx(full + s, __popc(bits) * box_bytes);
+          mbar_arrive_expect_tx(full + s, bytes);
         }
         __syncwarp();
-        if (good) {
-          const uint32_t dst = smem_u32(smem + s * C::kStageBytes) + kv * 16384 + (lane << p.box_shift) * C::kPanelRow;
-          const int slot = key0 & ((1 << a.b.page_shift) - 1);
-#pragma unroll
-          for (int pn = 0; pn < C::kPanels; ++pn) tma_load_4d(dst + pn * C::kPanelBytes, map, full + s, pn * 64, h, slot, page);
-        }
         issued = at + 1;
       }
       if (ok) it += n;
