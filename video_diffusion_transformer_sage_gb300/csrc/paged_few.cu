@@ -12,7 +12,8 @@
 // CTA per SM (struct Walk), so ragged batches and single long sequences load every SM alike.  A CTA walks its tiles
 // through one ring of TMA stages that does not stop at unit borders.  A unit that lies in one CTA is finished
 // there.  Otherwise each CTA leaves (maximum, sum, O) of its part in the workspace and takes a ticket; the last
-// one joins the parts in the order of their keys, so the result does not depend on which CTA came last.
+// one joins the parts in the order of their keys, so the result does not depend on which CTA came last (paged_join.h
+// has the tickets' and slots' owners).
 //
 // Inside a CTA: two or four loading warps (page table entries by lane, one TMA box per page) and two teams of
 // four consumer warps that take the tiles in turn, a quarter of a tile's keys to each warp.  Each warp
@@ -37,8 +38,6 @@ constexpr int kFewConsumers = 256, kFewThreads = 384;
 constexpr int kFewRegsProducer = 40, kFewRegsConsumer = 232;
 static_assert(128 * kFewRegsProducer + 256 * kFewRegsConsumer <= kFewThreads * 168, "register split exceeds launch");
 constexpr uint64_t kFewWaitNs = 2000000000ull;
-// Parts take two slots per CTA from the front, joined groups one from the back.
-constexpr int kFewMaxCtas = (kPagedSlots - 1) / 3;
 constexpr float kFewRise = 8.0f;   // log2 of how far a maximum may fall behind
 
 template <int D, bool kE4M3, int MT>
@@ -133,12 +132,6 @@ __device__ __forceinline__ int draw_ticket(int32_t* counter, int n) {
   if (before != n - 1) return 0;
   *counter = 0;
   return 1;
-}
-// Parts of a group when more than 16 are joined: about the square root.
-__device__ __forceinline__ int group_size(int parts) {
-  int per = 5;
-  while (per * per < parts) ++per;
-  return per;
 }
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -327,7 +320,7 @@ struct Walk {
 // A part left in the workspace, its ticket drawn: joined at the CTA's end if it was its unit's last.
 struct Pending {
   int counter, count;                   // the ticket's counter and value that makes it the last
-  int first, cf, parts;                 // first part of its group; the unit's first row of CTAs and number of them
+  int first, cf, parts;                 // first part of its group; the unit's first row of CTAs and its parts
   int start, rows, h, qi;
 };
 
@@ -802,7 +795,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const bool whole_unit = wk.k == 0 && n == wk.w.nt;
     int cf = 0, parts = 1;
     if (!whole_unit) wk.unit_parts(p, cf, parts);
-    const int slot = blockIdx.x * 2 + (wk.k == 0 ? 1 : 0);
+    const int slot = join_part_slot(blockIdx.x, 1, 0, wk.k == 0);   // row * lock + col is the CTA's number
     const int live = min(R, wk.w.rows - qi * R);        // rows of the tile that exist
     const float vs = kE4M3 ? __ldg(a.v_scale + h) : 1.0f;
 #pragma unroll
@@ -873,13 +866,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       // The loop above ended with the CTA's barrier: thread 0's release covers every thread's stores.  Whether the part
       // was the last is looked at when the CTA's tiles are done, so its next unit does not wait for the ticket.
       if (tid == 0) {
-        // More than 16 parts (one sequence with few K/V heads over all SMs) are joined in groups first.
-        const int per = parts <= 16 ? parts : group_size(parts);
-        const int first = (static_cast<int>(blockIdx.x) / p.lock - cf) / per * per;
+        // More than 16 parts (one sequence with few K/V heads over many SMs) are joined in groups first.
+        const int groups = join_groups(parts), gr = join_group_of(parts, groups, static_cast<int>(blockIdx.x) / p.lock - cf);
+        const int first = join_first(parts, groups, gr);
         Pending& d = s_pending[wk.k == 0 ? 1 : 0];
-        d.counter = (cf + first) * p.lock + col;
+        d.counter = join_counter(cf + first, p.lock, col);
         d.first = first;
-        d.count = min(per, parts - first);
+        d.count = join_first(parts, groups, gr + 1) - first;
         d.cf = cf;
         d.parts = parts;
         d.start = wk.w.start;
@@ -943,17 +936,18 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
       }
     };
-    auto part_slot = [&](int q) { return ((cf + q) * p.lock + col) * 2 + (q == 0 ? 1 : 0); };
-    if (parts <= 16) {
+    auto part_slot = [&](int q) { return join_part_slot(cf + q, p.lock, col, q == 0); };
+    const int groups = join_groups(parts);
+    if (groups == 1) {
       join(parts, part_slot, -1);
     } else {
       // The group's parts into a slot of the group's; then, if that was the last group, the groups.
-      const int per = group_size(parts), first = e.first, groups = (parts + per - 1) / per;
-      join(e.count, [&](int q) { return part_slot(first + q); }, kPagedSlots - 1 - e.counter);
+      const int first = e.first;
+      join(e.count, [&](int q) { return part_slot(first + q); }, join_group_slot(cf + first, p.lock, col));
       consumer_sync();
-      if (tid == 0) s_last[d] = draw_ticket(a.counters + kPagedMaxCtas + cf * p.lock + col, groups);
+      if (tid == 0) s_last[d] = draw_ticket(a.counters + join_unit_counter(cf, p.lock, col), groups);
       consumer_sync();
-      if (s_last[d]) join(groups, [&](int q) { return kPagedSlots - 1 - ((cf + q * per) * p.lock + col); }, -1);
+      if (s_last[d]) join(groups, [&](int q) { return join_group_slot(cf + join_first(parts, groups, q), p.lock, col); }, -1);
     }
   }
 }

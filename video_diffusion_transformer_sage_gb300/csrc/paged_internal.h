@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "paged_join.h"
 #include "sage_internal.h"
 #include "sage_paged.h"
 
@@ -46,10 +47,8 @@ struct PagedAppendArgs {
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, int d, bool e4m3, cudaStream_t s);
 
-// The most CTAs whose partial results the workspace holds, and the rows of one partial result.
-constexpr int kPagedMaxCtas = 320;
+// The rows of one partial result.
 constexpr int kPagedChunkRows = 256;
-constexpr int kPagedSlots = 2 * kPagedMaxCtas;
 
 struct PagedAttnArgs {
   PagedBatchDev b;
