@@ -16,7 +16,7 @@
  * goes on with the rest as each entry point says, and the status block records SAGE_ERR_INVALID_ARG
  * with where = 16 (page table entry), 17 (length) or 18 (row of the rotary table), which
  * sage_check_device_status returns; the first one recorded stays until it is read.  A device wait that
- * expires is recorded as in sage.h (where = 19, 20 or 21).  Since lengths are read on the device, a captured CUDA graph
+ * expires is recorded as in sage.h (where = 19, 20 or 21), in the place of an index that was not read yet.  Since lengths are read on the device, a captured CUDA graph
  * may be replayed after they changed, as long as the buffers and n_tokens, n_seqs stay.
  */
 #ifndef SAGE_GB300_PAGED_H

@@ -47,6 +47,7 @@
 
 #include "sage_internal.h"
 #include "sm103_ptx.cuh"
+#include "status.cuh"
 #include "tensor_map.h"
 
 namespace sage {
@@ -127,7 +128,7 @@ struct AttnParams {
 };
 
 __device__ __forceinline__ void record_error(int32_t* status, int32_t where, volatile int* abort_flag) {
-  if (atomicCAS(status, 0, 1) == 0) status[1] = where;
+  record_timeout(status, where);
   *abort_flag = 1;
 }
 

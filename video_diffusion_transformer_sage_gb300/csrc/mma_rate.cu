@@ -21,6 +21,7 @@
 
 #include "sage_internal.h"
 #include "sm103_ptx.cuh"
+#include "status.cuh"
 
 namespace sage {
 namespace {
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(128, 1) mma_rate_kernel(int mode, int iters, i
         break;
     }
     tc_commit(&bar_done);
-    if (!mbar_wait(&bar_done, 0, limit) && atomicCAS(status, 0, 1) == 0) status[1] = kWhereDebugMma;
+    if (!mbar_wait(&bar_done, 0, limit)) record_timeout(status, kWhereDebugMma);
   }
   tc_fence_before();
   __syncthreads();

@@ -1,14 +1,10 @@
-// paged_batch.cuh -- device side: finding a token's sequence and its bounds, and the error record.
+// paged_batch.cuh -- device side: finding a token's sequence and its bounds.
 #pragma once
 #include "paged_internal.h"
 #include "sm103_ptx.cuh"
+#include "status.cuh"
 
 namespace sage {
-
-// The first bad index of a call stays recorded until the host reads it; nothing stops for it.
-__device__ __forceinline__ void record_bad_index(int32_t* status, int32_t where) {
-  if (atomicCAS(status, 0, kStatusBadIndex) == 0) status[1] = where;
-}
 
 // The rows of sequence b, [start, end), whatever cu_q holds: inside [0, n_tokens), never reversed.
 __device__ __forceinline__ void seq_rows(const PagedBatchDev& b, int s, int& start, int& end) {

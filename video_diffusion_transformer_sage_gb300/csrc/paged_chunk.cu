@@ -100,8 +100,8 @@ struct ChunkParams {
   uint32_t items;
 };
 
-__device__ __forceinline__ void record_timeout(int32_t* status, int32_t where, volatile int* abort_flag) {
-  if (atomicCAS(status, 0, kStatusTimeout) == 0) status[1] = where;
+__device__ __forceinline__ void give_up(int32_t* status, int32_t where, volatile int* abort_flag) {
+  record_timeout(status, where);
   *abort_flag = 1;
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
   // A bounded wait by a whole warp; records the first timeout.  False once anything timed out.
   auto wait = [&](uint64_t* bar, uint32_t parity, int where) {
     if (warp_wait(bar, parity)) return true;
-    if (lane == 0) record_timeout(a.status, where, &sh.abort);
+    if (lane == 0) give_up(a.status, where, &sh.abort);
     __syncwarp();
     return false;
   };
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
           bool ready = false;
           for (int n = 0; n < kItemWaits && !ready && !sh.abort; ++n) ready = warp_wait(draw, (k - 1) & 1);
           if (!ready) {
-            if (lane == 0) record_timeout(a.status, kWherePagedEmpty, &sh.abort);
+            if (lane == 0) give_up(a.status, kWherePagedEmpty, &sh.abort);
             __syncwarp();
             break;
           }
@@ -789,7 +789,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
           }
         }
       }
-      if (!ok && lane == 0) record_timeout(a.status, kWherePagedMma, &sh.abort);
+      if (!ok && lane == 0) give_up(a.status, kWherePagedMma, &sh.abort);
       __syncwarp();
       // Every MMA issued has finished before the tensor memory is freed.
       warp_tc_commit(mma_final);
@@ -818,7 +818,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
           if (ct >= S && (C::kSplitKV || kv == 0))
             ok = warp_wait((kv || !C::kSplitKV ? v_empty : k_empty) + s, (ct / S - 1) & 1);
           ok = ok && warp_wait(raw_full + kv, ct & 1);
-          if (!ok) record_timeout(a.status, kWherePagedFull, &sh.abort);
+          if (!ok) give_up(a.status, kWherePagedFull, &sh.abort);
           ok = !__any_sync(0xffffffffu, !ok || sh.abort);
           if (!ok) break;
           const uint32_t bits = sh.raw_bits[kv];
@@ -971,7 +971,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
           __syncwarp();
         }, i == 0, m, l, s_free + t, pv_done + t, static_cast<int>(mine) + i);
         if (!ok) {
-          if (lane == 0) record_timeout(a.status, kWherePagedMma, &sh.abort);
+          if (lane == 0) give_up(a.status, kWherePagedMma, &sh.abort);
           break;
         }
         tc_fence_before();

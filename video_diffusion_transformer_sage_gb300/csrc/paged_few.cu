@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (s_skip) return;   // an earlier wait ran out: no work until the status has been read
 
   auto fail = [&](int where) {
-    if (atomicCAS(a.status, 0, kStatusTimeout) == 0) a.status[1] = where;
+    record_timeout(a.status, where);
     s_abort = 1;
   };
 

@@ -10,9 +10,6 @@
 
 namespace sage {
 
-// status[0] of a status block: 1 = a device wait expired (every later call on the block skips its
-// work), kStatusBadIndex = an index from device memory was out of range (nothing is skipped).
-constexpr int32_t kStatusTimeout = 1, kStatusBadIndex = 2;
 enum PagedWhere : int32_t { kWherePage = 16, kWhereLength = 17, kWhereRopeRow = 18, kWherePagedFull = 19,
                             kWherePagedEmpty = 20, kWherePagedMma = 21 };
 

@@ -7,7 +7,6 @@
 #include <cstdint>
 #include <cstring>
 
-#include "paged_internal.h"
 #include "sage_internal.h"
 
 namespace {

@@ -7,8 +7,11 @@
 
 namespace sage {
 
-// Device-side status codes recorded in the status block (first int32: nonzero on error,
-// second int32: where the error was detected).
+// First int32 of a status block: 1 = a device wait expired (every later call on the block skips its
+// work), kStatusBadIndex = an index from device memory was out of range (a paged call: nothing is skipped).
+constexpr int32_t kStatusTimeout = 1, kStatusBadIndex = 2;
+
+// Second int32 of a status block: where the error was detected.
 enum DeviceWhere : int32_t {
   kWhereNone = 0,
   kWhereQFull = 1,
