@@ -121,7 +121,8 @@ size_t sage_paged_workspace_bytes(int64_t head_dim);
  * over the visible positions j of the token's sequence, K / V head h / (n_heads_q / n_heads):
  *   causal 0: all of [0, kv_len);   causal 1: those up to the token's own position pos;
  *   window > 0 (with causal 1 only): of those the last `window`, j > pos - window.
- * A row that sees no key becomes 0, its lse -infinity.  Scores, maxima, sums and accumulators are fp32;
+ * A row that sees no key becomes 0, its lse -infinity; any other whose q holds a NaN becomes NaN, and its lse too.
+ * Scores, maxima, sums and accumulators are fp32;
  * p is rounded to bf16 for the product with V, as in sage_attn_dense_bf16_tc, or to fp16 with an E4M3
  * cache (whose codes fp16 holds exactly; q is then held as fp16 times a power of two per row).  Against a running
  * maximum that may lag by 2^8, p lies in [0, 2^8].  Per element, |out - exact| <= 2^-7 sum_j w_j |v_j| + 2^-8 |out|

@@ -1,5 +1,7 @@
-// paged_batch.cuh -- device side: finding a token's sequence and its bounds.
+// paged_batch.cuh -- device side: finding a token's sequence and its bounds; a row's log-sum-exp.
 #pragma once
+#include <cmath>
+
 #include "paged_internal.h"
 #include "sm103_ptx.cuh"
 #include "status.cuh"
@@ -29,6 +31,12 @@ __device__ __forceinline__ int find_seq(const PagedBatchDev& b, int t) {
     if (step == 1) break;
   }
   return t < __ldg(b.cu_q + lo + 1) ? lo : -1;
+}
+
+// A row's natural log-sum-exp of its maximum (log2 units) and sum: -infinity for a row that saw no key (l = 0), NaN where
+// its scores are no numbers.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : l == 0.0f ? -INFINITY : l;
 }
 
 }  // namespace sage

@@ -382,10 +382,6 @@ __device__ __forceinline__ bool softmax_step(uint32_t tS, uint32_t tO, uint32_t 
   return true;
 }
 
-__device__ __forceinline__ float lse_of(float m, float l) {
-  return l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-}
-
 // What the roles of a CTA share.
 struct ChunkShared {
   Unit unit[2];                    // the items in work and next

@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   };
   auto store_lse = [&](int start, int h, int qi, int r, float mm, float ll) {
     const int rr = qi * R + r, tok = rr / p.group, hq = h * p.group + rr % p.group;
-    a.lse[static_cast<int64_t>(start + tok) * a.hq + hq] = ll > 0.0f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+    a.lse[static_cast<int64_t>(start + tok) * a.hq + hq] = lse_of(mm, ll);
   };
   int it = 0;
   for (int seg = 0; wk.at < wk.end; ++seg) {
@@ -852,7 +852,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             v.w = fmaf(y.w, f[w], v.w);
           }
           if (whole_unit) {
-            store4(wk.w.start, h, qi, r, d4, ll > 0.0f ? vs / ll : 0.0f, v.x, v.y, v.z, v.w);
+            store4(wk.w.start, h, qi, r, d4, ll > 0.0f ? vs / ll : ll, v.x, v.y, v.z, v.w);
             if (a.lse && d4 == 0) store_lse(wk.w.start, h, qi, r, mm, ll);
           } else {
             *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(slot) * R + r) * D + d4) = v;
@@ -916,9 +916,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           }
 #pragma unroll
           for (int q = 0; q < kAhead; ++q) {
-            const float mn = fmaxf(mm, ml[q].x);
-            if (mn == -INFINITY) continue;        // no key so far
-            const float f0 = ex2_approx(mm - mn), f1 = ex2_approx(ml[q].x - mn);
+            // No key so far: both factors are 0, and what is added is 0, or NaN where a part's scores are no numbers.
+            const float mn = fmaxf(mm, ml[q].x), base = mn == -INFINITY ? 0.0f : mn;
+            const float f0 = ex2_approx(mm - base), f1 = ex2_approx(ml[q].x - base);
             ll = ll * f0 + ml[q].y * f1;
             v.x = v.x * f0 + x[q].x * f1;
             v.y = v.y * f0 + x[q].y * f1;
@@ -931,7 +931,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(to) * R + r) * D + d4) = v;
           if (d4 == 0) a.part_ml[to * R + r] = make_float2(mm, ll);
         } else {
-          store4(e.start, e.h, e.qi, r, d4, ll > 0.0f ? vs / ll : 0.0f, v.x, v.y, v.z, v.w);
+          store4(e.start, e.h, e.qi, r, d4, ll > 0.0f ? vs / ll : ll, v.x, v.y, v.z, v.w);
           if (a.lse && d4 == 0) store_lse(e.start, e.h, e.qi, r, mm, ll);
         }
       }
