@@ -122,13 +122,14 @@ size_t sage_paged_workspace_bytes(int64_t head_dim);
  *   causal 0: all of [0, kv_len);   causal 1: those up to the token's own position pos;
  *   window > 0 (with causal 1 only): of those the last `window`, j > pos - window.
  * A row that sees no key becomes 0, its lse -infinity; any other whose q holds a NaN becomes NaN, and its lse too.
- * Scores, maxima, sums and accumulators are fp32;
- * p is rounded to bf16 for the product with V, as in sage_attn_dense_bf16_tc, or to fp16 with an E4M3
- * cache (whose codes fp16 holds exactly; q is then held as fp16 times a power of two per row).  Against a running
- * maximum that may lag by 2^8, p lies in [0, 2^8].  Per element, |out - exact| <= 2^-7 sum_j w_j |v_j| + 2^-8 |out|
- * plus fp32 rounding, w the exact weights.  Stored K and V of a sequence's visible range must be finite (a NaN in a
- * value that only some of the rows see may reach the others).  Key positions whose page entry is out of
- * range are left out, as masked ones.
+ * Scores, maxima, sums and accumulators are fp32; p is rounded to bf16 for the product with V, as in
+ * sage_attn_dense_bf16_tc, or to fp16 with an E4M3 cache (whose codes fp16 holds exactly; q is then held as fp16
+ * times a power of two per row).  Against a running maximum that may lag by 2^8, p lies in [0, 2^8] (fp16: times
+ * 2^7).  Per element, |out - exact| <= 2^-7 sum_j w_j |v_j| + 2^-8 |out| plus fp32 rounding, w the exact weights; with
+ * an E4M3 cache plus 2^-32 (sum_j |v_j| + n |out|) over the n visible keys, the steps of fp16's subnormals, which
+ * p reaches at 2^-21 of the row's largest.  Stored K and V of a sequence's visible range must be finite (a NaN in a
+ * value that only some of the rows see may reach the others).  Key positions whose page entry is
+ * out of range are left out, as masked ones.
  *   q            bf16 [n_tokens, n_heads_q, head_dim] view; n_heads_q a multiple of the cache's
  *                n_heads, at most 128 times as many.
  *   out          bf16, element (t, h, c) at out[t * out_stride_token + h * out_stride_head + c],

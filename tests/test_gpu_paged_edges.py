@@ -1,7 +1,10 @@
 """The paged K/V cache on the GPU where its arithmetic or its records could go wrong."""
+import math
+
 import pytest
 import torch
 
+import paged_ref
 import video_diffusion_transformer_sage_gb300 as sage
 from paged_ref import Problem
 
@@ -33,6 +36,33 @@ def test_a_query_row_of_no_numbers_gives_none(lens, fmt):
     assert bool(out[t, h].isnan().all()) and bool(lse[t, h].isnan())
     out[t, h], lse[t, h] = clean[t, h], clean_lse[t, h]
     assert torch.equal(out, clean) and torch.equal(lse, clean_lse)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("q_len,d,kv", [(1, 64, 60), (1, 128, 30), (9, 64, 60), (70, 64, 100), (70, 128, 100), (300, 128, 100)])
+@pytest.mark.parametrize("low", [14, 22])
+def test_weights_far_below_the_largest_keep_their_precision(q_len, d, kv, fmt, low):
+    """A first key that takes nearly all the weight and has no value: what is left is the sum over keys whose weights are
+    2^-low of the largest and less.  It keeps the bound of every other case."""
+    p = Problem([q_len], [kv], 2, 2, d, 64, fmt, seed=61)
+    page = int(p.table[0, 0]), int(p.table[0, 1]) if kv > 64 else 0
+    k = torch.zeros((kv, 2, d), device=p.dev)
+    # with q = 1, sm_scale = ln 2 and unit scales, the base-2 score of a key is the sum of its channels
+    k[1:, :, :low // 2] = -2.0
+    k[1:, :, d - 1] = -0.125 * (torch.arange(1, kv, device=p.dev) % 8)[:, None]
+    for i in range(kv):
+        p.k_pages[page[i // 64], i % 64] = k[i].to(p.k_pages.dtype)
+    p.v_pages[page[0], 0] = torch.zeros((2, d), device=p.dev).to(p.v_pages.dtype)
+    if fmt == "e4m3":
+        p.k_scale.fill_(1.0)
+    q = torch.ones((q_len, 2, d), dtype=torch.bfloat16, device=p.dev)
+    cache, batch = _handles(p)
+    lse = torch.zeros((q_len, 2), dtype=torch.float32, device=p.dev)
+    out = sage.sage_paged_attn(q, cache, batch, sm_scale=math.log(2.0), causal=False, lse=lse)
+    ref = paged_ref.attention(p, q, False, sm_scale=math.log(2.0))
+    assert float(ref[0].abs().max()) < 2.0 ** (4 - low) * 64       # nothing but the small weights
+    paged_ref.check_attention(p, out, ref, sm_scale=math.log(2.0))
+    assert float((lse.double() - ref[1]).abs().max()) <= 1.01 * 2.0 ** -8
 
 
 def test_a_timeout_replaces_a_bad_index_that_nobody_read():

@@ -12,8 +12,8 @@
 // as in attn_fwd.cu (Q tiles in turn, so one tile's softmax overlaps the other's MMAs).  A unit of at most 128
 // rows has one Q tile; its key tiles then go to the two slots t in turn, each with a maximum, sum and O of its
 // own, joined at the end: the same overlap, and half the steps.  O is rescaled only
-// when a row's maximum rises by more than 2^8 (P then stays below 2^8, far inside both 16-bit types
-// and fp32): the result is the same ratio, and most tiles rescale nothing.
+// when a row's maximum rises by more than 2^8 (P then stays below 2^8, or 2^15 where it is lifted for fp16, inside
+// both 16-bit types and fp32): the result is the same ratio, and most tiles rescale nothing.
 //
 // bf16 cache: bf16 operands, one TMA box per page and 64 channels, straight into the swizzled tiles.
 // E4M3 cache: the codes come by TMA into a staging tile and one warpgroup widens them to fp16 (exact) in
@@ -313,11 +313,12 @@ __device__ __forceinline__ bool softmax_step(uint32_t tS, uint32_t tO, uint32_t 
     for (int k = 0; k < 128; ++k)
       if (!((mask[k >> 5] >> (k & 31)) & 1u)) sr[k] = 0xFF800000u;   // -infinity
   }
-  const float mx = fmaxf(max64(sr), max64(sr + 64)) * c;
-  const bool up = mx > m + kRise;          // also the first visible key: m is -infinity before it
-  const float alpha = (up && !first) ? ex2_approx(m - mx) : 1.0f;
+  constexpr float kLift = kE4M3 ? kLiftE4M3 : 0.0f;
+  const float mx = fmaxf(max64(sr), max64(sr + 64)) * c, lower = mx - kLift;
+  const bool up = mx > m + (kRise + kLift);   // also the first visible key: m is -infinity before it
+  const float alpha = (up && !first) ? ex2_approx(m - lower) : 1.0f;
   const bool rise = up && !first;
-  if (up) m = mx;
+  if (up) m = lower;
   const float base = m == -INFINITY ? 0.0f : m;   // no key so far: every P below is 0
   const uint64_t bias2 = f2_pack(-base, -base), c2 = f2_pack(c, c);
   uint64_t l2[4][2];

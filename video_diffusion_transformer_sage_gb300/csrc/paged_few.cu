@@ -660,8 +660,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             seen_bits |= (in ? 1u : 0u) << (t * 2 + j);
           }
       }
-      // The maximum moves only when it rises by more than 2^8 (P stays below 2^8, the ratio is the same), so O is
-      // rarely rescaled.
+      // The maximum moves only when it rises by more than 2^8 (P stays below 2^8, or 2^15 where it is lifted; the ratio is
+      // the same), so O is rarely rescaled.
+      constexpr float kLift = kE4M3 ? kLiftE4M3 : 0.0f;
       bool rise = false;
       float al[MT][2];
 #pragma unroll
@@ -683,10 +684,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           for (int t = 1; t < C::kNT; ++t) mx = fmax3(mx, x[mt][t][e * 2], x[mt][t][e * 2 + 1]);
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * sc[mt][e];
-          const bool up = mx > m[mt][e] + kFewRise;          // also the first visible key
-          al[mt][e] = up ? ex2_approx(m[mt][e] - mx) : 1.0f;
+          const bool up = mx > m[mt][e] + (kFewRise + kLift);   // also the first visible key
+          const float lower = mx - kLift;
+          al[mt][e] = up ? ex2_approx(m[mt][e] - lower) : 1.0f;
           rise |= up;
-          if (up) m[mt][e] = mx;
+          if (up) m[mt][e] = lower;
           const float base = m[mt][e] == -INFINITY ? 0.0f : m[mt][e];   // no key so far: every p below is 0
 #pragma unroll
           for (int t = 0; t < C::kNT; ++t) {
