@@ -84,3 +84,50 @@ def test_a_timeout_replaces_a_bad_index_that_nobody_read():
     p2 = Problem([2], [20], 2, 2, 64, 8, seed=62)
     cache, batch = _handles(p2)
     assert torch.equal(sage.sage_paged_attn(p2.q, cache, batch, ws=ws), want)
+
+
+def test_a_record_is_not_erased_by_the_blocks_making():
+    """The cache's status block is needed first by a call on a busy stream; a record of a call on another stream, which
+    runs before that, stays."""
+    p = Problem([2], [20], 2, 2, 64, 8, seed=63)
+    busy, idle = torch.cuda.Stream(), torch.cuda.Stream()
+    bad = sage.PagedBatch(p.cu_q, p.kv_len, torch.full_like(p.table, p.n_pages))
+    work = torch.randn((6000, 6000), device="cuda")
+    torch.cuda.synchronize()
+    for given in (busy, busy.cuda_stream):
+        cache, batch = _handles(p)
+        with torch.cuda.stream(busy):
+            for _ in range(8):
+                work = work @ work * 1e-4
+        sage.sage_paged_append(p.k, p.v, cache, batch, stream=given)
+        sage.sage_paged_append(p.k, p.v, cache, bad, stream=idle)
+        idle.synchronize()
+        torch.cuda.synchronize()
+        assert sage.sage_check_device_status(cache.status) == (1, 16)
+        assert sage.sage_check_device_status(cache.status) == (0, 0)
+
+
+def test_a_block_made_in_a_graph_capture_is_ready_and_keeps_its_records():
+    """The first call of a cache is captured: the block is zeros before any replay, and replays do not erase what others
+    recorded; a replay's own bad index is recorded."""
+    p = Problem([2], [20], 2, 2, 64, 8, seed=64)
+    warm, _ = _handles(p)
+    cache, batch = _handles(p)
+    sage.sage_paged_append(p.k, p.v, warm, batch)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sage.sage_paged_append(p.k, p.v, cache, batch)
+    assert sage.sage_check_device_status(cache.status) == (0, 0)
+    bad = sage.PagedBatch(p.cu_q, p.kv_len, torch.full_like(p.table, -1))
+    sage.sage_paged_append(p.k, p.v, cache, bad)
+    graph.replay()
+    assert sage.sage_check_device_status(cache.status) == (1, 16)
+    before = p.k_pages.clone()
+    p.k_pages.fill_(0)
+    graph.replay()
+    assert sage.sage_check_device_status(cache.status) == (0, 0)
+    assert torch.equal(p.k_pages[int(p.table[0, 2]), 2:4], before[int(p.table[0, 2]), 2:4])
+    p.table.fill_(p.n_pages)
+    graph.replay()
+    assert sage.sage_check_device_status(cache.status) == (1, 16)

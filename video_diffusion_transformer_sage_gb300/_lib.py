@@ -372,11 +372,24 @@ def sage_smooth_quant_qk_rmsnorm_rope(q: torch.Tensor, k: torch.Tensor, gamma_q:
 
 
 # ------------------------------------------------------------------- paged K/V cache (include/sage_paged.h)
+@contextlib.contextmanager
+def _capture_apart():
+    """What this thread enqueues and waits for on streams that are not captured does not end a capture on another one
+    (cuThreadExchangeStreamCaptureMode: relaxed)."""
+    mode, driver = ctypes.c_int(2), ctypes.CDLL("libcuda.so.1")
+    if driver.cuThreadExchangeStreamCaptureMode(ctypes.byref(mode)) != 0:
+        raise RuntimeError("cuThreadExchangeStreamCaptureMode failed")
+    try:
+        yield
+    finally:
+        driver.cuThreadExchangeStreamCaptureMode(ctypes.byref(mode))
+
+
 class PagedKV:
     """A paged K/V cache over the caller's page tensors [n_pages, page_size, n_heads, head_dim] (any page,
     slot and head strides, unit channel stride): bf16, or torch.float8_e4m3fn with fp32 scales
     k_scale and v_scale [n_heads].  `status` is the block that sage_paged_append records bad indices in
-    (read it with sage_check_device_status)."""
+    (read it with sage_check_device_status); it is made when first needed and may be used on any stream."""
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
                  v_scale: Optional[torch.Tensor] = None):
@@ -397,7 +410,7 @@ class PagedKV:
                 raise ValueError(f"expected contiguous fp32 scales of shape ({h},) on the pages' device")
         self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
         self.n_pages, self.page_size, self.n_heads, self.head_dim = n, ps, h, d
-        self.device, self._status = k_pages.device, None
+        self.device, self._status, self._status_streams = k_pages.device, None, set()
         self._c = SagePagedKVC(k_pages.data_ptr(), v_pages.data_ptr(), n, ps, h, d, *k_pages.stride()[:3],
                                *v_pages.stride()[:3], 1 if e4m3 else 0, k_scale.data_ptr() if e4m3 else None,
                                v_scale.data_ptr() if e4m3 else None)
@@ -406,8 +419,24 @@ class PagedKV:
     @property
     def status(self) -> torch.Tensor:
         if self._status is None:
-            self._status = status_block(self.device)
+            # Zeroed before this returns, on a stream of its own: no call on whatever stream comes before that, and inside
+            # a graph capture the zeroing is no part of the graph, whose replays would erase records.
+            side = torch.cuda.Stream(self.device)
+            with _capture_apart():
+                with torch.cuda.stream(side):
+                    status = status_block(self.device)
+                side.synchronize()
+            self._status = status
         return self._status
+
+    def _status_on(self, stream) -> torch.Tensor:
+        """The block for a call on `stream`, whose kernels may outlive the cache."""
+        status = self.status
+        raw = torch._C._cuda_getCurrentRawStream(self.device.index) if stream is None else _stream(stream)
+        if raw not in self._status_streams:
+            self._status_streams.add(raw)
+            status.record_stream(torch.cuda.ExternalStream(raw, device=self.device))
+        return status
 
 
 class PagedBatch:
@@ -512,10 +541,7 @@ def sage_paged_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKV, batch: P
                                   or not positions.is_contiguous() or positions.device != dev):
         raise ValueError("positions: expected a contiguous int32 tensor [N] on the cache's device")
     if status is None:
-        status = cache._status
-        if status is None:
-            with _made_on(stream, dev):
-                status = cache.status
+        status = cache._status_on(stream)
     elif status.device != dev or status.nbytes < 256:
         raise ValueError("status: expected a zeroed block of 256 bytes on the cache's device")
     rows = rope_cos.shape[0] if rope_cos is not None else 0
