@@ -87,7 +87,8 @@ typedef struct sage_paged_batch {
  *   Q: bf16_rn(z) to q_out.
  * With gamma, a table and a bf16 cache, the values are those of sage_qk_rmsnorm_rope bit for bit.
  *   q               bf16 [n_tokens, n_heads_q, head_dim] view, or NULL: K and V alone; its head
- *                   count is its own.  q_out, with its own strides, may be q's own memory.
+ *                   count is its own.  q_out has its own strides; it may be q itself, then with q's strides, and
+ *                   otherwise overlaps none of the inputs.
  *   k, v            bf16 [n_tokens, cache n_heads, head_dim] views.
  *   gamma_q/_k      device fp32 [head_dim] or NULL (no norm of that operand).
  *   rope_cos/_sin   device fp32 [rope_rows][head_dim / 2], both or neither (no rotation).  For a rotation of

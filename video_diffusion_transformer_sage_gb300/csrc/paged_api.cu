@@ -106,6 +106,10 @@ sage_status sage_paged_append(const sage_view* q, const sage_view* k, const sage
   if (q) {
     if ((st = check_rows(q, n, d)) != SAGE_OK) return st;
     if (n > 0 && (st = check_target(q_out, q_out_stride_token, q_out_stride_head, q)) != SAGE_OK) return st;
+    // In q's own memory each row may only go where it came from: another warp's row could be overwritten unread.
+    if (n > 0 && q_out == q->data &&
+        ((n > 1 && q_out_stride_token != q->stride_token) || (q->n_heads > 1 && q_out_stride_head != q->stride_head)))
+      return SAGE_ERR_INVALID_ARG;
   }
   if ((rope_cos == nullptr) != (rope_sin == nullptr) || (rope_cos && rope_rows <= 0)) return SAGE_ERR_INVALID_ARG;
   if (!(eps >= 0.0f) || !(eps < INFINITY)) return SAGE_ERR_INVALID_ARG;
