@@ -66,7 +66,8 @@ typedef struct sage_paged_kv {
  *               page of positions i * page_size .. (i + 1) * page_size - 1 of sequence b.  Only entries of
  *               pages that a call stores to or sees a key of are read, so pages before a sliding
  *               window may be given back.  Sequences may share pages that are only read.
- *               max_pages * page_size is at most 2^30; a kv_len above it is taken as that many. */
+ *               max_pages * page_size is at most 2^30.  Of a kv_len above it sage_paged_append stores no
+ *               position past the table, and sage_paged_attn takes it as that many tokens. */
 typedef struct sage_paged_batch {
   int64_t n_seqs;
   const int32_t* cu_q;
@@ -80,7 +81,8 @@ typedef struct sage_paged_batch {
  * sage_qk_rmsnorm_rope on the way: per token and head, in fp32 with every product and sum rounded on
  * its own and in that entry point's order,
  *   y = (x / sqrt(mean x^2 + eps)) * gamma   where gamma is given,
- *   z_2i = y_2i cos_i - y_2i+1 sin_i,  z_2i+1 = y_2i sin_i + y_2i+1 cos_i   where the table is given.
+ *   z_2i = y_2i cos_i - y_2i+1 sin_i,  z_2i+1 = y_2i sin_i + y_2i+1 cos_i   where the table is given
+ *   (neighbouring channels are a pair; weights made for pairs (i, i + head_dim / 2) need their rows reordered first).
  *   K: stored as bf16_rn(z), or as the E4M3 code (round to nearest even, saturating) of
  *      fl32(z * fl32(1 / k_scale[h])), z itself not rounded to bf16 first.
  *   V: stored as it is, or as the E4M3 code of fl32(v * fl32(1 / v_scale[h])).

@@ -520,7 +520,7 @@ def sage_paged_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKV, batch: P
     """New tokens' K and V [N, n_heads, D] into the cache, after the optional per-head RMSNorm (gamma_q,
     gamma_k: fp32 [D]) and rotation (rope_cos, rope_sin: fp32 [rows, D / 2]; row = position in the
     sequence, or positions[t], int32) of Q and K.  Returns Q so treated (q_out, made here when None; it
-    may be q itself), or None without q."""
+    may be q itself, then with q's strides), or None without q."""
     d, dev = cache.head_dim, cache.device
     vk, vv = _paged_view(k, d, dev, "k"), _paged_view(v, d, dev, "v")
     if batch.device != dev:
@@ -558,7 +558,7 @@ def sage_paged_attn(q: torch.Tensor, cache: PagedKV, batch: PagedBatch, sm_scale
                     causal: bool = True, window: Optional[int] = None, out: Optional[torch.Tensor] = None,
                     lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Attention of the batch's new tokens q [N, Hq, D] over the cache: all stored tokens of their sequence
-    (causal False), those up to their own position, or the last `window` of these.  lse: optional fp32
+    (causal False), those up to their own position, or the last `window` of these (None or 0: all).  lse: optional fp32
     [N, Hq], receives the log of the sum of exponentials.  ws: a paged_workspace (made here when None)."""
     d, dev = cache.head_dim, cache.device
     vq = _paged_view(q, d, dev, "q")
