@@ -67,7 +67,7 @@ typedef struct sage_paged_kv {
  *               pages that a call stores to or sees a key of are read, so pages before a sliding
  *               window may be given back.  Sequences may share pages that are only read.
  *               max_pages * page_size is at most 2^30.  Of a kv_len above it sage_paged_append stores no
- *               position past the table, and sage_paged_attn takes it as that many tokens. */
+ *               position past the table, and sage_paged_attn takes it as max_pages * page_size. */
 typedef struct sage_paged_batch {
   int64_t n_seqs;
   const int32_t* cu_q;
