@@ -20,6 +20,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libsage_gb300.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "sage.h")
 PAGED_HEADER = os.path.join(os.path.dirname(_HERE), "include", "sage_paged.h")
+TREE_HEADER = os.path.join(os.path.dirname(_HERE), "include", "sage_paged_tree.h")
 PAGED_WS_HEADER = 4096   # SAGE_PAGED_WS_HEADER: the bytes of a paged workspace that start as zeros
 
 STATUS = {0: "SAGE_OK", 1: "SAGE_ERR_INVALID_ARG", 2: "SAGE_ERR_ALIGNMENT", 3: "SAGE_ERR_UNSUPPORTED",
@@ -64,8 +65,13 @@ class SagePagedBatchC(ctypes.Structure):
                 ("page_table", ctypes.c_void_p), ("max_pages", ctypes.c_int64), ("table_stride", ctypes.c_int64)]
 
 
+class SagePagedTreeMaskC(ctypes.Structure):
+    _fields_ = [("mask", ctypes.c_void_p), ("mask_words", ctypes.c_int64), ("mask_stride", ctypes.c_int64),
+                ("depth", ctypes.c_void_p)]
+
+
 def header_functions(header: str = HEADER) -> list:
-    """Names of the functions a header (include/sage.h, or PAGED_HEADER) declares."""
+    """Names of the functions a header (include/sage.h, PAGED_HEADER, TREE_HEADER) declares."""
     text = open(header).read()
     return sorted(set(re.findall(r"^\s*(?:const\s+)?[a-z_0-9]+\**\s+\**(sage_[a-z_0-9]+)\s*\(", text, re.M)))
 
@@ -80,6 +86,7 @@ def lib():
         VP = ctypes.POINTER(SageView)
         QP = ctypes.POINTER(SageQuantizedC)
         KP, BP = ctypes.POINTER(SagePagedKVC), ctypes.POINTER(SagePagedBatchC)
+        TP = ctypes.POINTER(SagePagedTreeMaskC)
         sig = {
             "sage_status_string": ([ctypes.c_int], ctypes.c_char_p),
             "sage_quant_scratch_bytes": ([I, I, I], S),
@@ -104,6 +111,8 @@ def lib():
             "sage_paged_append": ([VP, VP, VP, P, P, P, P, I, P, F, KP, BP, P, I, I, P, P], ctypes.c_int),
             "sage_paged_workspace_bytes": ([I], S),
             "sage_paged_attn": ([VP, KP, BP, F, I, I, P, I, I, P, P, S, P], ctypes.c_int),
+            "sage_paged_tree": ([BP, I, P, I, TP, P, P, P], ctypes.c_int),
+            "sage_paged_attn_tree": ([VP, KP, BP, TP, F, I, P, I, I, P, P, S, P], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -554,12 +563,8 @@ def sage_paged_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKV, batch: P
     return q_out
 
 
-def sage_paged_attn(q: torch.Tensor, cache: PagedKV, batch: PagedBatch, sm_scale: Optional[float] = None,
-                    causal: bool = True, window: Optional[int] = None, out: Optional[torch.Tensor] = None,
-                    lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """Attention of the batch's new tokens q [N, Hq, D] over the cache: all stored tokens of their sequence
-    (causal False), those up to their own position, or the last `window` of these (None or 0: all).  lse: optional fp32
-    [N, Hq], receives the log of the sum of exponentials.  ws: a paged_workspace (made here when None)."""
+def _paged_attn_call(q, cache, batch, between, out, lse, ws, stream, what) -> torch.Tensor:
+    """The attention calls: `between` stands between the batch and the output."""
     d, dev = cache.head_dim, cache.device
     vq = _paged_view(q, d, dev, "q")
     if batch.device != dev:
@@ -578,9 +583,83 @@ def sage_paged_attn(q: torch.Tensor, cache: PagedKV, batch: PagedBatch, sm_scale
             ws = paged_workspace(d, dev)
     elif ws.device != dev:
         raise ValueError("ws lies on another device than the cache")
-    sm_scale = 1.0 / math.sqrt(d) if sm_scale is None else sm_scale
-    _check(_paged_call(dev, stream, lib().sage_paged_attn, (
-        ctypes.byref(vq), cache._ref, batch._ref, sm_scale, 1 if causal else 0, window or 0, vo.data, vo.stride_token,
-        vo.stride_head, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes)),
-        "sage_paged_attn")
+    _check(_paged_call(dev, stream, getattr(lib(), what), (
+        ctypes.byref(vq), cache._ref, batch._ref, *between, vo.data, vo.stride_token,
+        vo.stride_head, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes)), what)
     return out
+
+
+def sage_paged_attn(q: torch.Tensor, cache: PagedKV, batch: PagedBatch, sm_scale: Optional[float] = None,
+                    causal: bool = True, window: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of the batch's new tokens q [N, Hq, D] over the cache: all stored tokens of their sequence
+    (causal False), those up to their own position, or the last `window` of these (None or 0: all).  lse: optional fp32
+    [N, Hq], receives the log of the sum of exponentials.  ws: a paged_workspace (made here when None)."""
+    sm_scale = 1.0 / math.sqrt(cache.head_dim) if sm_scale is None else sm_scale
+    return _paged_attn_call(q, cache, batch, (sm_scale, 1 if causal else 0, window or 0), out, lse, ws, stream,
+                            "sage_paged_attn")
+
+
+# ------------------------------------------------------------------- drafted trees (include/sage_paged_tree.h)
+class PagedTree:
+    """Which new tokens each row of a call sees: int32 CUDA tensors mask [N, words] (bit i % 32 of word i / 32: the row sees
+    new token i of its sequence), depth [N] (its ancestors; needed with a window) and positions [N] (for sage_paged_append).
+    sage_paged_tree fills all three from the tokens' parents."""
+
+    def __init__(self, mask: torch.Tensor, depth: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None):
+        if mask.dim() != 2 or mask.dtype != torch.int32 or not mask.is_cuda or mask.shape[1] < 1:
+            raise ValueError("mask: expected an int32 CUDA tensor [N, words]")
+        n, words = mask.shape
+        if words > 1 and mask.stride(1) != 1:
+            raise ValueError("mask's rows must be contiguous")
+        for t in (depth, positions):
+            if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != (n,) or not t.is_contiguous()
+                                  or t.device != mask.device):
+                raise ValueError(f"depth and positions: expected contiguous int32 tensors ({n},) on the mask's device")
+        self.mask, self.depth, self.positions, self.n_tokens, self.device = mask, depth, positions, n, mask.device
+        self._c = SagePagedTreeMaskC(mask.data_ptr(), words, mask.stride(0), None if depth is None else depth.data_ptr())
+        self._ref = ctypes.byref(self._c)
+
+
+def sage_paged_tree(parents: torch.Tensor, batch: PagedBatch, tree: Optional[PagedTree] = None, *, status: torch.Tensor,
+                    window: Optional[int] = None, words: Optional[int] = None, stream=None) -> PagedTree:
+    """The tree of each sequence's new tokens from `parents`, int32 [N]: the parent's number among the sequence's new
+    tokens, before the token's own, or -1 for one that continues the cached text.  Fills `tree`, or a new one of `words`
+    words a row (32 tokens each).  window: that of the attention (ancestors further up are not seen).  status: a block or a
+    workspace that records bad indices."""
+    n, dev = parents.shape[0] if parents.dim() == 1 else -1, batch.device
+    if n < 0 or parents.dtype is not _I32 or parents.device != dev or not parents.is_contiguous():
+        raise ValueError("parents: expected a contiguous int32 tensor [N] on the batch's device")
+    if tree is None:
+        if words is None:
+            raise ValueError("words (of 32 tokens each, enough for the longest sequence's new tokens) or tree has to be given")
+        with _made_on(stream, dev):
+            tree = PagedTree(torch.empty((n, words), dtype=torch.int32, device=dev),
+                             *(torch.empty(n, dtype=torch.int32, device=dev) for _ in range(2)))
+    elif words is not None:
+        raise ValueError("words belongs to a tree that is made here")
+    if tree.n_tokens != n or tree.device != dev:
+        raise ValueError("tree must have the rows of parents, on the same device")
+    if status.device != dev or status.nbytes < 256:
+        raise ValueError("status: expected a zeroed block of 256 bytes on the batch's device")
+    positions = tree.positions
+    _check(_paged_call(dev, stream, lib().sage_paged_tree, (
+        batch._ref, n, parents.data_ptr(), window or 0, tree._ref, None if positions is None else positions.data_ptr(),
+        status.data_ptr())), "sage_paged_tree")
+    return tree
+
+
+def sage_paged_attn_tree(q: torch.Tensor, cache: PagedKV, batch: PagedBatch, tree: PagedTree,
+                         sm_scale: Optional[float] = None, window: Optional[int] = None,
+                         out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                         ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of the batch's new tokens q [N, Hq, D], trees of drafted tokens, over the cache: the cached tokens before
+    them (with a window, the last `window` before the token's own place) and the new tokens that the tree's mask shows.
+    Otherwise as sage_paged_attn."""
+    if tree.n_tokens != q.shape[0] or tree.device != cache.device:
+        raise ValueError("tree must have q's rows, on the cache's device")
+    if window and tree.depth is None:
+        raise ValueError("a window needs the tree's depth")
+    sm_scale = 1.0 / math.sqrt(cache.head_dim) if sm_scale is None else sm_scale
+    return _paged_attn_call(q, cache, batch, (tree._ref, sm_scale, window or 0), out, lse, ws, stream,
+                            "sage_paged_attn_tree")

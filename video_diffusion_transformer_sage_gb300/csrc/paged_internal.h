@@ -11,7 +11,7 @@
 namespace sage {
 
 enum PagedWhere : int32_t { kWherePage = 16, kWhereLength = 17, kWhereRopeRow = 18, kWherePagedFull = 19,
-                            kWherePagedEmpty = 20, kWherePagedMma = 21 };
+                            kWherePagedEmpty = 20, kWherePagedMma = 21, kWhereParent = 22 };
 
 // The batch as the kernels take it.
 struct PagedBatchDev {
@@ -62,11 +62,32 @@ struct PagedAttnArgs {
   int32_t* counters;           // [2 kPagedMaxCtas + 2], zero between calls
   float2* part_ml;             // [slots][rows]: running maximum (log2 units) and sum
   float* part_o;               // [slots][rows][D]
+  // A tree's mask (sage_paged_tree_mask); unused by the plain kernels.
+  const uint32_t* mask;
+  int64_t mask_stride;
+  int mask_words;
+  const int32_t* depth;
 };
 
 // paged_few.cu: up to 32 query rows (tokens x query heads of one K/V head) per tile.
 cudaError_t launch_paged_few(const PagedAttnArgs& a, const sage_paged_kv& c, int d, cudaStream_t s);
 // paged_chunk.cu: 256 query rows per unit.
 cudaError_t launch_paged_chunk(const PagedAttnArgs& a, const sage_paged_kv& c, int d, cudaStream_t s);
+// The same where the new tokens are trees (paged_few_tree.cu, paged_chunk_tree.cu).
+cudaError_t launch_paged_few_tree(const PagedAttnArgs& a, const sage_paged_kv& c, int d, cudaStream_t s);
+cudaError_t launch_paged_chunk_tree(const PagedAttnArgs& a, const sage_paged_kv& c, int d, cudaStream_t s);
+
+struct PagedTreeArgs {
+  PagedBatchDev b;
+  const int32_t* parents;
+  int window;
+  uint32_t* mask;
+  int64_t mask_stride;
+  int mask_words;
+  int32_t *depth, *positions;
+  int32_t* status;
+};
+// paged_tree.cu
+cudaError_t launch_paged_tree(const PagedTreeArgs& a, cudaStream_t s);
 
 }  // namespace sage
