@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(_HERE, "_build", "libsage_gb300.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "sage.h")
 PAGED_HEADER = os.path.join(os.path.dirname(_HERE), "include", "sage_paged.h")
 TREE_HEADER = os.path.join(os.path.dirname(_HERE), "include", "sage_paged_tree.h")
+POOL_HEADER = os.path.join(os.path.dirname(_HERE), "include", "sage_paged_pool.h")
 PAGED_WS_HEADER = 4096   # SAGE_PAGED_WS_HEADER: the bytes of a paged workspace that start as zeros
 
 STATUS = {0: "SAGE_OK", 1: "SAGE_ERR_INVALID_ARG", 2: "SAGE_ERR_ALIGNMENT", 3: "SAGE_ERR_UNSUPPORTED",
@@ -70,8 +71,14 @@ class SagePagedTreeMaskC(ctypes.Structure):
                 ("depth", ctypes.c_void_p)]
 
 
+class SagePagedPoolC(ctypes.Structure):
+    _fields_ = [("refs", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("n_rows", ctypes.c_int64), ("max_pages", ctypes.c_int64), ("table_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int64)]
+
+
 def header_functions(header: str = HEADER) -> list:
-    """Names of the functions a header (include/sage.h, PAGED_HEADER, TREE_HEADER) declares."""
+    """Names of the functions a header (include/sage.h, PAGED_HEADER, TREE_HEADER, POOL_HEADER) declares."""
     text = open(header).read()
     return sorted(set(re.findall(r"^\s*(?:const\s+)?[a-z_0-9]+\**\s+\**(sage_[a-z_0-9]+)\s*\(", text, re.M)))
 
@@ -86,7 +93,7 @@ def lib():
         VP = ctypes.POINTER(SageView)
         QP = ctypes.POINTER(SageQuantizedC)
         KP, BP = ctypes.POINTER(SagePagedKVC), ctypes.POINTER(SagePagedBatchC)
-        TP = ctypes.POINTER(SagePagedTreeMaskC)
+        TP, OP = ctypes.POINTER(SagePagedTreeMaskC), ctypes.POINTER(SagePagedPoolC)
         sig = {
             "sage_status_string": ([ctypes.c_int], ctypes.c_char_p),
             "sage_quant_scratch_bytes": ([I, I, I], S),
@@ -112,6 +119,12 @@ def lib():
             "sage_paged_workspace_bytes": ([I], S),
             "sage_paged_attn": ([VP, KP, BP, F, I, I, P, I, I, P, P, S, P], ctypes.c_int),
             "sage_paged_tree": ([BP, I, P, I, TP, P, P, P], ctypes.c_int),
+            "sage_paged_pool_workspace_bytes": ([I, I], S),
+            "sage_paged_release": ([OP, P, P, P, P], ctypes.c_int),
+            "sage_paged_reserve": ([OP, P, P, P, P, S, P], ctypes.c_int),
+            "sage_paged_fork": ([OP, P, P, P, I, P, P, P, P, P, S, P], ctypes.c_int),
+            "sage_paged_copy": ([KP, P, P, P, I, P, P], ctypes.c_int),
+            "sage_paged_compact": ([KP, BP, P, P, I, I, P, P, S, P], ctypes.c_int),
             "sage_paged_attn_tree": ([VP, KP, BP, TP, F, I, P, I, I, P, P, S, P], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
@@ -394,7 +407,36 @@ def _capture_apart():
         driver.cuThreadExchangeStreamCaptureMode(ctypes.byref(mode))
 
 
-class PagedKV:
+class _StatusOwner:
+    """Holds a status block (and scratch behind it), made when first needed; it may be used on any stream."""
+
+    def _own_status(self, device, nbytes: int) -> None:
+        self.device, self._status_bytes, self._status, self._status_streams = device, nbytes, None, set()
+
+    @property
+    def status(self) -> torch.Tensor:
+        if self._status is None:
+            # Zeroed before this returns, on a stream of its own: no call on whatever stream comes before that, and inside
+            # a graph capture the zeroing is no part of the graph, whose replays would erase records.
+            side = torch.cuda.Stream(self.device)
+            with _capture_apart():
+                with torch.cuda.stream(side):
+                    status = torch.zeros(self._status_bytes, dtype=torch.uint8, device=self.device)
+                side.synchronize()
+            self._status = status
+        return self._status
+
+    def _status_on(self, stream) -> torch.Tensor:
+        """The block for a call on `stream`, whose kernels may outlive its owner."""
+        status = self.status
+        raw = torch._C._cuda_getCurrentRawStream(self.device.index) if stream is None else _stream(stream)
+        if raw not in self._status_streams:
+            self._status_streams.add(raw)
+            status.record_stream(torch.cuda.ExternalStream(raw, device=self.device))
+        return status
+
+
+class PagedKV(_StatusOwner):
     """A paged K/V cache over the caller's page tensors [n_pages, page_size, n_heads, head_dim] (any page,
     slot and head strides, unit channel stride): bf16, or torch.float8_e4m3fn with fp32 scales
     k_scale and v_scale [n_heads].  `status` is the block that sage_paged_append records bad indices in
@@ -419,33 +461,11 @@ class PagedKV:
                 raise ValueError(f"expected contiguous fp32 scales of shape ({h},) on the pages' device")
         self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
         self.n_pages, self.page_size, self.n_heads, self.head_dim = n, ps, h, d
-        self.device, self._status, self._status_streams = k_pages.device, None, set()
+        self._own_status(k_pages.device, int(lib().sage_status_block_bytes()))
         self._c = SagePagedKVC(k_pages.data_ptr(), v_pages.data_ptr(), n, ps, h, d, *k_pages.stride()[:3],
                                *v_pages.stride()[:3], 1 if e4m3 else 0, k_scale.data_ptr() if e4m3 else None,
                                v_scale.data_ptr() if e4m3 else None)
         self._ref = ctypes.byref(self._c)
-
-    @property
-    def status(self) -> torch.Tensor:
-        if self._status is None:
-            # Zeroed before this returns, on a stream of its own: no call on whatever stream comes before that, and inside
-            # a graph capture the zeroing is no part of the graph, whose replays would erase records.
-            side = torch.cuda.Stream(self.device)
-            with _capture_apart():
-                with torch.cuda.stream(side):
-                    status = status_block(self.device)
-                side.synchronize()
-            self._status = status
-        return self._status
-
-    def _status_on(self, stream) -> torch.Tensor:
-        """The block for a call on `stream`, whose kernels may outlive the cache."""
-        status = self.status
-        raw = torch._C._cuda_getCurrentRawStream(self.device.index) if stream is None else _stream(stream)
-        if raw not in self._status_streams:
-            self._status_streams.add(raw)
-            status.record_stream(torch.cuda.ExternalStream(raw, device=self.device))
-        return status
 
 
 class PagedBatch:
@@ -663,3 +683,115 @@ def sage_paged_attn_tree(q: torch.Tensor, cache: PagedKV, batch: PagedBatch, tre
     sm_scale = 1.0 / math.sqrt(cache.head_dim) if sm_scale is None else sm_scale
     return _paged_attn_call(q, cache, batch, (tree._ref, sm_scale, window or 0), out, lse, ws, stream,
                             "sage_paged_attn_tree")
+
+
+# ------------------------------------------------------------------- the cache's pages (include/sage_paged_pool.h)
+class PagedPool(_StatusOwner):
+    """The pages of a cache and who holds them: int32 CUDA tensors refs [n_pages] (entries of page tables that hold the
+    page; 0: free) and page_table [n_rows, max_pages] (-1: no page), whose rows a PagedBatch may use.  `status` is the block
+    that the accounting calls record bad indices in, with their scratch behind it."""
+
+    def __init__(self, refs: torch.Tensor, page_table: torch.Tensor, page_size: int):
+        if refs.dim() != 1 or page_table.dim() != 2 or 0 in page_table.shape:
+            raise ValueError("expected refs [n_pages] and page_table [n_rows, max_pages]")
+        for t in (refs, page_table):
+            if t.dtype != torch.int32 or not t.is_cuda or t.device != refs.device:
+                raise ValueError("expected int32 CUDA tensors on one device")
+        if not refs.is_contiguous() or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            raise ValueError("refs must be contiguous, page_table's rows too")
+        self.refs, self.page_table, self.page_size = refs, page_table, page_size
+        self.n_rows, self.n_pages = page_table.shape[0], refs.numel()
+        self._own_status(refs.device, max(256, int(lib().sage_paged_pool_workspace_bytes(self.n_rows, self.n_pages))))
+        self._c = SagePagedPoolC(refs.data_ptr(), self.n_pages, page_table.data_ptr(), self.n_rows, page_table.shape[1],
+                                 page_table.stride(0), page_size)
+        self._ref = ctypes.byref(self._c)
+
+
+def _int_list(t: Optional[torch.Tensor], n: Optional[int], device, what: str):
+    if t is None:
+        return None
+    if t.dtype is not _I32 or t.dim() != 1 or (n is not None and t.shape[0] != n) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous int32 tensor [{'n' if n is None else n}] on the same device")
+    return t.data_ptr()
+
+
+def sage_paged_release(pool: PagedPool, hi: torch.Tensor, lo: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gives back the pages of each row whose positions all lie outside [lo, hi) (int32 [n_rows]; lo None: 0)."""
+    dev, n = pool.device, pool.n_rows
+    lo_at, hi_at = _int_list(lo, n, dev, "lo"), _int_list(hi, n, dev, "hi")
+    status = pool._status_on(stream)
+    _check(_paged_call(dev, stream, lib().sage_paged_release, (pool._ref, lo_at, hi_at, status.data_ptr())),
+           "sage_paged_release")
+
+
+def sage_paged_reserve(pool: PagedPool, hi: torch.Tensor, lo: Optional[torch.Tensor] = None,
+                       ok: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gives each row a page for every entry without one among those of its positions [lo, hi) (int32 [n_rows]; lo None:
+    0).  Returns ok, int32 [n_rows]: 1 where the row has all of them, 0 where the free pages did not last."""
+    dev, n = pool.device, pool.n_rows
+    lo_at, hi_at = _int_list(lo, n, dev, "lo"), _int_list(hi, n, dev, "hi")
+    if ok is None:
+        with _made_on(stream, dev):
+            ok = torch.empty(n, dtype=torch.int32, device=dev)
+    ok_at, ws = _int_list(ok, n, dev, "ok"), pool._status_on(stream)
+    _check(_paged_call(dev, stream, lib().sage_paged_reserve, (pool._ref, lo_at, hi_at, ok_at, ws.data_ptr(), ws.nbytes)),
+           "sage_paged_reserve")
+    return ok
+
+
+def sage_paged_fork(pool: PagedPool, src_rows: torch.Tensor, dst_rows: torch.Tensor, n_tokens: torch.Tensor,
+                    out: Optional[torch.Tensor] = None, stream=None):
+    """Row dst_rows[k], which holds no page, begins like row src_rows[k], n_tokens[k] positions long (int32 [n_forks] each):
+    full pages are shared, a page begun gets a free one of the child's own.  Returns (copy_src, copy_dst, copy_tokens,
+    ok), int32 [n_forks] each (rows of `out`, int32 [4, n_forks], made here when None): what sage_paged_copy has to copy
+    in each layer's cache, and 1 where the child was made."""
+    dev = pool.device
+    src, dst = _int_list(src_rows, None, dev, "src_rows"), _int_list(dst_rows, src_rows.shape[0], dev, "dst_rows")
+    n, tokens = src_rows.shape[0], _int_list(n_tokens, src_rows.shape[0], dev, "n_tokens")
+    if out is None:
+        with _made_on(stream, dev):
+            out = torch.empty((4, n), dtype=torch.int32, device=dev)
+    elif out.dtype is not _I32 or tuple(out.shape) != (4, n) or not out.is_contiguous() or out.device != dev:
+        raise ValueError(f"out: expected a contiguous int32 tensor [4, {n}] on the pool's device")
+    ws, at = pool._status_on(stream), out.data_ptr()
+    _check(_paged_call(dev, stream, lib().sage_paged_fork, (
+        pool._ref, src, dst, tokens, n, at, at + 4 * n, at + 8 * n, at + 12 * n, ws.data_ptr(), ws.nbytes)),
+        "sage_paged_fork")
+    return tuple(out.unbind(0))
+
+
+def sage_paged_copy(cache: PagedKV, src: torch.Tensor, dst: torch.Tensor, n_tokens: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """K and V of the first n_tokens[i] slots (None: all) of page src[i] to page dst[i], int32 [n] each; an entry with a
+    -1 is left out.  No page may be the target of two copies, or target and source."""
+    dev = cache.device
+    s = _int_list(src, None, dev, "src")
+    n = src.shape[0]
+    d, t = _int_list(dst, n, dev, "dst"), _int_list(n_tokens, n, dev, "n_tokens")
+    if status is None:
+        status = cache._status_on(stream)
+    elif status.device != dev or status.nbytes < 256:
+        raise ValueError("status: expected a zeroed block of 256 bytes on the cache's device")
+    _check(_paged_call(dev, stream, lib().sage_paged_copy, (cache._ref, s, d, t, n, status.data_ptr())), "sage_paged_copy")
+
+
+def sage_paged_compact(cache: PagedKV, batch: PagedBatch, first: torch.Tensor, keep: torch.Tensor, n_keep: torch.Tensor,
+                       ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """K and V of position keep[b, i] of sequence b to position first[b] + i, for i < n_keep[b], in place: int32 first
+    and n_keep [n_seqs], keep [n_seqs, max_keep], positions not before their new ones and below kv_len.  ws: a
+    paged_workspace, or its first SAGE_PAGED_WS_HEADER bytes as zeros (made here when None)."""
+    dev, n = cache.device, batch.n_seqs
+    if batch.device != dev:
+        raise ValueError("the batch lies on another device than the cache")
+    if keep.dim() != 2 or keep.shape[0] != n or keep.dtype is not _I32 or keep.device != dev \
+            or (keep.shape[1] > 1 and keep.stride(1) != 1):
+        raise ValueError(f"keep: expected an int32 tensor [{n}, max_keep] with contiguous rows on the cache's device")
+    f, k = _int_list(first, n, dev, "first"), _int_list(n_keep, n, dev, "n_keep")
+    if ws is None:
+        with _made_on(stream, dev):
+            ws = torch.zeros(PAGED_WS_HEADER, dtype=torch.uint8, device=dev)
+    elif ws.device != dev:
+        raise ValueError("ws lies on another device than the cache")
+    _check(_paged_call(dev, stream, lib().sage_paged_compact, (
+        cache._ref, batch._ref, f, keep.data_ptr(), keep.shape[1], keep.stride(0), k, ws.data_ptr(), ws.nbytes)),
+        "sage_paged_compact")

@@ -17,7 +17,7 @@ LIB = os.path.join(BUILD, "libsage_gb300.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["sage_api.cu", "quant.cu", "attn_fwd.cu", "attn_dense.cu", "noalloc.cu", "qk_transform.cu", "mma_rate.cu",
            "paged_api.cu", "paged_append.cu", "paged_few.cu", "paged_chunk.cu", "paged_tree.cu", "paged_few_tree.cu",
-           "paged_chunk_tree.cu"]
+           "paged_chunk_tree.cu", "paged_pool.cu", "paged_move.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr"]

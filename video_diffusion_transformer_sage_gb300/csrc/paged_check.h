@@ -82,7 +82,7 @@ inline PagedBatchDev batch_dev(const sage_paged_batch* b, const sage_paged_kv* c
 // Workspace: status block | counters | (maximum, sum) of each partial row | partial O.
 constexpr size_t kCountersOff = kPagedStatusBytes;
 constexpr size_t kMlOff = SAGE_PAGED_WS_HEADER;
-static_assert(kCountersOff + sizeof(int32_t) * (2 * kPagedMaxCtas + 2) <= kMlOff, "counters exceed the workspace header");
+static_assert(kCountersOff + sizeof(int32_t) * kPagedCounters <= kMlOff, "counters exceed the workspace header");
 constexpr size_t kSlots = kPagedSlots;
 constexpr size_t kPartOff = kMlOff + kSlots * kPagedChunkRows * sizeof(float2);
 

@@ -11,7 +11,8 @@
 namespace sage {
 
 enum PagedWhere : int32_t { kWherePage = 16, kWhereLength = 17, kWhereRopeRow = 18, kWherePagedFull = 19,
-                            kWherePagedEmpty = 20, kWherePagedMma = 21, kWhereParent = 22 };
+                            kWherePagedEmpty = 20, kWherePagedMma = 21, kWhereParent = 22,
+                            kWhereKept = 23, kWhereCount = 24, kWhereRow = 25, kWherePagedMove = 26 };
 
 // The batch as the kernels take it.
 struct PagedBatchDev {
@@ -44,6 +45,11 @@ struct PagedAppendArgs {
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, int d, bool e4m3, cudaStream_t s);
 
+// The counters of a workspace's header, zero between calls: those of the attention's joins and draws, then those of
+// sage_paged_compact (the next item, the CTAs that are done, the items read).
+constexpr int kPagedMoveCounters = 2 * kPagedMaxCtas + 2, kPagedMoveRing = 312;
+constexpr int kPagedCounters = kPagedMoveCounters + 2 + kPagedMoveRing;
+
 // The rows of one partial result.
 constexpr int kPagedChunkRows = 256;
 
@@ -59,7 +65,7 @@ struct PagedAttnArgs {
   int64_t ost, osh;
   float* lse;
   int32_t* status;
-  int32_t* counters;           // [2 kPagedMaxCtas + 2], zero between calls
+  int32_t* counters;           // [kPagedCounters], zero between calls
   float2* part_ml;             // [slots][rows]: running maximum (log2 units) and sum
   float* part_o;               // [slots][rows][D]
   // A tree's mask (sage_paged_tree_mask); unused by the plain kernels.
