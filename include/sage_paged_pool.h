@@ -14,7 +14,7 @@
  * before anything is launched.  What lies in device memory is checked by the kernels: an index that is out of range is never
  * followed, the rest goes on, and the status block records SAGE_ERR_INVALID_ARG with `where` = 16 (page), 17 (length), 23 (kept
  * position), 24 (a page given back that nobody holds) or 25 (row of the page table); an expired wait has where = 26.
- * Everything is read on the device, so a captured graph may be replayed after the numbers changed.  All results are
+ * Everything is read on the device, so a captured graph may be replayed after the numbers changed.  Results are
  * determined by the inputs, whatever runs when.
  */
 #ifndef SAGE_GB300_PAGED_POOL_H
@@ -89,15 +89,17 @@ sage_status sage_paged_copy(const sage_paged_kv* cache, const int32_t* src, cons
  * first[b] + i, for each i < n_keep[b], as if all were read before any is written.  The positions before first[b] stay; those
  * from first[b] + n_keep[b] on hold what is left (the caller sets kv_len, and may release their pages).
  *   first    device int32 [n_seqs].
- *   keep     device int32, n_keep[b] positions of sequence b, each from its new place on (keep[i] >= first + i) and
- *            below kv_len: ascending lists are, and a position may come twice.  One that is not is recorded (23) and its
- *            token not moved.  max_keep: the most a row may have; larger n_keep are cut (17), keep_stride >= max_keep.
+ *   keep     device int32, n_keep[b] positions of sequence b, ascending, each from its new place on (keep[i] >= first + i)
+ *            and below kv_len.  One that is not, or not above the one before it, is recorded (23) and its token not moved;
+ *            what the new places of a list hold that does not ascend is not determined.  max_keep: the most a row may have;
+ *            larger n_keep are cut (17), keep_stride >= max_keep.
  *   n_keep   device int32 [n_seqs].
  * Of the batch, kv_len (the tokens before the call) and page_table are read.  A token whose page, old or new, is out of range
  * is not moved (16).  Pages that are written belong to one sequence (a shared page would change for all).
  *   ws       256-byte aligned, >= SAGE_PAGED_WS_HEADER bytes, zeroed once: a workspace of sage_paged_attn, or its header
  *            alone.  Calls that may overlap on the GPU need workspaces of their own.
- * One launch. */
+ * One launch.  Lists longer than an item of 64 KB (256 tokens, or as many as one head's rows allow) are worked through in
+ * pieces of 48 KB; more than 2^25 of them are refused (SAGE_ERR_UNSUPPORTED). */
 sage_status sage_paged_compact(const sage_paged_kv* cache, const sage_paged_batch* batch, const int32_t* first,
                                const int32_t* keep, int64_t max_keep, int64_t keep_stride, const int32_t* n_keep, void* ws,
                                size_t ws_bytes, void* stream);

@@ -298,7 +298,7 @@ SHAPES = [
 
 @pytest.mark.parametrize("fmt,layout", LAYOUTS)
 @pytest.mark.parametrize("kv_lens,most,page,hkv,d", SHAPES, ids=lambda x: str(x)[:16])
-@pytest.mark.parametrize("kind", ["ascending", "any", "near"])
+@pytest.mark.parametrize("kind", ["ascending", "runs", "near"])
 def test_compact(fmt, layout, kv_lens, most, page, hkv, d, kind):
     r = random.Random(most + d)
     table, n_pages = _table(r, kv_lens, page)
@@ -311,11 +311,14 @@ def test_compact(fmt, layout, kv_lens, most, page, hkv, d, kind):
             keep.append([x for x in range(f, n) if x not in gone])
         elif kind == "ascending":
             keep.append(sorted(r.sample(range(f, n), r.randint(0, min(most, n - f)))))
-        else:                   # in any order, some twice
+        else:                   # runs of tokens: frames
             ks = []
-            for i in range(r.randint(0, min(most, n - f))):
-                ks.append(r.randint(f + i, n - 1))
-            keep.append(ks)
+            while len(ks) < most:
+                at = (ks[-1] if ks else f) + r.choice([1, 1, 1, 17, n // 9 + 1])
+                ks += range(at, min(at + r.randint(1, 2 * page), n))
+                if at >= n:
+                    break
+            keep.append(ks[:most])
     want = _moved(kv, table, page, first, keep)
     ws = sage.paged_workspace(d)
     _compact(cache, table, kv_lens, first, keep, ws=ws)
@@ -344,12 +347,13 @@ def test_compact_numbers_out_of_range():
     page, n = 8, 30
     table = [[4, 1, 3, 0]]
     for keep, first, where in (([3, 4], [5], 23), ([9, 30], [2], 23), ([9, -1], [2], 23), ([9, 2 ** 31 - 1], [2], 23),
-                               ([5, 7], [-1], 23), ([6, 28], [0], 16), ([25, 26], [6], 16)):
+                               ([5, 7], [-1], 23), ([9, 9, 12], [2], 23), ([9, 7, 12], [2], 23), ([6, 28], [0], 16), ([25, 26], [6], 16)):
         cache, kv = _cache(5, page, 2, 64, "bf16", "nhd")
         t = [list(table[0])]
         if where == 16:
             t[0][3] = 5 if keep[0] == 6 else -1
         good = [(k, first[0] + i) for i, k in enumerate(keep) if first[0] + i >= 0 and first[0] + i <= k < n
+                and (i == 0 or k > keep[i - 1])
                 and 0 <= t[0][k // page] < 5]
         want = [x.clone() for x in kv]
         for w, x in zip(want, kv):

@@ -122,34 +122,44 @@ def test_binding_refuses_before_any_call():
         sage.PagedPool(z(4), z(2, 0), 16)
 
 
-@pytest.mark.parametrize("ctas", [1, 2, 3, 7])
-def test_the_order_of_a_long_list_ends_and_overwrites_nothing(ctas):
-    """sage_paged_compact's items, drawn, read and written by CTAs in any interleaving: with a ring of `ctas` numbers no
-    item waits for ever, and none is written before all earlier ones are read."""
+@pytest.mark.parametrize("ctas,places,slots,buffers", [(1, 8, 8, 4), (3, 24, 8, 4), (7, 56, 8, 4), (4, 4, 8, 4), (5, 7, 3, 1)])
+def test_the_order_of_long_lists_ends_and_overwrites_nothing(ctas, places, slots, buffers):
+    """sage_paged_compact's items, drawn, read, announced and written by CTAs in any interleaving: no item waits for ever (also
+    with fewer places in the ring than items in work), and none is written before the items that it names have been read."""
     import random
-    for seed in range(40):
+    for seed in range(25):
         r = random.Random(seed)
-        items, ring, state, drawn, read, written = r.randint(1, 60), [0] * ctas, [None] * ctas, 0, set(), []
-        idle = 0
-        while len(written) < items:
-            c = r.randrange(ctas)
+        units, runs = r.randint(1, 4), r.randint(1, 30)
+        items = units * runs
+        needs = [[i - d * units for d in range(1, r.randint(0, i // units) + 1)] for i in range(items)]
+        ring = [0] * places
+        turns = [[] for _ in range(ctas)]              # each CTA's items in the order drawn
+        reads, writes, announced = [0] * ctas, [0] * ctas, [set() for _ in range(ctas)]
+        drawn, was_read, was_written, idle = 0, set(), set(), 0
+        while len(was_written) < items:
             idle += 1
-            assert idle < 20000, "stuck"
-            if state[c] is None:
-                if drawn < items:
-                    state[c] = ("drawn", drawn)
-                    drawn += 1
-            elif state[c][0] == "drawn":
-                item = state[c][1]
-                read.add(item)
-                assert ring[item % ctas] <= item
-                ring[item % ctas] = item + 1
-                state[c] = ("read", item)
-            else:
-                item = state[c][1]
-                back = range(1, min(ctas - 1, item) + 1)
-                if all(ring[(item - b) % ctas] >= item - b + 1 for b in back):
-                    assert read >= set(range(item))
-                    written.append(item)
-                    state[c] = None
+            assert idle < 5000, "stuck"
+            c, what = r.randrange(ctas), r.randrange(4)
+            mine = turns[c]
+            if what == 0 and drawn < items and len(mine) - writes[c] < slots:
+                mine.append(drawn)
+                drawn += 1
+            elif what == 1 and reads[c] < len(mine) and reads[c] - writes[c] < buffers:
+                was_read.add(mine[reads[c]])
+                reads[c] += 1
+            elif what == 2:                            # any buffer that has been read, not in order
+                open_ = [k for k in range(writes[c], reads[c]) if k not in announced[c]]
+                if open_:
+                    k = r.choice(open_)
+                    if ring[mine[k] % places] >= mine[k] // places:
+                        assert ring[mine[k] % places] == mine[k] // places
+                        ring[mine[k] % places] += 1
+                        announced[c].add(k)
+                        idle = 0
+            elif what == 3 and writes[c] in announced[c]:
+                item = mine[writes[c]]
+                if all(ring[n % places] >= n // places + 1 for n in needs[item]):
+                    assert was_read >= set(needs[item])
+                    was_written.add(item)
+                    writes[c] += 1
                     idle = 0

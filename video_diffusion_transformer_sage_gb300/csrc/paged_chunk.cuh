@@ -54,7 +54,7 @@ constexpr uint64_t kChunkWaitNs = 2000000000ull;
 constexpr int kItemWaits = 64;   // such waits for all of an item's key tiles
 constexpr float kRise = 8.0f;   // log2 of how far a maximum may fall behind before O is rescaled
 
-template <int D, bool kE4M3>
+template <int D, bool kE4M3, bool kTree>
 struct ChunkCfg {
   static constexpr int kThreads = kE4M3 ? 512 : 384;
   static constexpr int kPanels = D / 64;
@@ -62,13 +62,22 @@ struct ChunkCfg {
   static constexpr int kQTileBytes = kBM * D * 2;
   static constexpr int kTileBytes = kBN * D * 2;              // a K or V tile in 16 bits
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = D == 128 ? 2 : 4;
+  // A tree has few rows for the keys that it sees, so the loads have to be far ahead: K and V apart, each in a ring of
+  // its own, and with E4M3 rings of staging tiles in place of widened ones.  (One row tile at D = 64 with the shared ring
+  // of four: 97 us for 12032 keys of 152 heads in bf16, 112 in E4M3, of which 73 and 87 remain when K and V come from L2: a
+  // load's latency in every step.)
+  static constexpr int kKStages = !kTree ? (D == 128 ? 2 : 4) : kE4M3 ? (D == 128 ? 1 : 2) : (D == 128 ? 2 : 5);
+  static constexpr int kVStages = !kTree ? (D == 128 ? 2 : 4) : kE4M3 ? (D == 128 ? 2 : 3) : (D == 128 ? 2 : 5);
+  static constexpr int kRawStages = kTree && kE4M3 ? (D == 128 ? 2 : 5) : 1;
+  static constexpr int kBits = 8;                             // key tiles whose loaded boxes are remembered
   // K and V of a tile have barriers of their own where the ring is short (D = 128): a K stage is free again once
   // Q K^T has read it, a softmax before P V is done with V (chunk_frames 2358 -> 2236 us).  The four stages at
-  // D = 64 hide the loads anyway, and there the extra waits of the issuing warp cost 3 %.
-  static constexpr bool kSplitKV = D == 128;
+  // D = 64 hide the loads of prompts anyway, and there the extra waits of the issuing warp cost 3 %.
+  static constexpr bool kSplitKV = kTree || D == 128;
+  static constexpr int kKStep = kTree ? kTileBytes : kStageBytes, kVStep = kKStep;   // from stage to stage
+  static constexpr int kVBase = kTree ? kKStages * kTileBytes : kTileBytes;          // from the first K tile to the first V tile
   static constexpr int kRawTile = kBN * D;                    // a tile of codes
-  static constexpr int kRawBytes = kE4M3 ? 2 * kRawTile : 0;
+  static constexpr int kRawBytes = kE4M3 ? 2 * kRawTile * kRawStages : 0;
   // Tensor memory columns: S_t at 128 t, O_t at 256 + D t; P_t over S_t, or at 384 + 64 t (D = 64).
   static constexpr int kColO0 = 256;
   static constexpr bool kSepP = D == 64;
@@ -80,19 +89,19 @@ struct ChunkCfg {
   // is no room for both, and they leave through the slot's Q tile first.
   static constexpr bool kEarlyQ = !(kE4M3 && D == 128);
   static constexpr int kKvOff = 2 * kQTileBytes;
-  static constexpr int kRawOff = kKvOff + kStages * kStageBytes;
+  static constexpr int kRawOff = kKvOff + (kKStages + kVStages) * kTileBytes;
   static constexpr int kOutOff = kRawOff + kRawBytes;
   static constexpr int kExpOff = kOutOff + (kEarlyQ ? 2 * 16384 : 0);   // biased exponent of each Q row (E4M3)
   static constexpr int kBarOff = kExpOff + (kE4M3 ? 256 : 0);
-  // q_full[2], k_full[S], v_full[S], k_empty[S], v_empty[S], s_full[2], p_full[2], pv_done[2], s_free[2], o_free[2],
-  // ml_full, ml_empty, mma_final, raw_full[2] (K, V), raw_empty[2], unit_full[2], unit_empty[2], draw
-  static constexpr int kNumBars = 4 * kStages + 24;
+  // q_full[2], k_full[K stages], v_full[V stages], k_empty, v_empty likewise, s_full[2], p_full[2], pv_done[2], s_free[2], o_free[2],
+  // ml_full, ml_empty, mma_final, raw_full[2][R] (K, V), raw_empty[2][R], unit_full[2], unit_empty[2], draw
+  static constexpr int kNumBars = 2 * (kKStages + kVStages) + 20 + 4 * kRawStages;
   static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;
   // Registers a thread: launched at 168 (384 threads) or 128 (512).
   static constexpr int kRegsRoles = 72, kRegsSoftmax = kE4M3 ? 184 : 216, kRegsWiden = 72;
   static_assert(128 * kRegsRoles + 256 * kRegsSoftmax + (kE4M3 ? 128 * kRegsWiden : 0) <= (kE4M3 ? 512 * 128 : 384 * 168),
                 "register split exceeds launch");
-  static_assert(kSmem <= 232448 - 1408, "shared memory");
+  static_assert(kSmem <= 232448 - 1376, "shared memory");   // (ChunkShared and alignment)
 };
 
 struct ChunkParams {
@@ -261,17 +270,17 @@ __device__ __forceinline__ void warp_tc_commit(uint64_t* bar) {
       : "memory");
 }
 
-template <int D, bool kE4M3>
+template <int D, bool kE4M3, bool kTree>
 __device__ __forceinline__ void issue_qk(uint32_t s_tmem, uint32_t ql, uint32_t kl) {
   constexpr uint32_t idesc = idesc_f32acc(kBM, kBN) | (kE4M3 ? 0u : kIdescBf16);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
-    const uint32_t off = ((kk >> 2) * ChunkCfg<D, kE4M3>::kPanelBytes + (kk & 3) * 32) >> 4;
+    const uint32_t off = ((kk >> 2) * ChunkCfg<D, kE4M3, kTree>::kPanelBytes + (kk & 3) * 32) >> 4;
     warp_mma_f16_ss(s_tmem, sdesc_of_lo(ql + off), sdesc_of_lo(kl + off), idesc, kk > 0 ? 1u : 0u);
   }
 }
 // P: 16 keys in 8 tensor-memory columns; V: 16 keys are 2048 bytes.
-template <int D, bool kE4M3>
+template <int D, bool kE4M3, bool kTree>
 __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint32_t vl, bool first) {
   constexpr uint32_t idesc = idesc_f32acc(kBM, D) | kIdescBmn | (kE4M3 ? 0u : kIdescBf16);
 #pragma unroll
@@ -308,10 +317,10 @@ __device__ __forceinline__ uint32_t key_mask(int w, int lo, int hi, uint32_t bit
 // masked where `masked`, its maximum taken; P = 2^(S c - m) is written in 16 bits, l the sum of the unrounded P; O is
 // multiplied by 2^(m_old - m) where the maximum rose by more than kRise.  With separate P columns S is
 // released as soon as it is in registers and P waits for the P.V of the tile before (pv_done).
-template <int D, bool kE4M3, typename Mask>
+template <int D, bool kE4M3, bool kTree, typename Mask>
 __device__ __forceinline__ bool softmax_step(uint32_t tS, uint32_t tO, uint32_t tP, float c, bool masked, Mask&& make_mask,
                                              bool first, float& m, float& l, uint64_t* s_free, uint64_t* pv_done, int j) {
-  constexpr bool kSep = ChunkCfg<D, kE4M3>::kSepP;
+  constexpr bool kSep = ChunkCfg<D, kE4M3, kTree>::kSepP;
   uint32_t sr[128];
   SAGE_TMEM_LD32(tS + 0, (sr + 0));
   SAGE_TMEM_LD32(tS + 32, (sr + 32));
@@ -405,7 +414,7 @@ struct ChunkShared {
   Unit unit[2];                    // the items in work and next
   int skip;
   volatile int abort;
-  uint32_t bits[8], raw_bits[2];   // boxes loaded: of the last key tiles, and of the staging K and V tile
+  uint32_t bits[8], raw_bits[2][5];   // boxes loaded: of the last key tiles, and of the staging K and V tiles
   uint32_t tmem;
   float2 ml[128];                  // slot 1's maxima and sums (units of one row tile)
 };
@@ -416,11 +425,11 @@ struct Slot {   // a row tile's number, as a constant
 };
 
 template <int D, bool kE4M3, bool kTree>
-__global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
+__global__ void __launch_bounds__(ChunkCfg<D, kE4M3, kTree>::kThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        const __grid_constant__ ChunkParams p) {
-  using C = ChunkCfg<D, kE4M3>;
-  constexpr int S = C::kStages;
+  using C = ChunkCfg<D, kE4M3, kTree>;
+  constexpr int KS = C::kKStages, VS = C::kVStages, RS = C::kRawStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ ChunkShared sh;
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -429,10 +438,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
   uint8_t* q_exp = smem + C::kExpOff;
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* k_full = q_full + 2;
-  uint64_t* v_full = k_full + S;
-  uint64_t* k_empty = v_full + S;
-  uint64_t* v_empty = k_empty + S;
-  uint64_t* s_full = v_empty + S;
+  uint64_t* v_full = k_full + KS;
+  uint64_t* k_empty = v_full + VS;
+  uint64_t* v_empty = k_empty + KS;
+  uint64_t* s_full = v_empty + VS;
   uint64_t* p_full = s_full + 2;
   uint64_t* pv_done = p_full + 2;
   uint64_t* s_free = pv_done + 2;
@@ -441,8 +450,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
   uint64_t* ml_empty = ml_full + 1;
   uint64_t* mma_final = ml_empty + 1;
   uint64_t* raw_full = mma_final + 1;
-  uint64_t* raw_empty = raw_full + 2;
-  uint64_t* unit_full = raw_empty + 2;
+  uint64_t* raw_empty = raw_full + 2 * RS;
+  uint64_t* unit_full = raw_empty + 2 * RS;
   uint64_t* unit_empty = unit_full + 2;
   uint64_t* draw = unit_empty + 2;
   const PagedAttnArgs& a = p.a;
@@ -451,8 +460,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
   if (threadIdx.x == 0) {
     sh.skip = *reinterpret_cast<volatile int32_t*>(a.status) == kStatusTimeout;
     sh.abort = 0;
-    for (int i = 0; i < 2 * S; ++i) mbar_init(k_full + i, kE4M3 ? 128 : 1);        // and v_full
-    for (int i = 0; i < 2 * S; ++i) mbar_init(k_empty + i, 1);                     // and v_empty
+    for (int i = 0; i < KS + VS; ++i) mbar_init(k_full + i, !kE4M3 ? 1 : kTree ? 4 : 128);        // and v_full
+    for (int i = 0; i < KS + VS; ++i) mbar_init(k_empty + i, 1);                     // and v_empty
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + i, 128);
       mbar_init(s_full + i, 1);
@@ -460,8 +469,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
       mbar_init(pv_done + i, 1);
       mbar_init(s_free + i, 4);
       mbar_init(o_free + i, 128);
-      mbar_init(raw_full + i, 1);
-      mbar_init(raw_empty + i, 128);
+      for (int k = 0; k < RS; ++k) {
+        mbar_init(raw_full + i * RS + k, 1);
+        mbar_init(raw_empty + i * RS + k, kTree ? 4 : 128);
+      }
       mbar_init(unit_full + i, 1);
       // The loading warps, the issuing warp, the softmax and the widening warps.
       mbar_init(unit_empty + i, (C::kTwoLoaders ? 2 : 1) + 1 + 8 + (kE4M3 ? 4 : 0));
@@ -596,41 +607,46 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
         const int32_t* row = a.b.table + e.b * a.b.table_stride;
         release_unit(k);
         if (ntiles < 0) break;
+        auto entry = [&](int key0) {
+          return lane < boxes && key0 < uhi && key0 + box > ulo ? __ldg(row + (key0 >> a.b.page_shift)) : -1;
+        };
+        int ahead = kTree ? entry(key00) : 0;   // a tree's next tile's entries are on their way while this one waits
         for (int j = 0; j < ntiles && ok; ++j, ++ct) {
           const int key0 = key00 + j * kBN;
           if (warp == 0 && lane == 0 && j == max(0, ntiles - 3)) mbar_arrive(draw);
           const bool need = lane < boxes && key0 < uhi && key0 + box > ulo;
-          int page = -1;
-          if (need) page = __ldg(row + (key0 >> a.b.page_shift));
+          const int page = kTree ? ahead : entry(key0);
+          if (kTree && j + 1 < ntiles) ahead = entry(key0 + kBN);
           const bool good = need && page >= 0 && page < a.b.n_pages;
           if (need && !good) record_bad_index(a.status, kWherePage);
           const uint32_t bits = __ballot_sync(0xffffffffu, good);
           const int slot_in_page = key0 & ((1 << a.b.page_shift) - 1);
-          const uint32_t s = ct % S;
+          const uint32_t rs = ct % RS;
           for (int kv = kv0; kv < kv1; ++kv) {
             const CUtensorMap* map = kv ? &vmap : &kmap;
+            const uint32_t ring = kv ? VS : KS, s = ct % ring;
             const bool own_bar = C::kSplitKV || kv == 0;   // V shares K's barriers otherwise
-            uint64_t* full = kE4M3 ? raw_full + kv : (kv && own_bar ? v_full : k_full) + s;
+            uint64_t* full = kE4M3 ? raw_full + kv * RS + rs : (kv && own_bar ? v_full : k_full) + s;
             if (kE4M3) {
-              if (ct >= 1) ok = wait(raw_empty + kv, (ct - 1) & 1, kWherePagedEmpty);
-            } else if (own_bar && ct >= S) {
-              ok = wait((kv || !C::kSplitKV ? v_empty : k_empty) + s, (ct / S - 1) & 1, kWherePagedEmpty);
+              if (ct >= RS) ok = wait(raw_empty + kv * RS + rs, (ct / RS - 1) & 1, kWherePagedEmpty);
+            } else if (own_bar && ct >= ring) {
+              ok = wait((kv || !C::kSplitKV ? v_empty : k_empty) + s, (ct / ring - 1) & 1, kWherePagedEmpty);
             }
             ok = !__any_sync(0xffffffffu, !ok || sh.abort);
             if (!ok) break;
             if (lane == 0) {
-              if (kE4M3) sh.raw_bits[kv] = bits;
-              else if (kv == 0) sh.bits[ct % (2 * S)] = bits;
+              if (kE4M3) sh.raw_bits[kv][rs] = bits;
+              else if (kv == 0) sh.bits[ct % C::kBits] = bits;
               if (kE4M3 || own_bar)
                 mbar_arrive_expect_tx(full, __popc(bits) * box_bytes * (kE4M3 || C::kSplitKV ? 1u : 2u));
             }
             __syncwarp();
             if (good) {
               if (kE4M3) {
-                tma_load_4d(smem_u32(smem + C::kRawOff) + kv * C::kRawTile + (lane << p.box_shift) * D, map, full, 0, h,
+                tma_load_4d(smem_u32(smem + C::kRawOff) + (rs * 2 + kv) * C::kRawTile + (lane << p.box_shift) * D, map, full, 0, h,
                             slot_in_page, page);
               } else {
-                const uint32_t dst = smem_u32(sKV + s * C::kStageBytes) + kv * C::kTileBytes + (lane << p.box_shift) * 128;
+                const uint32_t dst = smem_u32(sKV) + (kv ? C::kVBase + s * C::kVStep : s * C::kKStep) + (lane << p.box_shift) * 128;
 #pragma unroll
                 for (int pn = 0; pn < C::kPanels; ++pn)
                   tma_load_4d(dst + pn * C::kPanelBytes, map, full, pn * 64, h, slot_in_page, page);
@@ -643,10 +659,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
       if (!ok) {
         // After a timeout: the copies issued have landed before the CTA ends.
         if (kE4M3) {
-          if (issued > 0) mbar_wait(raw_full + kv0, (issued - 1) & 1, kChunkWaitNs);
+          for (uint32_t i = issued > RS ? issued - RS : 0; i < issued; ++i)
+            mbar_wait(raw_full + kv0 * RS + i % RS, (i / RS) & 1, kChunkWaitNs);
         } else {
-          for (uint32_t i = issued > S ? issued - S : 0; i < issued; ++i)
-            mbar_wait((kv0 ? v_full : k_full) + i % S, (i / S) & 1, kChunkWaitNs);
+          const uint32_t ring = kv0 ? VS : KS;
+          for (uint32_t i = issued > ring ? issued - ring : 0; i < issued; ++i)
+            mbar_wait((kv0 ? v_full : k_full) + i % ring, (i / ring) & 1, kChunkWaitNs);
         }
       }
     } else if (warp == 1) {
@@ -654,8 +672,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
       const uint32_t colS = tmem, colO = tmem + C::kColO0, colP = tmem + C::kColP0;
       const uint32_t s_base = __shfl_sync(0xffffffffu, smem_u32(sQ), 0);
       const uint32_t q_lo = sdesc_lo(s_base), k_lo = sdesc_lo(s_base + C::kKvOff),
-                     v_lo = vdesc_lo(s_base + C::kKvOff + C::kTileBytes);
-      constexpr uint32_t kQLo = C::kQTileBytes >> 4, kStageLo = C::kStageBytes >> 4;
+                     v_lo = vdesc_lo(s_base + C::kKvOff + C::kVBase);
+      constexpr uint32_t kQLo = C::kQTileBytes >> 4, kKLo = C::kKStep >> 4, kVLo = C::kVStep >> 4;
       // The ring stage and phase of the next K tile and of the next V tile; per slot the S, P V, units and Q tiles so
       // far.
       int sk = 0, sv = 0;
@@ -664,14 +682,14 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
       auto mwait = [&](uint64_t* x, uint32_t parity) { return warp_wait(x, parity); };
       auto step_k = [&]() {
         if (C::kSplitKV) warp_tc_commit(k_empty + sk);
-        if (++sk == S) {
+        if (++sk == KS) {
           sk = 0;
           phk ^= 1u;
         }
       };
       auto step_v = [&]() {
         warp_tc_commit(v_empty + sv);
-        if (++sv == S) {
+        if (++sv == VS) {
           sv = 0;
           phv ^= 1u;
         }
@@ -687,7 +705,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
       auto qk = [&](auto T, int tile) {
         constexpr int t = decltype(T)::v;
         tc_fence_after();
-        issue_qk<D, kE4M3>(colS + t * kBN, q_lo + tile * kQLo, k_lo + sk * kStageLo);
+        issue_qk<D, kE4M3, kTree>(colS + t * kBN, q_lo + tile * kQLo, k_lo + sk * kKLo);
         warp_tc_commit(s_full + t);
         ++ns[t];
       };
@@ -698,7 +716,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
       auto pv = [&](auto T, bool first) {
         constexpr int t = decltype(T)::v;
         tc_fence_after();
-        issue_pv<D, kE4M3>(colO + t * D, colP + t * C::kStepP, v_lo + sv * kStageLo, first);
+        issue_pv<D, kE4M3, kTree>(colO + t * D, colP + t * C::kStepP, v_lo + sv * kVLo, first);
         warp_tc_commit(pv_done + t);
         ++np[t];
       };
@@ -814,6 +832,76 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
     const int r = threadIdx.x - 384;   // the key of the tile
     const uint32_t raw = smem_u32(smem + C::kRawOff) + r * D;
     const uint32_t rsw = D == 128 ? (r & 7) : ((r >> 1) & 3);
+    auto read_raw = [&](uint32_t at, uint4 v[D / 16]) {
+#pragma unroll
+      for (int ch = 0; ch < D / 16; ++ch)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v[ch].x), "=r"(v[ch].y), "=r"(v[ch].z), "=r"(v[ch].w)
+                     : "r"(at + ((ch ^ rsw) << 4)));
+    };
+    auto write_wide = [&](uint8_t* tile, const uint4 v[D / 16], bool live) {
+#pragma unroll
+      for (int ch = 0; ch < D / 16; ++ch) {
+        const uint32_t w[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
+        uint32_t f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f[2 * i]) : "h"(static_cast<uint16_t>(live ? w[i] : 0u)));
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f[2 * i + 1]) : "h"(static_cast<uint16_t>(live ? w[i] >> 16 : 0u)));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int c8 = ch * 2 + i;   // 8-channel chunk of the 16-bit row
+          *reinterpret_cast<uint4*>(tile + (c8 >> 3) * C::kPanelBytes + r * 128 + (((c8 & 7) ^ (r & 7)) << 4)) =
+              make_uint4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        }
+      }
+    };
+    // Tile ct of a tree: K and V read together where there are registers for both, one arrival per warp.
+    auto widen_ahead = [&](uint32_t ct, uint32_t rs, int key, int ulo, int uhi, bool some) {
+      constexpr bool kBoth = D == 64;
+      const uint32_t sk = ct % KS, sv = ct % VS, phase = (ct / RS) & 1, at = raw + rs * 2 * C::kRawTile;
+      uint4 v[kBoth ? 2 : 1][D / 16];
+      bool ok = warp_wait(raw_full + rs, phase);
+      read_raw(at, v[0]);
+      if (kBoth) {
+        ok = ok && warp_wait(raw_full + RS + rs, phase);
+        read_raw(at + C::kRawTile, v[kBoth]);
+      }
+      const uint32_t bits = sh.raw_bits[0][rs];
+      const bool live = ((bits >> (r >> p.box_shift)) & 1u) && key >= ulo && key < uhi && some;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(raw_empty + rs);
+        if (kBoth) mbar_arrive(raw_empty + RS + rs);
+      }
+      if (ok && ct >= KS) ok = warp_wait(k_empty + sk, (ct / KS - 1) & 1);
+      if (!ok || __any_sync(0xffffffffu, sh.abort)) {
+        if (!ok) give_up(a.status, kWherePagedFull, &sh.abort);
+        return false;
+      }
+      if (r == 0) sh.bits[ct % C::kBits] = bits;
+      write_wide(sKV + sk * C::kKStep, v[0], live);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(k_full + sk);
+      if (!kBoth) {
+        ok = warp_wait(raw_full + RS + rs, phase);
+        read_raw(at + C::kRawTile, v[0]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(raw_empty + RS + rs);
+      }
+      if (ok && ct >= VS) ok = warp_wait(v_empty + sv, (ct / VS - 1) & 1);
+      if (!ok) {
+        give_up(a.status, kWherePagedFull, &sh.abort);
+        return false;
+      }
+      write_wide(sKV + C::kVBase + sv * C::kVStep, v[kBoth], live);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v_full + sv);
+      return true;
+    };
     uint32_t ct = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -825,19 +913,25 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
       release_unit(k);
       if (ntiles < 0) break;
       for (int j = 0; j < ntiles && ok; ++j, ++ct) {
-        const uint32_t s = ct % S;
+        const uint32_t rs = ct % RS;
         // A tree's new tokens: those that some row of the unit sees.
         const bool some = !kTree || tree_key_seen(a, start, tok0, tok1, key_r - lane + j * kBN, prefix);
-        uint8_t* tile = sKV + s * C::kStageBytes;
+        if (kTree) {
+          ok = widen_ahead(ct, rs, key_r + j * kBN, ulo, uhi, some);
+          if (!ok) break;
+          continue;
+        }
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          if (ct >= S && (C::kSplitKV || kv == 0))
-            ok = warp_wait((kv || !C::kSplitKV ? v_empty : k_empty) + s, (ct / S - 1) & 1);
-          ok = ok && warp_wait(raw_full + kv, ct & 1);
+          const uint32_t ring = kv ? VS : KS, s = ct % ring;
+          uint8_t* tile = sKV + (kv ? C::kVBase + s * C::kVStep : s * C::kKStep);
+          if (ct >= ring && (C::kSplitKV || kv == 0))
+            ok = warp_wait((kv || !C::kSplitKV ? v_empty : k_empty) + s, (ct / ring - 1) & 1);
+          ok = ok && warp_wait(raw_full + kv * RS + rs, (ct / RS) & 1);
           if (!ok) give_up(a.status, kWherePagedFull, &sh.abort);
           ok = !__any_sync(0xffffffffu, !ok || sh.abort);
           if (!ok) break;
-          const uint32_t bits = sh.raw_bits[kv];
+          const uint32_t bits = sh.raw_bits[kv][rs];
           const int key = key_r + j * kBN;
           // Keys that no row sees count as zeros, whatever their slots hold.
           const bool live = ((bits >> (r >> p.box_shift)) & 1u) && key >= ulo && key < uhi && some;
@@ -846,9 +940,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
           for (int ch = 0; ch < D / 16; ++ch)
             asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                          : "=r"(v[ch].x), "=r"(v[ch].y), "=r"(v[ch].z), "=r"(v[ch].w)
-                         : "r"(raw + kv * C::kRawTile + ((ch ^ rsw) << 4)));
-          mbar_arrive(raw_empty + kv);
-          if (r == 0 && kv == 0) sh.bits[ct % (2 * S)] = bits;
+                         : "r"(raw + (rs * 2 + kv) * C::kRawTile + ((ch ^ rsw) << 4)));
+          mbar_arrive(raw_empty + kv * RS + rs);
+          if (r == 0 && kv == 0) sh.bits[ct % C::kBits] = bits;
 #pragma unroll
           for (int ch = 0; ch < D / 16; ++ch) {
             const uint32_t w[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
@@ -861,7 +955,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int c8 = ch * 2 + i;   // 8-channel chunk of the 16-bit row
-              *reinterpret_cast<uint4*>(tile + kv * C::kTileBytes + (c8 >> 3) * C::kPanelBytes + r * 128 +
+              *reinterpret_cast<uint4*>(tile + (c8 >> 3) * C::kPanelBytes + r * 128 +
                                         (((c8 & 7) ^ (r & 7)) << 4)) =
                   make_uint4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
             }
@@ -947,6 +1041,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
       const bool one = u.rows <= 128;
       bool ok = true;
       const int ntiles = u.nt, first = one ? 0 : t * 128;   // the slot's first row
+      const bool dead = first + wq * 32 >= u.rows;          // the warp has no row of the unit
       const int steps = one ? (ntiles + 1 - t) / 2 : ntiles;
       int klo, khi;   // this row's visible keys
       const int tok = (u.row0 + min(first + r, u.rows - 1)) / p.group, prefix = u.len - u.n_new;
@@ -974,18 +1069,28 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3>::kThreads, 1)
         ok = wait(s_full + t, (mine + i) & 1, kWherePagedMma);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t bits = sh.bits[(ct + j) % (2 * S)];
+        const uint32_t bits = sh.bits[(ct + j) % C::kBits];
         const bool masked = kb < alo || kb + kBN > ahi || bits != all_boxes;
-        ok = softmax_step<D, kE4M3>(tS, tO, tP, c, masked, [&](uint32_t mask[4]) {
+        if (kTree && dead && (!masked || kE4M3)) {
+          // None of the warp's rows exists: whatever stands in their P stays in their O.  (With P columns of its own S comes
+          // a tile ahead: the last tile's P has to be through before this one's is announced.)
+          if (C::kSepP) {
+            if (lane == 0) mbar_arrive(s_free + t);
+            if (i > 0 && !(ok = wait(pv_done + t, (mine + i - 1) & 1, kWherePagedMma))) break;
+          }
+          mbar_arrive(p_full + t);
+          continue;
+        }
+        ok = softmax_step<D, kE4M3, kTree>(tS, tO, tP, c, masked, [&](uint32_t mask[4]) {
           if (!kE4M3) {
             // Keys that no row of the unit sees may hold anything: their V counts as 0.
-            const uint32_t s = (ct + j) % S;
+            const uint32_t s = (ct + j) % VS;
             const int key = kb + r;
             const bool some = !kTree || tree_key_seen(a, u.start, u.row0 / p.group, (u.row0 + u.rows - 1) / p.group,
                                                       key - lane, prefix);
-            if (C::kSplitKV) wait(v_full + s, ((ct + j) / S) & 1, kWherePagedFull);
+            if (C::kSplitKV) wait(v_full + s, ((ct + j) / VS) & 1, kWherePagedFull);
             if (!(((bits >> (r >> p.box_shift)) & 1u) && key >= u.ulo && key < u.uhi && some)) {
-              uint8_t* v = sKV + s * C::kStageBytes + C::kTileBytes + r * 128;
+              uint8_t* v = sKV + C::kVBase + s * C::kVStep + r * 128;
 #pragma unroll
               for (int x = 0; x < 8 * C::kPanels; ++x)
                 *reinterpret_cast<uint4*>(v + (x >> 3) * C::kPanelBytes + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -1201,7 +1306,7 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
 
 template <int D, bool kE4M3, bool kTree>
 cudaError_t launch_t(const PagedAttnArgs& a, const sage_paged_kv& kv, cudaStream_t s) {
-  using C = ChunkCfg<D, kE4M3>;
+  using C = ChunkCfg<D, kE4M3, kTree>;
   ChunkParams p;
   p.a = a;
   if (!kE4M3) p.a.v_scale = nullptr;

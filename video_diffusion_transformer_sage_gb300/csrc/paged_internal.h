@@ -45,10 +45,10 @@ struct PagedAppendArgs {
 };
 cudaError_t launch_paged_append(const PagedAppendArgs& a, int d, bool e4m3, cudaStream_t s);
 
-// The counters of a workspace's header, zero between calls: those of the attention's joins and draws, then those of
-// sage_paged_compact (the next item, the CTAs that are done, the items read).
-constexpr int kPagedMoveCounters = 2 * kPagedMaxCtas + 2, kPagedMoveRing = 312;
-constexpr int kPagedCounters = kPagedMoveCounters + 2 + kPagedMoveRing;
+// The counters of a workspace's header are zero between calls, whichever call it is: the attention's joins and draws use them,
+// and sage_paged_compact (the next item, the CTAs that are done, the items read: places of 16 bits).
+constexpr int kPagedMoveRing = 1880;
+constexpr int kPagedCounters = 2 * kPagedMaxCtas + 2 > 2 + kPagedMoveRing / 2 ? 2 * kPagedMaxCtas + 2 : 2 + kPagedMoveRing / 2;
 
 // The rows of one partial result.
 constexpr int kPagedChunkRows = 256;

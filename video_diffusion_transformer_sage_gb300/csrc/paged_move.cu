@@ -8,14 +8,23 @@
 //
 // Compact moves every token to an earlier place of its own sequence, so a place may be written only when the tokens before
 // it in the list, which may stand there, have been read.  A token's own place lies before all that later tokens are read
-// from (keep[i] >= first + i), so that is all.  An item is a run of tokens of one sequence, of K or V, and some of the heads, up
-// to 64 KB, held in shared memory between reading and writing:
-//   lists that fit one item     a CTA for each item, nothing to wait for;
-//   longer ones                 CTAs draw items in the order of a list's tokens; an item is written when all items drawn
-//                               before it have been read.  Reading waits for nothing, so every wait ends.  While an item is
-//                               not read, every later one is held by a CTA of its own, which waits for it: with G CTAs
-//                               only the G - 1 items before an item can be outstanding, and a ring of G numbers, the last
-//                               item read in each place, tells which are.
+// from (keep[i] >= first + i), so that is all.  An item is a run of tokens of one sequence, of K or V, and some of the heads,
+// held in shared memory between reading and writing:
+//   lists that fit one item (64 KB)   a CTA for each item, nothing to wait for;
+//   longer ones                       one CTA per SM with eight items in work, four of them with 48 KB of shared memory, each step
+//                                     of an item by warps of their own: drawn (in the order of the lists' tokens), its
+//                                     places found, its rows read, announced, and written after a look at whether
+//                                     the items that read from its new places have done so.  In an ascending list these are
+//                                     as many entries as the item has tokens, found by search; most often they were
+//                                     read long ago.  Rows go by bulk copies where a token's heads lie together, by 16 bytes a
+//                                     thread where they do not (a bulk copy takes ~20 ns whatever its size).
+// Which items have been read stands in a ring of 8 numbers per CTA: in place `item mod its length` the round of the last item read,
+// each put there after the one a round before it.  Items ascend within a CTA, reading waits for nothing but that and a buffer, and
+// the lowest item not yet read finds its place ready: so every wait ends.
+// The long kernel's steps on compact_frames (24192 tokens of 56 heads, 1.39 GB; floor 196 us): an item read, waited for and written
+// in turn, two CTAs per SM 554 us; reading and writing by warps of their own 420-520, 200 of it waiting for all items drawn
+// before; the search and bulk copies 337; eight items found ahead, the lists side by side, no fences, a place in the ring for every
+// item in work 220 (6.3 TB/s; 207 without looking at the ring).  Rows of 256 bytes, by 16 bytes a thread: 353 for as much.
 #include <algorithm>
 
 #include "paged_batch.cuh"
@@ -28,9 +37,11 @@ namespace {
 constexpr int kMoveThreads = 256;
 constexpr int kCopyPer = 8;                                    // 16-byte pieces of a thread
 constexpr int kCopyPieces = kMoveThreads * kCopyPer;           // 32 KB
-constexpr int kItemPieces = 4096;                              // 64 KB
+constexpr int kItemPieces = 4096, kLongPieces = 3072;          // of an item: 64 KB, of a long list 48 KB
+constexpr int kLongItems = 8, kLongBuffers = 4;                // in work in a CTA
+constexpr int kMovePlaces = 8;                                 // of the ring, for each CTA: no item waits for one that is not drawn
+static_assert(kMovePlaces >= kLongItems, "items wait for their places");
 constexpr int kItemTokens = 256;                               // at most, of an item
-constexpr int kMoveCtasPerSm = 2;
 constexpr uint64_t kMoveWaitNs = 2000000000ull;
 
 struct PageSide {   // K or V: bytes
@@ -99,9 +110,9 @@ struct CompactArgs {
   int row_shift, heads;
   int slab, slabs;             // heads of an item, items side by side
   int tokens, runs;            // tokens of an item, items of a list of max_keep
-  uint32_t items;              // n_seqs * 2 * slabs * runs
+  uint32_t units, items;       // n_seqs * 2 * slabs; times runs
   int32_t* status;
-  int32_t* counters;           // next item, CTAs done, ring [kPagedMoveRing]: 1 + the last item read in each place
+  int32_t* counters;           // next item, CTAs done, ring of 16-bit numbers: 1 + the round last read in each place
 };
 
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
@@ -115,52 +126,60 @@ __device__ __forceinline__ uint4 load_shared16(uint32_t a) {
 
 struct MoveShared {
   int64_t from[kItemTokens], to[kItemTokens];   // bytes from the pages' beginning; from < 0: not moved
-  uint32_t item;
-  int go;
 };
-
-// Reads an item's tokens; what write() needs of it.
+// An item: what it takes to read and to write it.
 struct Item {
   uint32_t pieces, per;   // 16-byte pieces, and those of a token
   const PageSide* side;
   int64_t head0;          // bytes to its first head
+  int b, i0, count;       // sequence, first token of its list, tokens
 };
-__device__ __forceinline__ Item read_item(const CompactArgs& a, uint32_t item, MoveShared& sh, uint32_t smem) {
-  const uint32_t unit = item / a.runs, run = item - unit * a.runs, half = unit / a.slabs;
-  const int slab = unit - half * a.slabs, b = half >> 1;
+__device__ __forceinline__ Item find_item(const CompactArgs& a, uint32_t item) {
+  // The lists side by side, so that an item's predecessors were drawn long before it.
+  const uint32_t run = item / a.units, unit = item - run * a.units, half = unit / a.slabs;
+  const int slab = unit - half * a.slabs;
   Item it;
+  it.b = half >> 1;
   it.side = &a.side[half & 1];
   it.head0 = static_cast<int64_t>(slab) * a.slab * it.side->head;
   it.per = static_cast<uint32_t>(min(a.slab, a.heads - slab * a.slab)) << a.row_shift;
-  const int n_all = __ldg(a.n_keep + b), n = min(max(n_all, 0), a.max_keep);
-  const int i0 = run * a.tokens, count = min(a.tokens, n - i0);
-  const bool first = slab == 0 && !(half & 1) && threadIdx.x == 0;
-  if (first && run == 0 && n_all != n) record_bad_index(a.status, kWhereLength);
-  it.pieces = count > 0 ? count * it.per : 0;
-  __syncthreads();   // the last item's places are no longer needed
-  if (static_cast<int>(threadIdx.x) < count) {
-    const int i = i0 + threadIdx.x;
-    const int64_t old = __ldg(a.keep + b * a.keep_stride + i), now = static_cast<int64_t>(__ldg(a.first + b)) + i;
+  it.i0 = run * a.tokens;
+  it.count = max(0, min(a.tokens, min(max(__ldg(a.n_keep + it.b), 0), a.max_keep) - it.i0));
+  it.pieces = it.count * it.per;
+  return it;
+}
+// Where its tokens lie and go to, by `n` threads.
+__device__ __forceinline__ void find_places(const CompactArgs& a, const Item& it, MoveShared& sh, int me, int n) {
+  const bool first_head = it.head0 == 0 && it.side == &a.side[0];   // one item of each run records what is wrong
+  if (me == 0 && first_head && it.i0 == 0) {
+    const int k = __ldg(a.n_keep + it.b);
+    if (k < 0 || k > a.max_keep) record_bad_index(a.status, kWhereLength);
+  }
+  for (int t = me; t < it.count; t += n) {
+    const int i = it.i0 + t;
+    const int64_t old = __ldg(a.keep + it.b * a.keep_stride + i), now = static_cast<int64_t>(__ldg(a.first + it.b)) + i;
     int64_t from = -1, to = -1;
-    const int where_slab = slab == 0 && !(half & 1);
-    if (now < 0 || old < now || old >= min(__ldg(a.b.kv_len + b), a.b.cap)) {
-      if (where_slab) record_bad_index(a.status, kWhereKept);
+    const int64_t last = i > 0 ? __ldg(a.keep + it.b * a.keep_stride + i - 1) : -1;
+    if (now < 0 || old < now || old <= last || old >= min(__ldg(a.b.kv_len + it.b), a.b.cap)) {
+      if (first_head) record_bad_index(a.status, kWhereKept);
     } else if (old != now) {
-      const int32_t* row = a.b.table + b * a.b.table_stride;
+      const int32_t* row = a.b.table + it.b * a.b.table_stride;
       const int p0 = __ldg(row + (old >> a.b.page_shift)), p1 = __ldg(row + (now >> a.b.page_shift));
       if (p0 < 0 || p0 >= a.b.n_pages || p1 < 0 || p1 >= a.b.n_pages) {
-        if (where_slab) record_bad_index(a.status, kWherePage);
+        if (first_head) record_bad_index(a.status, kWherePage);
       } else {
         const int mask = (1 << a.b.page_shift) - 1;
         from = p0 * it.side->page + (old & mask) * it.side->token + it.head0;
         to = p1 * it.side->page + (now & mask) * it.side->token + it.head0;
       }
     }
-    sh.from[threadIdx.x] = from;
-    sh.to[threadIdx.x] = to;
+    sh.from[t] = from;
+    sh.to[t] = to;
   }
-  __syncthreads();
-  for (uint32_t p = threadIdx.x; p < it.pieces; p += kMoveThreads) {
+}
+// Reads its tokens into shared memory by `n` threads; the calling thread's copies have landed when it returns.
+__device__ __forceinline__ void read_item(const CompactArgs& a, const Item& it, const MoveShared& sh, uint32_t smem, int me, int n) {
+  for (uint32_t p = me; p < it.pieces; p += n) {
     const uint32_t tok = p / it.per, in = p - tok * it.per;
     const int64_t from = sh.from[tok];
     if (from >= 0)
@@ -168,11 +187,10 @@ __device__ __forceinline__ Item read_item(const CompactArgs& a, uint32_t item, M
                                       ((in & ((1u << a.row_shift) - 1u)) << 4));
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  return it;
 }
-// Each thread writes the pieces that it has read.
-__device__ __forceinline__ void write_item(const CompactArgs& a, const Item& it, const MoveShared& sh, uint32_t smem) {
-  for (uint32_t p = threadIdx.x; p < it.pieces; p += kMoveThreads) {
+__device__ __forceinline__ void write_item(const CompactArgs& a, const Item& it, const MoveShared& sh, uint32_t smem, int me,
+                                           int n) {
+  for (uint32_t p = me; p < it.pieces; p += n) {
     const uint32_t tok = p / it.per, in = p - tok * it.per;
     if (sh.from[tok] < 0) continue;
     const uint4 v = load_shared16(smem + p * 16);
@@ -180,56 +198,251 @@ __device__ __forceinline__ void write_item(const CompactArgs& a, const Item& it,
                               ((in & ((1u << a.row_shift) - 1u)) << 4)) = v;
   }
 }
+__device__ __forceinline__ bool timed_out(const int32_t* status) {
+  return *reinterpret_cast<const volatile int32_t*>(status) == kStatusTimeout;
+}
 
 __global__ void __launch_bounds__(kMoveThreads) paged_compact_kernel(const __grid_constant__ CompactArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ MoveShared sh;
-  const uint32_t smem = smem_u32(smem_raw);
-  if (threadIdx.x == 0) sh.go = *reinterpret_cast<volatile int32_t*>(a.status) != kStatusTimeout;
+  if (__syncthreads_or(threadIdx.x == 0 && timed_out(a.status))) return;   // no work until the status has been read
+  const Item it = find_item(a, blockIdx.x);
+  find_places(a, it, sh, threadIdx.x, kMoveThreads);
   __syncthreads();
-  if (!sh.go) return;   // an earlier wait ran out: no work until the status has been read
-  if (a.runs == 1) {
-    // The list is one item: it has been read whole before any of it is written.
-    const Item it = read_item(a, blockIdx.x, sh, smem);
-    __syncthreads();
-    write_item(a, it, sh, smem);
-    return;
+  read_item(a, it, sh, smem_u32(smem_raw), threadIdx.x, kMoveThreads);
+  __syncthreads();   // the whole list has been read
+  write_item(a, it, sh, smem_u32(smem_raw), threadIdx.x, kMoveThreads);
+}
+
+// Warp 0 draws, 1-4 find, 5-8 announce and look at the ring (a buffer each: both are chains of waits for L2); then those that
+// read and those that write: one warp each for bulk copies, eight each (reading in two groups of four, items in turn) without.
+constexpr int kFinders = 4;
+static_assert(kLongBuffers == kFinders, "an end for each warp that finds, and for each buffer");
+template <bool kBulk>
+struct LongCfg {
+  static constexpr int kReaders = kBulk ? 32 : 128, kReadGroups = kBulk ? 1 : 2, kWriters = kBulk ? 32 : 256;
+  static constexpr int kReader0 = (1 + kFinders + kLongBuffers) * 32, kWriter0 = kReader0 + kReaders * kReadGroups;
+  static constexpr int kThreads = kWriter0 + kWriters;
+};
+template <int kThreads>
+__device__ __forceinline__ void role_sync(int barrier) {
+  if (kThreads == 32) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(barrier), "n"(kThreads) : "memory");
+}
+
+// What the steps of an item need of it.
+struct LongItem {
+  uint32_t item;
+  uint32_t moved;       // tokens that move
+  uint32_t near, far;   // items `near` .. `far` before this one read from its new places (far 0: none)
+  Item it;
+};
+
+// The first entry of b's list, among the n before entry i0, that is not below `place` (n: none), by a warp.  The list ascends.
+__device__ __forceinline__ int first_not_below(const CompactArgs& a, int b, int n, int64_t place) {
+  const int lane = threadIdx.x & 31;
+  const int32_t* keep = a.keep + b * a.keep_stride;
+  int lo = 0;
+  while (n > 0) {
+    const int step = (n + 31) / 32, at = lo + min((lane + 1) * step, n) - 1;   // the last entry of each part
+    const uint32_t below = __ballot_sync(0xffffffffu, __ldg(keep + at) < place);
+    const int parts = __popc(below);   // parts that lie below as a whole
+    const int skip = min(parts * step, n);
+    lo += skip;
+    n = step == 1 || skip == n ? 0 : min(step, n - skip) - 1;   // (a part's last entry is known)
+    if (step == 1) break;
   }
-  int32_t *next = a.counters, *ring = next + 2;
-  const uint32_t ctas = gridDim.x;   // at most kPagedMoveRing
-  while (true) {
-    __syncthreads();
-    if (threadIdx.x == 0) sh.item = static_cast<uint32_t>(atomicAdd(next, 1));
-    __syncthreads();
-    const uint32_t item = sh.item;
-    if (item >= a.items) break;
-    const Item it = read_item(a, item, sh, smem);
-    __syncthreads();   // every thread's copies have landed
-    if (threadIdx.x == 0) {
-      __threadfence();
-      *reinterpret_cast<volatile int32_t*>(ring + item % ctas) = static_cast<int32_t>(item + 1);
+  return lo;
+}
+
+template <bool kBulk>
+__global__ void __launch_bounds__(LongCfg<kBulk>::kThreads, 1) paged_compact_long_kernel(const __grid_constant__ CompactArgs a) {
+  using C = LongCfg<kBulk>;
+  constexpr uint32_t M = kLongItems, B = kLongBuffers;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ MoveShared sh[M];
+  __shared__ LongItem li[M];   // item a.items: no more
+  __shared__ uint64_t drawn[M], found[M], done[M], full[B], go[B], empty[B];
+  __shared__ volatile int s_abort;
+  __shared__ int s_last;
+  int32_t* next = a.counters;
+  volatile uint16_t* ring = reinterpret_cast<uint16_t*>(next + 2);
+  const uint32_t places = kMovePlaces * gridDim.x;   // at most kPagedMoveRing
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    s_abort = timed_out(a.status);
+    for (uint32_t i = 0; i < M; ++i) {
+      mbar_init(drawn + i, 1);
+      mbar_init(found + i, 1);
+      mbar_init(done + i, 1);
     }
-    // Each thread looks after the items `back` before this one (those that have nothing to write wait too: see above).
-    bool ok = true;
-    for (uint32_t back = threadIdx.x + 1; back < ctas && back <= item; back += kMoveThreads) {
-      const volatile int32_t* at = ring + (item - back) % ctas;
+    for (uint32_t i = 0; i < B; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(go + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (s_abort) return;   // an earlier wait ran out: no work until the status has been read
+  // After a wait that ran out nothing more is drawn or written, but the turns still go round.
+  auto fail = [&] {
+    if (lane == 0) {
+      record_timeout(a.status, kWherePagedMove);
+      s_abort = 1;
+    }
+    __syncwarp();
+  };
+  auto wait = [&](uint64_t* bar, uint32_t k, uint32_t n) {   // by a whole warp: turn k of n barriers
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar + k % n, (k / n) & 1, 4 * kMoveWaitNs));
+    if (!ok) fail();
+    return ok;
+  };
+  auto pass = [&](uint64_t* bar, uint32_t k, uint32_t n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar + k % n);
+  };
+  // Turn k's item, or a.items.
+  auto item_of = [&](bool ok, uint32_t k) { return ok ? li[k % M].item : a.items; };
+  if (warp == 0) {
+    for (uint32_t k = 0, ends = 0; ends < kFinders; ++k) {   // an end for each warp that finds
+      const bool ok = k < M || wait(done, k - M, M);
+      uint32_t item = a.items;
+      if (lane == 0 && ok && !s_abort && ends == 0) item = min(static_cast<uint32_t>(atomicAdd(next, 1)), a.items);
+      item = __shfl_sync(0xffffffffu, item, 0);
+      if (lane == 0) li[k % M].item = item;
+      pass(drawn, k, M);
+      ends += item >= a.items;
+    }
+  } else if (warp <= kFinders) {
+    for (uint32_t k = warp - 1;; k += kFinders) {
+      const bool ok = wait(drawn, k, M);
+      const uint32_t item = item_of(ok, k);
+      if (item < a.items) {
+        const Item it = find_item(a, item);
+        MoveShared& m = sh[k % M];
+        find_places(a, it, m, lane, 32);
+        __syncwarp();
+        uint32_t moved = 0;
+        for (int t = lane; t < it.count; t += 32) moved += m.from[t] >= 0;
+        moved = __reduce_add_sync(0xffffffffu, moved);
+        // The entries before this item that stand in its new places: as many as it has tokens, at most.
+        const int from = it.count > 0 && it.i0 > 0
+                             ? first_not_below(a, it.b, it.i0, static_cast<int64_t>(__ldg(a.first + it.b)) + it.i0)
+                             : it.i0;
+        const int end = min(it.i0, from + it.count);
+        if (lane == 0) {
+          LongItem& l = li[k % M];
+          l.it = it;
+          l.moved = moved;
+          l.far = from < end ? it.i0 / a.tokens - from / a.tokens : 0;
+          l.near = from < end ? it.i0 / a.tokens - (end - 1) / a.tokens : 0;
+        }
+      }
+      pass(found, k, M);
+      if (item >= a.items) break;
+    }
+  } else if (warp <= kFinders + static_cast<int>(B)) {
+    // ------------------------------------------------------------ announce, and look at the ring
+    // No fences: an item's rows have arrived in shared memory before its number is stored, and a write that is issued after the
+    // number was seen cannot change what was read.  (With fences 45 us more of compact_frames.)
+    for (uint32_t k = warp - kFinders - 1;; k += B) {
+      const bool ok = wait(found, k, M);
+      const uint32_t item = item_of(ok, k), round = item / places, far = li[k % M].far, near = li[k % M].near;
+      volatile uint16_t* at = ring + item % places;
       const uint64_t t0 = global_timer_ns();
-      while (ok && static_cast<uint32_t>(*at) < item - back + 1) ok = global_timer_ns() - t0 < kMoveWaitNs;
+      auto late = [&] {
+        __nanosleep(40);
+        if (__any_sync(0xffffffffu, global_timer_ns() - t0 > kMoveWaitNs)) fail();
+      };
+      // Whether the items that have to be read before this one is written are.
+      auto clear = [&] {
+        bool all = true;
+        for (uint32_t d = near + lane; d <= far; d += 32) {
+          const uint32_t other = item - d * a.units;
+          all &= ring[other % places] >= other / places + 1;
+        }
+        return __all_sync(0xffffffffu, all);
+      };
+      bool all = true;
+      if (item < a.items) {
+        while (!s_abort && *at < round) late();   // the item a round before
+        __syncwarp();
+        all = far == 0 || clear();
+      }
+      if (wait(full, k, B) && item < a.items) {
+        if (lane == 0) *at = static_cast<uint16_t>(round + 1);
+        while (!all && !s_abort) {
+          all = clear();
+          if (!all) late();
+        }
+      }
+      pass(go, k, B);
+      if (item >= a.items) break;
     }
-    if (!ok) record_timeout(a.status, kWherePagedMove);
-    __threadfence();
-    if (!__syncthreads_and(ok)) return;
-    write_item(a, it, sh, smem);
+  } else if (static_cast<int>(threadIdx.x) < C::kWriter0) {
+    // ------------------------------------------------------------ read
+    const int group = (threadIdx.x - C::kReader0) / C::kReaders, me = threadIdx.x - C::kReader0 - group * C::kReaders;
+    for (uint32_t k = group, ends = 0; ends < B / C::kReadGroups; k += C::kReadGroups) {   // an end for each buffer
+      const uint32_t buf = k % B;
+      bool ok = wait(found, k, M);
+      ok = (k < B || wait(empty, k - B, B)) && ok;
+      const uint32_t item = item_of(ok, k), moved = item < a.items ? li[k % M].moved : 0;
+      if (kBulk) {
+        const Item it = li[k % M].it;
+        if (me == 0) {
+          if (moved > 0) mbar_arrive_expect_tx(full + buf, moved * it.per * 16);
+          else mbar_arrive(full + buf);
+        }
+        __syncwarp();
+        if (moved > 0)
+          for (int t = me; t < it.count; t += 32)
+            if (sh[k % M].from[t] >= 0)
+              bulk_load(smem_raw + buf * kLongPieces * 16 + t * it.per * 16, it.side->pages + sh[k % M].from[t], it.per * 16, full + buf);
+      } else {
+        if (moved > 0) read_item(a, li[k % M].it, sh[k % M], smem_u32(smem_raw) + buf * kLongPieces * 16, me, C::kReaders);
+        role_sync<C::kReaders>(1 + group);   // every thread's copies have landed
+        if (me == 0) mbar_arrive(full + buf);
+      }
+      ends += item >= a.items;
+    }
+  } else {
+    // ------------------------------------------------------------ write
+    const int me = threadIdx.x - C::kWriter0;
+    for (uint32_t k = 0;; ++k) {
+      const uint32_t buf = k % B;
+      const bool ok = wait(go, k, B);
+      const uint32_t item = item_of(ok, k);
+      if (item < a.items && li[k % M].moved > 0 && !s_abort) {
+        const Item it = li[k % M].it;
+        if (kBulk) {
+          for (int t = me; t < it.count; t += 32)
+            if (sh[k % M].from[t] >= 0)
+              bulk_store(it.side->pages + sh[k % M].to[t], smem_raw + buf * kLongPieces * 16 + t * it.per * 16, it.per * 16);
+          bulk_commit();
+          bulk_wait_read<0>();
+        } else {
+          write_item(a, it, sh[k % M], smem_u32(smem_raw) + buf * kLongPieces * 16, me, C::kWriters);
+        }
+      }
+      role_sync<C::kWriters>(3);
+      if (me == 0) {
+        mbar_arrive(empty + buf);
+        mbar_arrive(done + k % M);
+      }
+      if (item >= a.items) break;
+    }
+    if (kBulk) bulk_wait_all();
   }
   // The last CTA to draw no more leaves the counters at zero for the next call.
-  __shared__ int s_last;
+  __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    s_last = atomicAdd(next + 1, 1) == static_cast<int>(ctas) - 1;
+    s_last = atomicAdd(next + 1, 1) == static_cast<int>(gridDim.x) - 1;
   }
   __syncthreads();
-  if (s_last)
-    for (uint32_t w = threadIdx.x; w < ctas + 2; w += kMoveThreads) a.counters[w] = 0;
+  if (s_last && !s_abort)
+    for (uint32_t w = threadIdx.x; w < 2 + (places + 1) / 2; w += C::kThreads) a.counters[w] = 0;
 }
 
 void page_sides(const sage_paged_kv* c, PageSide side[2]) {
@@ -308,28 +521,36 @@ sage_status sage_paged_compact(const sage_paged_kv* cache, const sage_paged_batc
   a.row_shift = pieces_shift(cache);
   a.heads = static_cast<int>(cache->n_heads);
   a.status = static_cast<int32_t*>(ws);
-  a.counters = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kCountersOff) + kPagedMoveCounters;
+  a.counters = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kCountersOff);
   // As many heads to an item as leave room for the whole list, where one head does; else rows of about 4 KB.
   const int64_t row = int64_t(1) << a.row_shift;
-  int64_t slab = std::min<int64_t>(a.heads, kItemPieces / row / max_keep);
+  int64_t slab = std::min<int64_t>(a.heads, kItemPieces / row / max_keep), pieces = kItemPieces;
   const bool whole = max_keep <= kItemTokens && slab >= 1;
-  if (!whole) slab = std::min<int64_t>(a.heads, 256 / row);
+  if (!whole) {
+    slab = std::min<int64_t>(a.heads, 256 / row);
+    pieces = kLongPieces;
+  }
   a.slabs = static_cast<int>((a.heads + slab - 1) / slab);
   a.slab = static_cast<int>(slab);
-  a.tokens = static_cast<int>(std::min<int64_t>({kItemTokens, kItemPieces / (slab * row), max_keep}));
+  a.tokens = static_cast<int>(std::min<int64_t>({kItemTokens, pieces / (slab * row), max_keep}));
   a.runs = static_cast<int>((max_keep + a.tokens - 1) / a.tokens);
   const int64_t items = batch->n_seqs * 2 * a.slabs * a.runs;
-  if (items >= int64_t(1) << 31) return SAGE_ERR_UNSUPPORTED;
+  if (items > (whole ? INT32_MAX : int64_t(1) << 25)) return SAGE_ERR_UNSUPPORTED;   // (rounds of the ring in 16 bits)
+  a.units = static_cast<uint32_t>(items / a.runs);
   a.items = static_cast<uint32_t>(items);
-  const int smem = static_cast<int>(a.tokens * slab * row * 16);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(paged_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kItemPieces * 16);
+  // Bulk copies where a token's rows of K and of V lie together.
+  const bool bulk = slab == 1 || (a.side[0].head == row * 16 && a.side[1].head == row * 16);
+  auto* kernel = whole ? paged_compact_kernel : bulk ? paged_compact_long_kernel<true> : paged_compact_long_kernel<false>;
+  const int most = whole ? kItemPieces * 16 : kLongBuffers * kLongPieces * 16;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return cuda_status(e);
-  const int64_t most = std::min<int64_t>(sms * kMoveCtasPerSm, kPagedMoveRing);
-  const unsigned grid = static_cast<unsigned>(a.runs == 1 ? items : std::min(items, most));
-  paged_compact_kernel<<<grid, kMoveThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
+  const int64_t ctas = whole ? items : std::min<int64_t>({items, sms, kPagedMoveRing / kMovePlaces});
+  const int threads = whole ? kMoveThreads : bulk ? LongCfg<true>::kThreads : LongCfg<false>::kThreads;
+  const int smem = whole ? static_cast<int>(a.tokens * slab * row * 16) : most;
+  kernel<<<static_cast<unsigned>(ctas), threads, smem, static_cast<cudaStream_t>(stream)>>>(a);
   return cuda_status(cudaGetLastError());
 }
 
