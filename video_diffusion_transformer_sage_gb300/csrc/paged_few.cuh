@@ -1029,9 +1029,14 @@ cudaError_t launch_t(const PagedAttnArgs& a, const sage_paged_kv& kv, cudaStream
 template <int D, bool kE4M3, bool kTree>
 cudaError_t launch_rows(const PagedAttnArgs& a, const sage_paged_kv& kv, cudaStream_t s) {
   // Two row tiles where the batch's mean rows per sequence need more than one: K and V are then read
-  // once for 32 rows.
+  // once for 32 rows.  For a tree only where that reading counts: the second tile costs a small batch 2-5 us (28 rows, 8 heads, one
+  // tile twice / two tiles: 4 x 650 keys of 128 channels 12.1 / 16.3 us bf16, 12.7 / 20.3 E4M3; 8 x 4000 37.9 / 39.6, 33.5 / 37.4;
+  // 16 x 4000 85.8 / 59.2, 56.2 / 66.4; 32 x 8000 307 / 175, 178 / 178; of 64 channels 4 x 2000 12.4 / 13.8, 13.3 / 16.5,
+  // 8 x 4000 23.7 / 22.3, 22.9 / 22.5).
   const int64_t rows = static_cast<int64_t>(a.b.n_tokens) * (a.hq / a.hkv);
-  return rows > 16 * static_cast<int64_t>(a.b.n_seqs) ? launch_t<D, kE4M3, 2, kTree>(a, kv, s) : launch_t<D, kE4M3, 1, kTree>(a, kv, s);
+  const int64_t keys = static_cast<int64_t>(a.b.n_seqs) * a.b.cap * a.hkv;
+  const bool small = kTree && keys <= (D == 64 ? 1 << 17 : kE4M3 ? 1 << 20 : 1 << 18);
+  return rows > 16 * static_cast<int64_t>(a.b.n_seqs) && !small ? launch_t<D, kE4M3, 2, kTree>(a, kv, s) : launch_t<D, kE4M3, 1, kTree>(a, kv, s);
 }
 
 template <bool kTree>
