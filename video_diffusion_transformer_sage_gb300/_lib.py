@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 import re
@@ -394,11 +395,22 @@ def sage_smooth_quant_qk_rmsnorm_rope(q: torch.Tensor, k: torch.Tensor, gamma_q:
 
 
 # ------------------------------------------------------------------- paged K/V cache (include/sage_paged.h)
+@functools.lru_cache(maxsize=None)
+def _driver():
+    return ctypes.CDLL("libcuda.so.1")
+
+
+@functools.lru_cache(maxsize=None)
+def _side_stream(index: int) -> torch.cuda.Stream:
+    """The stream of a device that status blocks are zeroed on, apart from whatever else goes on."""
+    return torch.cuda.Stream(index)
+
+
 @contextlib.contextmanager
 def _capture_apart():
     """What this thread enqueues and waits for on streams that are not captured does not end a capture on another one
     (cuThreadExchangeStreamCaptureMode: relaxed)."""
-    mode, driver = ctypes.c_int(2), ctypes.CDLL("libcuda.so.1")
+    mode, driver = ctypes.c_int(2), _driver()
     if driver.cuThreadExchangeStreamCaptureMode(ctypes.byref(mode)) != 0:
         raise RuntimeError("cuThreadExchangeStreamCaptureMode failed")
     try:
@@ -418,8 +430,8 @@ class _StatusOwner:
         if self._status is None:
             # Zeroed before this returns, on a stream of its own: no call on whatever stream comes before that, and inside
             # a graph capture the zeroing is no part of the graph, whose replays would erase records.
-            side = torch.cuda.Stream(self.device)
             with _capture_apart():
+                side = _side_stream(self.device.index)
                 with torch.cuda.stream(side):
                     status = torch.zeros(self._status_bytes, dtype=torch.uint8, device=self.device)
                 side.synchronize()

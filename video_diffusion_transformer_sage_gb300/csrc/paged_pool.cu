@@ -36,8 +36,8 @@ struct PoolArgs {
   int32_t* list;   // [n_pages]: the free pages in ascending order
 };
 
+// What one CTA of the cluster wrote before it, the others read behind it (past L1: __ldcg).
 __device__ __forceinline__ void cluster_barrier() {
-  __threadfence();
   asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
 __device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
@@ -99,45 +99,62 @@ __device__ __forceinline__ uint32_t free_of_four(const PoolArgs& a, int p, int t
   }
   return (c[0] == 0) | (c[1] == 0) << 1 | (c[2] == 0) << 2 | (c[3] == 0) << 3;
 }
-__device__ __forceinline__ void count_free(const PoolArgs& a) {
+// A warp's part of up to kKept * 128 pages (all of 2^19) is kept as bits between counting and listing.
+constexpr int kKept = 16;
+__device__ __forceinline__ uint64_t count_free(const PoolArgs& a) {
   const int lane = threadIdx.x & 31;
   int from, to, n = 0;
   part_of_counts(a, from, to);
-  constexpr int kAhead = 8;
-  for (int p = from + lane * 4; p - lane * 4 < to; p += 128 * kAhead) {
-    uint32_t f[kAhead];
+  uint64_t kept = 0;
+  for (int p0 = from; p0 < to; p0 += 128 * kKept) {
+    uint32_t f[kKept];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) f[k] = p + k * 128 < to ? free_of_four(a, p + k * 128, to) : 0;
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) n += __popc(f[k]);
-  }
-  n = warp_sum(n);
-  if (lane == 0) a.sums[blockIdx.x * kPoolWarps + (threadIdx.x >> 5)] = n;
-}
-// Writes this warp's free pages to the list, which begins with `before` of other warps', up to `most` in all.
-__device__ __forceinline__ void list_free(const PoolArgs& a, int before, int64_t most) {
-  const int lane = threadIdx.x & 31;
-  int from, to;
-  part_of_counts(a, from, to);
-  constexpr int kAhead = 4;
-  for (int p0 = from; p0 < to && before < most; p0 += 128 * kAhead) {
-    uint32_t f[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
+    for (int k = 0; k < kKept; ++k) {
       const int p = p0 + k * 128 + lane * 4;
       f[k] = p < to ? free_of_four(a, p, to) : 0;
     }
+    kept = 0;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int incl = warp_scan(__popc(f[k]));
-      int at = before + incl - __popc(f[k]);
+    for (int k = 0; k < kKept; ++k) kept |= static_cast<uint64_t>(f[k]) << (4 * k);
+    n += __popcll(kept);
+  }
+  n = warp_sum(n);
+  if (lane == 0) a.sums[blockIdx.x * kPoolWarps + (threadIdx.x >> 5)] = n;
+  return kept;
+}
+// Writes this warp's free pages to the list, which begins with `before` of other warps', up to `most` in all.
+__device__ __forceinline__ void list_free(const PoolArgs& a, uint64_t kept, int before, int64_t most) {
+  const int lane = threadIdx.x & 31;
+  int from, to;
+  part_of_counts(a, from, to);
+  for (int p0 = from; p0 < to && before < most; p0 += 128 * kKept) {
+    if (to - from > 128 * kKept) {   // more than was kept: read again
+      kept = 0;
+      for (int k = 0; k < kKept; ++k) {
+        const int p = p0 + k * 128 + lane * 4;
+        if (p < to) kept |= static_cast<uint64_t>(free_of_four(a, p, to)) << (4 * k);
+      }
+    }
+    // The free pages of four groups of 128 added up at a time, a byte each (at most 128).
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if ((f[k] >> j) & 1u) {
-          if (at < most) a.list[at] = p0 + k * 128 + lane * 4 + j;
-          ++at;
-        }
-      before += __shfl_sync(0xffffffffu, incl, 31);
+    for (int k4 = 0; k4 < kKept; k4 += 4) {
+      const uint32_t bits = static_cast<uint32_t>(kept >> (4 * k4)) & 0xFFFFu;
+      uint32_t mine = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mine |= __popc((bits >> (4 * k)) & 15u) << (8 * k);
+      const uint32_t incl = static_cast<uint32_t>(warp_scan(static_cast<int>(mine)));
+      const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        int at = before + static_cast<int>(((incl >> (8 * k)) & 255u) - ((mine >> (8 * k)) & 255u));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if ((bits >> (4 * k + j)) & 1u) {
+            if (at < most) a.list[at] = p0 + (k4 + k) * 128 + lane * 4 + j;
+            ++at;
+          }
+        before += static_cast<int>((all >> (8 * k)) & 255u);
+      }
     }
   }
 }
@@ -217,6 +234,7 @@ __device__ __forceinline__ void part_of_items(int n, int& from, int& to) {
 __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads, 1)
     paged_reserve_kernel(const __grid_constant__ PoolArgs a) {
   __shared__ int64_t sh[2][kPoolWarps];
+  __shared__ int32_t mine[kMaxSeqs / kPoolCtas];   // the needs of the CTA's rows
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int cap = a.max_pages << a.page_shift;   // at most 2^30
   int from, to;
@@ -235,15 +253,14 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     const int32_t* entries = a.table + r * a.table_stride;
     for (int i = first + lane; i < last; i += 32) n += entries[i] < 0;
     n = warp_sum(n);
-    if (lane == 0) a.need[r] = n;
+    if (lane == 0) a.need[r] = mine[r - from] = n;
   }
-  count_free(a);
+  const uint64_t kept = count_free(a);
   cluster_barrier();
-  auto need = [&](int r) { return __ldcg(a.need + r); };
-  const PoolSums s = add_up(a, a.n_rows, from, need, sh);
-  list_free(a, s.free_before, s.all);
+  const PoolSums s = add_up(a, a.n_rows, from, [&](int r) { return __ldcg(a.need + r); }, sh);
+  list_free(a, kept, s.free_before, s.all);
   cluster_barrier();
-  for_each_in_order(from, to, s.before, need, [&](int r, int n, int64_t at) {
+  for_each_in_order(from, to, s.before, [&](int r) { return mine[r - from]; }, [&](int r, int n, int64_t at) {
     const bool good = n == 0 || at + n <= s.free_all;
     if (a.ok && lane == 0) a.ok[r] = good;
     if (n == 0 || !good) return;
@@ -269,6 +286,7 @@ __device__ __forceinline__ int fork_mark(int k) { return INT32_MIN + k; }
 __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads, 1)
     paged_fork_kernel(const __grid_constant__ PoolArgs a) {
   __shared__ int64_t sh[2][kPoolWarps];
+  __shared__ uint8_t mine[kMaxSeqs / kPoolCtas];   // of the CTA's forks: 1 has its row, 2 is possible, 4 needs a page
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int cap = a.max_pages << a.page_shift;
   int from, to;
@@ -289,26 +307,23 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
       if (len < 0 || len > cap) record_bad_index(a.status, kWhereLength);
     }
   }
-  count_free(a);
+  const uint64_t kept = count_free(a);
   cluster_barrier();
   auto length = [&](int k) { return min(max(__ldg(a.len + k), 0), cap); };
-  // Whether fork k has its row, and whether its source is no child itself.
-  auto has_row = [&](int k) {
+  // Whether fork k has its row (its mark stands there), its source is no child itself, and a begun page is to be had.  Every CTA
+  // asks for all forks, before any row is written (behind the second barrier).
+  const PoolSums s = add_up(a, a.n_forks, from, [&](int k) {
     const int src = __ldg(a.src + k), dst = __ldg(a.dst + k);
-    return exists(src) && exists(dst) && src != dst && __ldcg(row_of(dst)) == fork_mark(k);
-  };
-  auto possible = [&](int k) { return has_row(k) && __ldcg(row_of(__ldg(a.src + k))) >= fork_mark(a.n_forks); };
-  auto need = [&](int k) { return possible(k) && (length(k) & ((1 << a.page_shift) - 1)) != 0 ? 1 : 0; };
-  // Every CTA asks for all forks, before any row is written (behind the second barrier).
-  const PoolSums s = add_up(a, a.n_forks, from, need, sh);
-  for (int k = from + warp; k < to; k += kPoolWarps) {
-    const int n = has_row(k) | possible(k) << 1 | need(k) << 2;
-    if (lane == 0) a.need[k] = n;
-  }
-  list_free(a, s.free_before, s.all);
+    int state = exists(src) && exists(dst) && src != dst && __ldcg(row_of(dst)) == fork_mark(k) ? 1 : 0;
+    if (state && __ldcg(row_of(src)) >= fork_mark(a.n_forks)) state |= 2;
+    if (state == 3 && (length(k) & ((1 << a.page_shift) - 1)) != 0) state |= 4;
+    if (k >= from && k < to) mine[k - from] = static_cast<uint8_t>(state);
+    return state >> 2;
+  }, sh);
+  list_free(a, kept, s.free_before, s.all);
   cluster_barrier();
-  for_each_in_order(from, to, s.before, [&](int k) { return __ldcg(a.need + k) >> 2; }, [&](int k, int n, int64_t at) {
-    const int state = __ldcg(a.need + k);
+  for_each_in_order(from, to, s.before, [&](int k) { return mine[k - from] >> 2; }, [&](int k, int n, int64_t at) {
+    const int state = mine[k - from];
     const bool can = state & 2, good = can && (n == 0 || at < s.free_all);
     const int len = length(k), full = len >> a.page_shift, part = len & ((1 << a.page_shift) - 1);
     int c_src = -1, c_dst = -1, c_tokens = 0;
