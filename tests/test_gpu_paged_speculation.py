@@ -109,7 +109,7 @@ def test_speculative_decoding(fmt, d, hq, page, most):
         q, stored = w.append(q_lens, batch, tree.positions)
         out = sage.sage_paged_attn_tree(q, w.cache, batch, tree, ws=w.ws)
         p, seen = w.problem(q_lens), tree_ref.closure(q_lens, parents)[0]
-        paged_ref.check_attention(p, out, tree_ref.attention(p, q, seen))
+        tree_ref.check_attention(p, out, tree_ref.attention(p, q, seen), q)
         # one path from a root to some node, or nothing, is accepted
         keep, at = [], 0
         for b, n in enumerate(q_lens):

@@ -158,12 +158,14 @@ def _tree(q_lens, parents, rows, window=0, kind="tree", seed=0):
     return seen, depth, sage.PagedTree(mask[:, :words], _i32(depth + [10 ** 6] * (rows - len(depth))))
 
 
-def _check(p, out, lse, ref):
-    paged_ref.check_attention(p, out, ref)
+def _check(p, out, lse, ref, q=None):
+    q = p.q if q is None else q
+    tree_ref.check_attention(p, out, ref, q)
     # ln of the sum: score errors, and the rounded weights' 2^-8 (see paged_ref.attention_bound)
     empty = torch.isinf(ref[1])
     assert torch.equal(torch.isinf(lse[:p.n]), empty)
     lim = p.d * 2.0 ** -23 * ref[3] / math.sqrt(p.d) + 1.01 * 2.0 ** -8 + 1e-5 * (1 + ref[1].abs())
+    lim = lim + tree_ref.score_slack(p, q, ref)
     assert ((lse[:p.n].double() - ref[1]).abs() <= lim)[~empty].all()
 
 

@@ -4,6 +4,7 @@ import random
 
 import torch
 
+import paged_ref
 from paged_ref import Problem
 
 
@@ -43,6 +44,27 @@ def packed(seen, words, rows, fill=0):
         out[at:at + n] = (wide[:, :words * 32].view(n, words, 32) << torch.arange(32)).sum(-1)
         at += n
     return torch.where(out >= 1 << 31, out - (1 << 32), out).to(torch.int32)
+
+
+def score_slack(p: Problem, q, ref, sm_scale=None):
+    """What the bounds of paged_ref.attention_bound grow by with an E4M3 cache and many rows, relative on a weight, [n, hq].
+
+    There the kernel holds q as the sum of two E4M3 values times a power of two, the row's largest in [2^7, 2^8): the first is at
+    most 2^-4 of the value off, the second represents that difference but for half a step of E4M3's smallest, 2^-10.  So a
+    channel is at most 2^-10 off where the row's largest is at least 2^7: 2^-17 of it, and a score at most
+    2^-17 max_c |q_c| sum_c |k_c| sm; a weight is a ratio of two exponentials: twice that."""
+    if p.fmt != "e4m3":
+        return torch.zeros_like(ref[1])
+    sm = 1 / math.sqrt(p.d) if sm_scale is None else sm_scale
+    k = torch.nan_to_num(p.values(p.k_pages, p.k_scale).abs()).sum(-1).amax((0, 1))        # [hkv], over all stored keys
+    return 2 * 2.0 ** -17 * q[:p.n].double().abs().amax(-1) * k.repeat_interleave(p.hq // p.hkv) * sm
+
+
+def check_attention(p: Problem, got, ref, q, sm_scale=None):
+    off = (got[:p.n].double() - ref[0]).abs() - paged_ref.attention_bound(p, ref, sm_scale)
+    off -= score_slack(p, q, ref, sm_scale)[..., None] * ref[2]
+    assert torch.isfinite(got[:p.n].float()).all()
+    assert float(off.max()) <= 0.0, (float(off.max()), [int(i) for i in torch.nonzero(off == off.max())[0]])
 
 
 def attention(p: Problem, q, seen, depth=None, window=0, sm_scale=None):

@@ -63,21 +63,25 @@ struct ChunkCfg {
   static constexpr int kTileBytes = kBN * D * 2;              // a K or V tile in 16 bits
   static constexpr int kStageBytes = 2 * kTileBytes;
   // A tree has few rows for the keys that it sees, so the loads have to be far ahead: K and V apart, each in a ring of
-  // its own, and with E4M3 rings of staging tiles in place of widened ones.  (One row tile at D = 64 with the shared ring
-  // of four: 97 us for 12032 keys of 152 heads in bf16, 112 in E4M3, of which 73 and 87 remain when K and V come from L2: a
-  // load's latency in every step.)
-  static constexpr int kKStages = !kTree ? (D == 128 ? 2 : 4) : kE4M3 ? (D == 128 ? 1 : 2) : (D == 128 ? 2 : 5);
+  // its own.  (One row tile at D = 64 with the shared ring of four: 97 us for 12032 keys of 152 heads in bf16, 112 in E4M3, of
+  // which 73 and 87 remain when K and V come from L2: a load's latency in every step.)  With E4M3 K is not widened either: Q
+  // is split into two E4M3 values, and Q K^T takes the codes as they lie (kNativeK; widening both took ~2100 cycles a tile,
+  // 148 us of verify_e4m3).
+  static constexpr bool kNativeK = kTree && kE4M3;
+  static constexpr int kKStages = !kTree ? (D == 128 ? 2 : 4) : kE4M3 ? (D == 128 ? 3 : 6) : (D == 128 ? 2 : 5);
   static constexpr int kVStages = !kTree ? (D == 128 ? 2 : 4) : kE4M3 ? (D == 128 ? 2 : 3) : (D == 128 ? 2 : 5);
-  static constexpr int kRawStages = kTree && kE4M3 ? (D == 128 ? 2 : 5) : 1;
-  static constexpr int kBits = 8;                             // key tiles whose loaded boxes are remembered
+  static constexpr int kRawStages = kNativeK ? (D == 128 ? 3 : 7) : 1;
+  static constexpr int kRawSides = kNativeK ? 1 : 2;          // staging tiles of V, or of K and V
+  static constexpr int kBits = kNativeK ? 16 : 8;             // key tiles whose loaded boxes are remembered
   // K and V of a tile have barriers of their own where the ring is short (D = 128): a K stage is free again once
   // Q K^T has read it, a softmax before P V is done with V (chunk_frames 2358 -> 2236 us).  The four stages at
   // D = 64 hide the loads of prompts anyway, and there the extra waits of the issuing warp cost 3 %.
   static constexpr bool kSplitKV = kTree || D == 128;
-  static constexpr int kKStep = kTree ? kTileBytes : kStageBytes, kVStep = kKStep;   // from stage to stage
-  static constexpr int kVBase = kTree ? kKStages * kTileBytes : kTileBytes;          // from the first K tile to the first V tile
   static constexpr int kRawTile = kBN * D;                    // a tile of codes
-  static constexpr int kRawBytes = kE4M3 ? 2 * kRawTile * kRawStages : 0;
+  static constexpr int kKTile = kNativeK ? kRawTile : kTileBytes;
+  static constexpr int kKStep = kTree ? kKTile : kStageBytes, kVStep = kTree ? kTileBytes : kStageBytes;   // from stage to stage
+  static constexpr int kVBase = kTree ? kKStages * kKTile : kTileBytes;   // from the first K tile to the first V tile
+  static constexpr int kRawBytes = kE4M3 ? kRawSides * kRawTile * kRawStages : 0;
   // Tensor memory columns: S_t at 128 t, O_t at 256 + D t; P_t over S_t, or at 384 + 64 t (D = 64).
   static constexpr int kColO0 = 256;
   static constexpr bool kSepP = D == 64;
@@ -89,13 +93,13 @@ struct ChunkCfg {
   // is no room for both, and they leave through the slot's Q tile first.
   static constexpr bool kEarlyQ = !(kE4M3 && D == 128);
   static constexpr int kKvOff = 2 * kQTileBytes;
-  static constexpr int kRawOff = kKvOff + (kKStages + kVStages) * kTileBytes;
+  static constexpr int kRawOff = kKvOff + kKStages * kKTile + kVStages * kTileBytes;
   static constexpr int kOutOff = kRawOff + kRawBytes;
   static constexpr int kExpOff = kOutOff + (kEarlyQ ? 2 * 16384 : 0);   // biased exponent of each Q row (E4M3)
   static constexpr int kBarOff = kExpOff + (kE4M3 ? 256 : 0);
   // q_full[2], k_full[K stages], v_full[V stages], k_empty, v_empty likewise, s_full[2], p_full[2], pv_done[2], s_free[2], o_free[2],
-  // ml_full, ml_empty, mma_final, raw_full[2][R] (K, V), raw_empty[2][R], unit_full[2], unit_empty[2], draw
-  static constexpr int kNumBars = 2 * (kKStages + kVStages) + 20 + 4 * kRawStages;
+  // ml_full, ml_empty, mma_final, raw_full[2][R] (K, V; V alone), raw_empty, unit_full[2], unit_empty[2], draw
+  static constexpr int kNumBars = 2 * (kKStages + kVStages) + 20 + 2 * kRawSides * kRawStages;
   static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;
   // Registers a thread: launched at 168 (384 threads) or 128 (512).
   static constexpr int kRegsRoles = 72, kRegsSoftmax = kE4M3 ? 184 : 216, kRegsWiden = 72;
@@ -270,8 +274,36 @@ __device__ __forceinline__ void warp_tc_commit(uint64_t* bar) {
       : "memory");
 }
 
+// E4M3 by E4M3.
+__device__ __forceinline__ void warp_mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// High descriptor word of a tile with the 64-byte swizzle: 8 rows of 64 bytes are 512 bytes apart (mode 4).
+constexpr uint32_t kSdescHi64 = (512u >> 4) | (1u << 14) | (4u << 29);
+template <int D>
+__device__ __forceinline__ uint64_t raw_desc_of_lo(uint32_t lo) {
+  return D == 128 ? sdesc_of_lo(lo) : (static_cast<uint64_t>(kSdescHi64) << 32) | lo;
+}
+
 template <int D, bool kE4M3, bool kTree>
 __device__ __forceinline__ void issue_qk(uint32_t s_tmem, uint32_t ql, uint32_t kl) {
+  if constexpr (ChunkCfg<D, kE4M3, kTree>::kNativeK) {
+    // Both values of Q, 32 channels a step: of D = 128 in a panel each, of D = 64 in a half of the row each.
+    constexpr uint32_t idesc8 = idesc_f32acc(kBM, kBN);
+#pragma unroll
+    for (int part = 0; part < 2; ++part)
+#pragma unroll
+      for (int kk = 0; kk < D / 32; ++kk) {
+        const uint32_t qo = (D == 128 ? part * ChunkCfg<D, kE4M3, kTree>::kPanelBytes + kk * 32 : part * 64 + kk * 32) >> 4;
+        warp_mma_f8_ss(s_tmem, sdesc_of_lo(ql + qo), raw_desc_of_lo<D>(kl + (kk * 32 >> 4)), idesc8, part + kk > 0 ? 1u : 0u);
+      }
+    return;
+  }
   constexpr uint32_t idesc = idesc_f32acc(kBM, kBN) | (kE4M3 ? 0u : kIdescBf16);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
@@ -414,7 +446,7 @@ struct ChunkShared {
   Unit unit[2];                    // the items in work and next
   int skip;
   volatile int abort;
-  uint32_t bits[8], raw_bits[2][5];   // boxes loaded: of the last key tiles, and of the staging K and V tiles
+  uint32_t bits[16], raw_bits[2][7];   // boxes loaded: of the last key tiles, and of the staging K and V tiles
   uint32_t tmem;
   float2 ml[128];                  // slot 1's maxima and sums (units of one row tile)
 };
@@ -450,8 +482,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3, kTree>::kThreads, 1)
   uint64_t* ml_empty = ml_full + 1;
   uint64_t* mma_final = ml_empty + 1;
   uint64_t* raw_full = mma_final + 1;
-  uint64_t* raw_empty = raw_full + 2 * RS;
-  uint64_t* unit_full = raw_empty + 2 * RS;
+  uint64_t* raw_empty = raw_full + C::kRawSides * RS;
+  uint64_t* unit_full = raw_empty + C::kRawSides * RS;
   uint64_t* unit_empty = unit_full + 2;
   uint64_t* draw = unit_empty + 2;
   const PagedAttnArgs& a = p.a;
@@ -460,7 +492,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3, kTree>::kThreads, 1)
   if (threadIdx.x == 0) {
     sh.skip = *reinterpret_cast<volatile int32_t*>(a.status) == kStatusTimeout;
     sh.abort = 0;
-    for (int i = 0; i < KS + VS; ++i) mbar_init(k_full + i, !kE4M3 ? 1 : kTree ? 4 : 128);        // and v_full
+    for (int i = 0; i < KS + VS; ++i) mbar_init(k_full + i, !kE4M3 || (kTree && i < KS) ? 1 : kTree ? 4 : 128);        // and v_full
     for (int i = 0; i < KS + VS; ++i) mbar_init(k_empty + i, 1);                     // and v_empty
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + i, 128);
@@ -469,7 +501,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3, kTree>::kThreads, 1)
       mbar_init(pv_done + i, 1);
       mbar_init(s_free + i, 4);
       mbar_init(o_free + i, 128);
-      for (int k = 0; k < RS; ++k) {
+      for (int k = 0; k < RS && i < C::kRawSides; ++k) {
         mbar_init(raw_full + i * RS + k, 1);
         mbar_init(raw_empty + i * RS + k, kTree ? 4 : 128);
       }
@@ -626,25 +658,29 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3, kTree>::kThreads, 1)
             const CUtensorMap* map = kv ? &vmap : &kmap;
             const uint32_t ring = kv ? VS : KS, s = ct % ring;
             const bool own_bar = C::kSplitKV || kv == 0;   // V shares K's barriers otherwise
-            uint64_t* full = kE4M3 ? raw_full + kv * RS + rs : (kv && own_bar ? v_full : k_full) + s;
-            if (kE4M3) {
-              if (ct >= RS) ok = wait(raw_empty + kv * RS + rs, (ct / RS - 1) & 1, kWherePagedEmpty);
+            const bool staged = kE4M3 && !(C::kNativeK && kv == 0);
+            const int side = C::kNativeK ? 0 : kv;
+            uint64_t* full = staged ? raw_full + side * RS + rs : (kv && own_bar ? v_full : k_full) + s;
+            if (staged) {
+              if (ct >= RS) ok = wait(raw_empty + side * RS + rs, (ct / RS - 1) & 1, kWherePagedEmpty);
             } else if (own_bar && ct >= ring) {
               ok = wait((kv || !C::kSplitKV ? v_empty : k_empty) + s, (ct / ring - 1) & 1, kWherePagedEmpty);
             }
             ok = !__any_sync(0xffffffffu, !ok || sh.abort);
             if (!ok) break;
             if (lane == 0) {
-              if (kE4M3) sh.raw_bits[kv][rs] = bits;
-              else if (kv == 0) sh.bits[ct % C::kBits] = bits;
+              if (staged) sh.raw_bits[side][rs] = bits;
+              if (!kE4M3 && kv == 0) sh.bits[ct % C::kBits] = bits;
+              if (C::kNativeK && kv == 0) sh.bits[ct % C::kBits] = bits;
               if (kE4M3 || own_bar)
                 mbar_arrive_expect_tx(full, __popc(bits) * box_bytes * (kE4M3 || C::kSplitKV ? 1u : 2u));
             }
             __syncwarp();
             if (good) {
               if (kE4M3) {
-                tma_load_4d(smem_u32(smem + C::kRawOff) + (rs * 2 + kv) * C::kRawTile + (lane << p.box_shift) * D, map, full, 0, h,
-                            slot_in_page, page);
+                const uint32_t tile = staged ? smem_u32(smem + C::kRawOff) + (rs * C::kRawSides + side) * C::kRawTile
+                                             : smem_u32(sKV) + s * C::kKStep;
+                tma_load_4d(tile + (lane << p.box_shift) * D, map, full, 0, h, slot_in_page, page);
               } else {
                 const uint32_t dst = smem_u32(sKV) + (kv ? C::kVBase + s * C::kVStep : s * C::kKStep) + (lane << p.box_shift) * 128;
 #pragma unroll
@@ -658,9 +694,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3, kTree>::kThreads, 1)
       }
       if (!ok) {
         // After a timeout: the copies issued have landed before the CTA ends.
-        if (kE4M3) {
+        if (kE4M3 && !(C::kNativeK && kv0 == 0)) {
           for (uint32_t i = issued > RS ? issued - RS : 0; i < issued; ++i)
-            mbar_wait(raw_full + kv0 * RS + i % RS, (i / RS) & 1, kChunkWaitNs);
+            mbar_wait(raw_full + (C::kNativeK ? 0 : kv0) * RS + i % RS, (i / RS) & 1, kChunkWaitNs);
         } else {
           const uint32_t ring = kv0 ? VS : KS;
           for (uint32_t i = issued > ring ? issued - ring : 0; i < issued; ++i)
@@ -857,46 +893,22 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3, kTree>::kThreads, 1)
         }
       }
     };
-    // Tile ct of a tree: K and V read together where there are registers for both, one arrival per warp.
+    // V of a tree's tile ct, one arrival per warp.
     auto widen_ahead = [&](uint32_t ct, uint32_t rs, int key, int ulo, int uhi, bool some) {
-      constexpr bool kBoth = D == 64;
-      const uint32_t sk = ct % KS, sv = ct % VS, phase = (ct / RS) & 1, at = raw + rs * 2 * C::kRawTile;
-      uint4 v[kBoth ? 2 : 1][D / 16];
-      bool ok = warp_wait(raw_full + rs, phase);
-      read_raw(at, v[0]);
-      if (kBoth) {
-        ok = ok && warp_wait(raw_full + RS + rs, phase);
-        read_raw(at + C::kRawTile, v[kBoth]);
-      }
+      const uint32_t sv = ct % VS;
+      uint4 v[D / 16];
+      bool ok = warp_wait(raw_full + rs, (ct / RS) & 1);
+      read_raw(raw + rs * C::kRawTile, v);
       const uint32_t bits = sh.raw_bits[0][rs];
       const bool live = ((bits >> (r >> p.box_shift)) & 1u) && key >= ulo && key < uhi && some;
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(raw_empty + rs);
-        if (kBoth) mbar_arrive(raw_empty + RS + rs);
-      }
-      if (ok && ct >= KS) ok = warp_wait(k_empty + sk, (ct / KS - 1) & 1);
+      if (lane == 0) mbar_arrive(raw_empty + rs);
+      if (ok && ct >= VS) ok = warp_wait(v_empty + sv, (ct / VS - 1) & 1);
       if (!ok || __any_sync(0xffffffffu, sh.abort)) {
         if (!ok) give_up(a.status, kWherePagedFull, &sh.abort);
         return false;
       }
-      if (r == 0) sh.bits[ct % C::kBits] = bits;
-      write_wide(sKV + sk * C::kKStep, v[0], live);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(k_full + sk);
-      if (!kBoth) {
-        ok = warp_wait(raw_full + RS + rs, phase);
-        read_raw(at + C::kRawTile, v[0]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(raw_empty + RS + rs);
-      }
-      if (ok && ct >= VS) ok = warp_wait(v_empty + sv, (ct / VS - 1) & 1);
-      if (!ok) {
-        give_up(a.status, kWherePagedFull, &sh.abort);
-        return false;
-      }
-      write_wide(sKV + C::kVBase + sv * C::kVStep, v[kBoth], live);
+      write_wide(sKV + C::kVBase + sv * C::kVStep, v, live);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(v_full + sv);
@@ -916,11 +928,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3, kTree>::kThreads, 1)
         const uint32_t rs = ct % RS;
         // A tree's new tokens: those that some row of the unit sees.
         const bool some = !kTree || tree_key_seen(a, start, tok0, tok1, key_r - lane + j * kBN, prefix);
-        if (kTree) {
+        if constexpr (kTree) {
           ok = widen_ahead(ct, rs, key_r + j * kBN, ulo, uhi, some);
-          if (!ok) break;
-          continue;
-        }
+        } else {
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           const uint32_t ring = kv ? VS : KS, s = ct % ring;
@@ -962,6 +972,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3, kTree>::kThreads, 1)
           }
           fence_proxy_async_smem();
           if (C::kSplitKV || kv == 1) mbar_arrive((kv && C::kSplitKV ? v_full : k_full) + s);
+        }
         }
       }
     }
@@ -1018,12 +1029,35 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3, kTree>::kThreads, 1)
           int e = static_cast<int>((__float_as_uint(mx) >> 23) & 255) - 127;
           e = mx == 0.0f ? 0 : min(max(e, -126), 126);
           const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          uint32_t f[4];
+          if constexpr (C::kNativeK) {
+            // The sum of two E4M3 values times 2^(e - 7), the row's largest in [128, 256): exact but for values 2^-10
+            // below it, which keep an absolute error of 2^-17 of the row's largest.  What is no number stays none.
+            uint16_t part[2][4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            f[x] = pack2<true>(__uint_as_float(w[x] << 16) * down, __uint_as_float(w[x] & 0xFFFF0000u) * down);
-          *reinterpret_cast<uint4*>(tile + (c8 >> 3) * C::kPanelBytes + rr * 128 + (((c8 & 7) ^ (rr & 7)) << 4)) =
-              make_uint4(f[0], f[1], f[2], f[3]);
+            for (int x = 0; x < 4; ++x) {
+              float y[2] = {__uint_as_float(w[x] << 16) * down * 128.0f, __uint_as_float(w[x] & 0xFFFF0000u) * down * 128.0f};
+#pragma unroll
+              for (int i = 0; i < 2; ++i) y[i] = fabsf(y[i]) < INFINITY ? y[i] : __uint_as_float(0x7FFFFFFFu);
+              part[0][x] = e4m3x2(y[0], y[1]);
+              uint32_t back;
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(part[0][x]));
+              const float2 first = __half22float2(*reinterpret_cast<const __half2*>(&back));
+              part[1][x] = e4m3x2(y[0] - first.x, y[1] - first.y);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int ch = (D == 64 ? i * 4 : 0) + (c8 >> 1);   // 16-byte chunk of the row
+              *reinterpret_cast<uint2*>(tile + (D == 128 ? i * C::kPanelBytes : 0) + rr * 128 + ((ch ^ (rr & 7)) << 4) + (c8 & 1) * 8) =
+                  make_uint2(pack_h2(part[i][0], part[i][1]), pack_h2(part[i][2], part[i][3]));
+            }
+          } else {
+            uint32_t f[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              f[x] = pack2<true>(__uint_as_float(w[x] << 16) * down, __uint_as_float(w[x] & 0xFFFF0000u) * down);
+            *reinterpret_cast<uint4*>(tile + (c8 >> 3) * C::kPanelBytes + rr * 128 + (((c8 & 7) ^ (rr & 7)) << 4)) =
+                make_uint4(f[0], f[1], f[2], f[3]);
+          }
           if (c8 == 0) q_exp[t * 128 + rr] = static_cast<uint8_t>(127 + e);
         }
       }
@@ -1053,7 +1087,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3, kTree>::kThreads, 1)
         // (In a unit of one row tile slot 0's warps wrote the exponents.)
         if (one && t == 1) ok = wait(q_full, k & 1, kWherePagedFull);
         else __syncwarp();
-        c *= __ldg(a.k_scale + u.h) * __uint_as_float(static_cast<uint32_t>(q_exp[first + r]) << 23);
+        c *= __ldg(a.k_scale + u.h) * __uint_as_float(static_cast<uint32_t>(q_exp[first + r]) << 23) *
+             (C::kNativeK ? 0.0078125f : 1.0f);
       }
       float m = -INFINITY, l = 0.0f;
       const int key_t0 = u.t0 * kBN;
