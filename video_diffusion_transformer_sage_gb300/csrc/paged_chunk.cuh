@@ -624,6 +624,67 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3, kTree>::kThreads, 1)
         next_item[0] = next_item[1] = 0;
     } else if (warp == 0 || (C::kTwoLoaders && warp == 3)) {
       // ------------------------------------------------------------ page table and TMA
+      if constexpr (kTree && (kE4M3 || D == 64)) {
+        // A tree's K, and its V (E4M3: into the staging tiles): a loading warp and a ring for each.  The stage and its turn go
+        // along with the tiles, the next tile's page entries are on their way while this one waits (the loop below took
+        // ~1350 cycles a tile, longer than the arithmetic of a small one: E4M3 at D = 64 79 -> 75 us for 12032 keys of 152 heads,
+        // pages of 16 tokens 89 -> 75).
+        const bool is_k = warp == 0;
+        const CUtensorMap* map = is_k ? &kmap : &vmap;
+        tma_prefetch_desc(map);
+        const bool staged = C::kNativeK && !is_k;
+        uint64_t* full = is_k ? k_full : staged ? raw_full : v_full;
+        uint64_t* empty = is_k ? k_empty : staged ? raw_empty : v_empty;
+        const uint32_t ring = is_k ? KS : staged ? RS : VS, step = is_k ? C::kKStep : staged ? C::kRawTile : C::kVStep;
+        constexpr int kRow = kE4M3 ? D : 128;   // bytes of a key in a stage
+        const uint32_t base = smem_u32(is_k ? sKV : staged ? smem + C::kRawOff : sKV + C::kVBase) + (lane << p.box_shift) * kRow;
+        const int box = 1 << p.box_shift;
+        const uint32_t box_bytes = static_cast<uint32_t>(box) * D * (kE4M3 ? 1 : 2);
+        uint32_t st = 0, turn = 0, ct = 0;   // the stage, how often the ring has gone round, tiles
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+          ok = wait(unit_full + (k & 1), (k >> 1) & 1, kWherePagedEmpty);
+          if (!ok) break;
+          const Unit& e = sh.unit[k & 1];
+          const int ntiles = e.nt, h = e.h, ulo = e.ulo, uhi = e.uhi;
+          const int32_t* row = a.b.table + e.b * a.b.table_stride;
+          int key0 = e.t0 * kBN + (lane << p.box_shift);
+          release_unit(k);
+          if (ntiles < 0) break;
+          auto needed = [&] { return lane < boxes && key0 < uhi && key0 + box > ulo; };
+          bool need = needed();
+          int page = need ? __ldg(row + (key0 >> a.b.page_shift)) : -1;
+          for (int j = 0; j < ntiles; ++j, ++ct) {
+            if (is_k && lane == 0 && j == max(0, ntiles - 3)) mbar_arrive(draw);
+            const bool good = need && page >= 0 && page < a.b.n_pages;
+            if (need && !good) record_bad_index(a.status, kWherePage);
+            const uint32_t bits = __ballot_sync(0xffffffffu, good);
+            const int slot = key0 & ((1 << a.b.page_shift) - 1), at_page = page;
+            key0 += kBN;
+            need = j + 1 < ntiles && needed();
+            page = need ? __ldg(row + (key0 >> a.b.page_shift)) : -1;
+            if (turn > 0 && !(ok = wait(empty + st, (turn - 1) & 1, kWherePagedEmpty))) break;
+            if (lane == 0) {
+              if (staged) sh.raw_bits[0][st] = bits;
+              if (is_k) sh.bits[ct % C::kBits] = bits;
+              mbar_arrive_expect_tx(full + st, __popc(bits) * box_bytes);
+            }
+            __syncwarp();
+            if (good) {
+              const uint32_t dst = base + st * step;
+              tma_load_4d(dst, map, full + st, 0, h, slot, at_page);
+            }
+            if (++st == ring) {
+              st = 0;
+              ++turn;
+            }
+          }
+        }
+        if (!ok) {
+          // After a timeout: the copies issued have landed before the CTA ends.
+          for (uint32_t i = ct > ring ? ct - ring : 0; i < ct; ++i) mbar_wait(full + i % ring, (i / ring) & 1, kChunkWaitNs);
+        }
+      } else {
       const int kv0 = warp == 0 ? 0 : 1, kv1 = C::kTwoLoaders && warp == 0 ? 1 : 2;   // K, V or both
       tma_prefetch_desc(&kmap);
       tma_prefetch_desc(&vmap);
@@ -639,16 +700,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3, kTree>::kThreads, 1)
         const int32_t* row = a.b.table + e.b * a.b.table_stride;
         release_unit(k);
         if (ntiles < 0) break;
-        auto entry = [&](int key0) {
-          return lane < boxes && key0 < uhi && key0 + box > ulo ? __ldg(row + (key0 >> a.b.page_shift)) : -1;
-        };
-        int ahead = kTree ? entry(key00) : 0;   // a tree's next tile's entries are on their way while this one waits
         for (int j = 0; j < ntiles && ok; ++j, ++ct) {
           const int key0 = key00 + j * kBN;
           if (warp == 0 && lane == 0 && j == max(0, ntiles - 3)) mbar_arrive(draw);
           const bool need = lane < boxes && key0 < uhi && key0 + box > ulo;
-          const int page = kTree ? ahead : entry(key0);
-          if (kTree && j + 1 < ntiles) ahead = entry(key0 + kBN);
+          int page = -1;
+          if (need) page = __ldg(row + (key0 >> a.b.page_shift));
           const bool good = need && page >= 0 && page < a.b.n_pages;
           if (need && !good) record_bad_index(a.status, kWherePage);
           const uint32_t bits = __ballot_sync(0xffffffffu, good);
@@ -658,29 +715,25 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3, kTree>::kThreads, 1)
             const CUtensorMap* map = kv ? &vmap : &kmap;
             const uint32_t ring = kv ? VS : KS, s = ct % ring;
             const bool own_bar = C::kSplitKV || kv == 0;   // V shares K's barriers otherwise
-            const bool staged = kE4M3 && !(C::kNativeK && kv == 0);
-            const int side = C::kNativeK ? 0 : kv;
-            uint64_t* full = staged ? raw_full + side * RS + rs : (kv && own_bar ? v_full : k_full) + s;
-            if (staged) {
-              if (ct >= RS) ok = wait(raw_empty + side * RS + rs, (ct / RS - 1) & 1, kWherePagedEmpty);
+            uint64_t* full = kE4M3 ? raw_full + kv * RS + rs : (kv && own_bar ? v_full : k_full) + s;
+            if (kE4M3) {
+              if (ct >= RS) ok = wait(raw_empty + kv * RS + rs, (ct / RS - 1) & 1, kWherePagedEmpty);
             } else if (own_bar && ct >= ring) {
               ok = wait((kv || !C::kSplitKV ? v_empty : k_empty) + s, (ct / ring - 1) & 1, kWherePagedEmpty);
             }
             ok = !__any_sync(0xffffffffu, !ok || sh.abort);
             if (!ok) break;
             if (lane == 0) {
-              if (staged) sh.raw_bits[side][rs] = bits;
-              if (!kE4M3 && kv == 0) sh.bits[ct % C::kBits] = bits;
-              if (C::kNativeK && kv == 0) sh.bits[ct % C::kBits] = bits;
+              if (kE4M3) sh.raw_bits[kv][rs] = bits;
+              else if (kv == 0) sh.bits[ct % C::kBits] = bits;
               if (kE4M3 || own_bar)
                 mbar_arrive_expect_tx(full, __popc(bits) * box_bytes * (kE4M3 || C::kSplitKV ? 1u : 2u));
             }
             __syncwarp();
             if (good) {
               if (kE4M3) {
-                const uint32_t tile = staged ? smem_u32(smem + C::kRawOff) + (rs * C::kRawSides + side) * C::kRawTile
-                                             : smem_u32(sKV) + s * C::kKStep;
-                tma_load_4d(tile + (lane << p.box_shift) * D, map, full, 0, h, slot_in_page, page);
+                tma_load_4d(smem_u32(smem + C::kRawOff) + (rs * 2 + kv) * C::kRawTile + (lane << p.box_shift) * D, map, full, 0,
+                            h, slot_in_page, page);
               } else {
                 const uint32_t dst = smem_u32(sKV) + (kv ? C::kVBase + s * C::kVStep : s * C::kKStep) + (lane << p.box_shift) * 128;
 #pragma unroll
@@ -694,14 +747,15 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3, kTree>::kThreads, 1)
       }
       if (!ok) {
         // After a timeout: the copies issued have landed before the CTA ends.
-        if (kE4M3 && !(C::kNativeK && kv0 == 0)) {
+        if (kE4M3) {
           for (uint32_t i = issued > RS ? issued - RS : 0; i < issued; ++i)
-            mbar_wait(raw_full + (C::kNativeK ? 0 : kv0) * RS + i % RS, (i / RS) & 1, kChunkWaitNs);
+            mbar_wait(raw_full + kv0 * RS + i % RS, (i / RS) & 1, kChunkWaitNs);
         } else {
           const uint32_t ring = kv0 ? VS : KS;
           for (uint32_t i = issued > ring ? issued - ring : 0; i < issued; ++i)
             mbar_wait((kv0 ? v_full : k_full) + i % ring, (i / ring) & 1, kChunkWaitNs);
         }
+      }
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issue
