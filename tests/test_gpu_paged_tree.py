@@ -283,10 +283,11 @@ def test_attention_length_above_the_table_is_cut_and_recorded():
     paged_ref.check_attention(p, out, ref)
 
 
+@pytest.mark.parametrize("fmt,d", [("bf16", 64), ("e4m3", 64), ("e4m3", 128)])
 @pytest.mark.parametrize("q_len", [4, 50])
-def test_attention_a_query_row_with_nan(q_len):
+def test_attention_a_query_row_with_nan(q_len, fmt, d):
     """NaN in a row's q: NaN out, unless it sees no key; the other rows are as they were."""
-    p = Problem([q_len], [300 + q_len], 4, 2, 64, 16, seed=46)
+    p = Problem([q_len], [300 + q_len], 4, 2, d, 16, fmt, seed=46)
     seen, depth, tree = _tree([q_len], tree_ref.parents_of([q_len], 9), p.rows)
     cache, batch = _handles(p)
     want = sage.sage_paged_attn_tree(p.q, cache, batch, tree)
@@ -310,6 +311,28 @@ def test_attention_strided_views_and_expanded_query():
     sage.sage_paged_attn_tree(q, cache, batch, tree, sm_scale=0.3, out=out)
     paged_ref.check_attention(p, out, tree_ref.attention(p, q, seen, sm_scale=0.3), sm_scale=0.3)
     assert bool((wide[:, :6 * 64] == -7.0).all())
+
+
+@pytest.mark.parametrize("q_len", [4, 70])
+@pytest.mark.parametrize("fmt,d", [("bf16", 128), ("e4m3", 128), ("e4m3", 64)])
+def test_attention_of_rows_of_very_different_size(q_len, fmt, d):
+    """Query rows scaled by 2^-90 .. 2^10, and the scores' scale with them; a head of zeros; rows with one channel far above
+    the others."""
+    p = Problem([q_len], [400], 4, 2, d, 16, fmt, seed=34)
+    seen, depth, tree = _tree([q_len], tree_ref.parents_of([q_len], 12), p.rows)
+    cache, batch = _handles(p)
+    lse = torch.empty((p.rows, 4), dtype=torch.float32, device="cuda")
+    for shift in (-90, 10):
+        q = (p.q.float() * 2.0 ** shift).to(torch.bfloat16)
+        sm = 2.0 ** -shift / math.sqrt(d)
+        out = sage.sage_paged_attn_tree(q, cache, batch, tree, sm_scale=sm)
+        tree_ref.check_attention(p, out, tree_ref.attention(p, q, seen, sm_scale=sm), q, sm_scale=sm)
+    q = p.q.contiguous().clone()
+    q[:, 1] = 0                       # uniform weights
+    q[:, 2, 7] = 300.0
+    q[:, 3, :-1] *= 2.0 ** -9
+    out = sage.sage_paged_attn_tree(q, cache, batch, tree, lse=lse)
+    _check(p, out, lse, tree_ref.attention(p, q, seen), q)
 
 
 @pytest.mark.parametrize("q_len", [6, 48])
