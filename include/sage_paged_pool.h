@@ -81,7 +81,7 @@ sage_status sage_paged_fork(const sage_paged_pool* pool, const int32_t* src_rows
  *   src, dst   device int32 [n_copies].  An entry with a -1 on either side is left out; src = dst changes nothing.  A page
  *              may be the source of several copies; none may be the target of two, or target and source of two.
  *   n_tokens   device int32 [n_copies], or NULL: whole pages.  Taken into [0, page_size]; others are recorded (17).
- * n_copies at most 2^22.  One launch for each 65535 copies. */
+ * n_copies at most 2^22.  One launch for each 65535 copies.  (Here and below K and V may be the same pages: they move once.) */
 sage_status sage_paged_copy(const sage_paged_kv* cache, const int32_t* src, const int32_t* dst, const int32_t* n_tokens,
                             int64_t n_copies, void* status_block, void* stream);
 

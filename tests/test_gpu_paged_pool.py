@@ -377,6 +377,40 @@ def test_compact_numbers_out_of_range():
     assert sage.sage_check_device_status(ws) == (1, 23)
 
 
+@pytest.mark.parametrize("most", [5, 700])
+def test_values_that_are_the_keys_move_once(most):
+    """One tensor for K and V."""
+    r = random.Random(most)
+    table, n_pages = _table(r, [900], 16)
+    cache, kv = _cache(n_pages, 16, 2, 128, "bf16", "nhd")
+    both = sage.PagedKV(cache.k_pages, cache.k_pages)
+    for _ in range(5):
+        keep = sorted(r.sample(range(3, 900), most))
+        want = _moved(kv[:1], table, 16, [3], [keep])[0]
+        _compact(both, table, [900], [3], [keep])
+        assert torch.equal(kv[0], want)
+    want[table[0][5]] = want[table[0][0]]
+    sage.sage_paged_copy(both, _i32([table[0][0]]), _i32([table[0][5]]))
+    assert torch.equal(kv[0], want)
+
+
+def test_accounting_of_very_many_rows():
+    """More rows than a grid has in one direction."""
+    rows = 65536
+    gpu = sage.PagedPool(torch.zeros(rows + 7, dtype=torch.int32, device="cuda"),
+                         torch.full((rows, 2), -1, dtype=torch.int32, device="cuda"), 8)
+    hi = torch.full((rows,), 8, dtype=torch.int32, device="cuda")
+    assert bool(sage.sage_paged_reserve(gpu, hi).all())
+    assert torch.equal(gpu.page_table[:, 0], torch.arange(rows, dtype=torch.int32, device="cuda"))
+    hi[::2] = 0
+    sage.sage_paged_release(gpu, hi)
+    assert int(gpu.refs.sum()) == rows // 2 and bool((gpu.page_table[::2] == -1).all()) and bool((gpu.page_table[1::2, 0] >= 0).all())
+    src = torch.arange(1, 2 * 20000, 2, dtype=torch.int32, device="cuda")
+    lists = sage.sage_paged_fork(gpu, src, src - 1, torch.full_like(src, 8))
+    assert bool(lists[3].all()) and torch.equal(gpu.page_table[0:40000:2, 0], gpu.page_table[1:40000:2, 0])
+    assert sage.sage_check_device_status(gpu.status) == (0, 0)
+
+
 def test_compact_nothing():
     cache, kv = _cache(5, 8, 2, 64, "bf16", "nhd")
     before = [x.clone() for x in kv]

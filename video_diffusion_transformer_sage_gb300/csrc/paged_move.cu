@@ -110,7 +110,8 @@ struct CompactArgs {
   int row_shift, heads;
   int slab, slabs;             // heads of an item, items side by side
   int tokens, runs;            // tokens of an item, items of a list of max_keep
-  uint32_t units, items;       // n_seqs * 2 * slabs; times runs
+  int sides;                   // 2, or 1 where K and V are the same pages
+  uint32_t units, items;       // n_seqs * sides * slabs; times runs
   int32_t* status;
   int32_t* counters;           // next item, CTAs done, ring of 16-bit numbers: 1 + the round last read in each place
 };
@@ -139,8 +140,8 @@ __device__ __forceinline__ Item find_item(const CompactArgs& a, uint32_t item) {
   const uint32_t run = item / a.units, unit = item - run * a.units, half = unit / a.slabs;
   const int slab = unit - half * a.slabs;
   Item it;
-  it.b = half >> 1;
-  it.side = &a.side[half & 1];
+  it.b = a.sides == 2 ? half >> 1 : half;
+  it.side = &a.side[a.sides == 2 ? half & 1 : 0];
   it.head0 = static_cast<int64_t>(slab) * a.slab * it.side->head;
   it.per = static_cast<uint32_t>(min(a.slab, a.heads - slab * a.slab)) << a.row_shift;
   it.i0 = run * a.tokens;
@@ -452,6 +453,10 @@ void page_sides(const sage_paged_kv* c, PageSide side[2]) {
   side[0] = {static_cast<uint8_t*>(c->k_pages), c->k_stride_page * e * p, c->k_stride_token * e * t, c->k_stride_head * e * h};
   side[1] = {static_cast<uint8_t*>(c->v_pages), c->v_stride_page * e * p, c->v_stride_token * e * t, c->v_stride_head * e * h};
 }
+// Values that are the keys themselves move once.
+int page_side_count(const sage_paged_kv* c, const PageSide side[2]) {
+  return c->k_pages == c->v_pages && side[0].page == side[1].page && side[0].token == side[1].token && side[0].head == side[1].head ? 1 : 2;
+}
 int pieces_shift(const sage_paged_kv* c) {   // 16-byte pieces of a row: 4, 8 or 16
   const int64_t row = c->head_dim * (c->format == 1 ? 1 : 2);
   return row == 64 ? 2 : row == 128 ? 3 : 4;
@@ -489,7 +494,8 @@ sage_status sage_paged_copy(const sage_paged_kv* cache, const int32_t* src, cons
     a.src = src + at;
     a.dst = dst + at;
     a.tokens = n_tokens ? n_tokens + at : nullptr;
-    const dim3 grid(static_cast<unsigned>((pieces + kCopyPieces - 1) / kCopyPieces), static_cast<unsigned>(n), 2);
+    const dim3 grid(static_cast<unsigned>((pieces + kCopyPieces - 1) / kCopyPieces), static_cast<unsigned>(n),
+                    static_cast<unsigned>(page_side_count(cache, a.side)));
     paged_copy_kernel<<<grid, kMoveThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
     if ((st = cuda_status(cudaGetLastError())) != SAGE_OK) return st;
   }
@@ -534,7 +540,8 @@ sage_status sage_paged_compact(const sage_paged_kv* cache, const sage_paged_batc
   a.slab = static_cast<int>(slab);
   a.tokens = static_cast<int>(std::min<int64_t>({kItemTokens, pieces / (slab * row), max_keep}));
   a.runs = static_cast<int>((max_keep + a.tokens - 1) / a.tokens);
-  const int64_t items = batch->n_seqs * 2 * a.slabs * a.runs;
+  a.sides = page_side_count(cache, a.side);
+  const int64_t items = batch->n_seqs * a.sides * a.slabs * a.runs;
   if (items > (whole ? INT32_MAX : int64_t(1) << 25)) return SAGE_ERR_UNSUPPORTED;   // (rounds of the ring in 16 bits)
   a.units = static_cast<uint32_t>(items / a.runs);
   a.items = static_cast<uint32_t>(items);

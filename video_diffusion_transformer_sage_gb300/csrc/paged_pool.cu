@@ -53,26 +53,27 @@ __device__ __forceinline__ int warp_scan(int x) {   // inclusive
 
 // ------------------------------------------------------------------------------------------- release
 __global__ void __launch_bounds__(kReleaseThreads) paged_release_kernel(const __grid_constant__ PoolArgs a) {
-  const int row = blockIdx.x;
-  const int lo = a.lo ? __ldg(a.lo + row) : 0, hi = __ldg(a.hi + row);
-  int32_t* entries = a.table + row * a.table_stride;
-  int page[kReleasePer];
+  for (int row = blockIdx.y; row < a.n_rows; row += gridDim.y) {
+    const int lo = a.lo ? __ldg(a.lo + row) : 0, hi = __ldg(a.hi + row);
+    int32_t* entries = a.table + row * a.table_stride;
+    int page[kReleasePer];
 #pragma unroll
-  for (int k = 0; k < kReleasePer; ++k) {
-    const int i = (blockIdx.y * kReleasePer + k) * kReleaseThreads + threadIdx.x;
-    // Positions [i, i + 1) << page_shift, at most 2^30.
-    const bool out = i < a.max_pages && (((i + 1) << a.page_shift) <= lo || (i << a.page_shift) >= hi || hi <= lo);
-    page[k] = out ? entries[i] : -1;
-  }
+    for (int k = 0; k < kReleasePer; ++k) {
+      const int i = (blockIdx.x * kReleasePer + k) * kReleaseThreads + threadIdx.x;
+      // Positions [i, i + 1) << page_shift, at most 2^30.
+      const bool out = i < a.max_pages && (((i + 1) << a.page_shift) <= lo || (i << a.page_shift) >= hi || hi <= lo);
+      page[k] = out ? entries[i] : -1;
+    }
 #pragma unroll
-  for (int k = 0; k < kReleasePer; ++k) {
-    if (page[k] < 0) continue;
-    entries[(blockIdx.y * kReleasePer + k) * kReleaseThreads + threadIdx.x] = -1;
-    if (page[k] >= a.n_pages) {
-      record_bad_index(a.status, kWherePage);
-    } else if (atomicSub(a.refs + page[k], 1) <= 0) {
-      atomicAdd(a.refs + page[k], 1);
-      record_bad_index(a.status, kWhereCount);
+    for (int k = 0; k < kReleasePer; ++k) {
+      if (page[k] < 0) continue;
+      entries[(blockIdx.x * kReleasePer + k) * kReleaseThreads + threadIdx.x] = -1;
+      if (page[k] >= a.n_pages) {
+        record_bad_index(a.status, kWherePage);
+      } else if (atomicSub(a.refs + page[k], 1) <= 0) {
+        atomicAdd(a.refs + page[k], 1);
+        record_bad_index(a.status, kWhereCount);
+      }
     }
   }
 }
@@ -432,10 +433,9 @@ sage_status sage_paged_release(const sage_paged_pool* pool, const int32_t* lo, c
   a.lo = lo;
   a.hi = hi;
   constexpr int kPer = kReleaseThreads * kReleasePer;
-  const int64_t parts = (pool->max_pages + kPer - 1) / kPer;
-  if (parts > 65535) return SAGE_ERR_UNSUPPORTED;
-  paged_release_kernel<<<dim3(static_cast<unsigned>(a.n_rows), static_cast<unsigned>(parts)), kReleaseThreads, 0,
-                         static_cast<cudaStream_t>(stream)>>>(a);
+  const unsigned parts = static_cast<unsigned>((pool->max_pages + kPer - 1) / kPer);
+  const unsigned rows = static_cast<unsigned>(a.n_rows < 65535 ? a.n_rows : 65535);
+  paged_release_kernel<<<dim3(parts, rows), kReleaseThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
   return cuda_status(cudaGetLastError());
 }
 
