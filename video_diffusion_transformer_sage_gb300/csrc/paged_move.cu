@@ -545,18 +545,18 @@ sage_status sage_paged_compact(const sage_paged_kv* cache, const sage_paged_batc
   if (items > (whole ? INT32_MAX : int64_t(1) << 25)) return SAGE_ERR_UNSUPPORTED;   // (rounds of the ring in 16 bits)
   a.units = static_cast<uint32_t>(items / a.runs);
   a.items = static_cast<uint32_t>(items);
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   // Bulk copies where a token's rows of K and of V lie together.
   const bool bulk = slab == 1 || (a.side[0].head == row * 16 && a.side[1].head == row * 16);
   auto* kernel = whole ? paged_compact_kernel : bulk ? paged_compact_long_kernel<true> : paged_compact_long_kernel<false>;
-  const int most = whole ? kItemPieces * 16 : kLongBuffers * kLongPieces * 16;
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-  if (e != cudaSuccess) return cuda_status(e);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaSuccess;
+  if (!whole && (e = cudaGetDevice(&dev)) == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int64_t ctas = whole ? items : std::min<int64_t>({items, sms, kPagedMoveRing / kMovePlaces});
   const int threads = whole ? kMoveThreads : bulk ? LongCfg<true>::kThreads : LongCfg<false>::kThreads;
-  const int smem = whole ? static_cast<int>(a.tokens * slab * row * 16) : most;
+  const int smem = whole ? static_cast<int>(a.tokens * slab * row * 16) : kLongBuffers * kLongPieces * 16;
+  if (e == cudaSuccess && smem > 40 * 1024)   // (less needs no leave, which takes a microsecond)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, whole ? kItemPieces * 16 : smem);
+  if (e != cudaSuccess) return cuda_status(e);
   kernel<<<static_cast<unsigned>(ctas), threads, smem, static_cast<cudaStream_t>(stream)>>>(a);
   return cuda_status(cudaGetLastError());
 }
