@@ -7,7 +7,7 @@
  *   a prompt or drafts       sage_paged_reserve: pages for the positions to come, before sage_paged_append
  *   beams, parallel samples  sage_paged_fork: the child shares the full pages of its parent and gets a page of its own for
  *                            the begun one, which sage_paged_copy fills
- *   judged drafts            sage_paged_compact moves the accepted tokens together, sage_paged_release gives back the pages
+ *   verified drafts          sage_paged_compact moves the accepted tokens together, sage_paged_release gives back the pages
  *                            behind them; it also gives back those before a sliding window, or all of a finished sequence
  *
  * The rules of sage.h and sage_paged.h hold: device pointers, caller-owned buffers, nothing allocated, arguments checked

@@ -7,7 +7,7 @@
  *   sage_paged_tree(parents, ...)                once for all layers: who sees whom, and where each token stands
  *   sage_paged_append(..., positions, ...)       K and V stored one after the other, rotated by their places in the text
  *   sage_paged_attn_tree(q, ..., tree, ...)      each token sees the cached text and its own ancestors
- * and when the guesses have been judged, sage_paged_compact (sage_paged_pool.h) moves the accepted path's tokens
+ * and when the guesses have been verified, sage_paged_compact (sage_paged_pool.h) moves the accepted path's tokens
  * together.  The rules of sage.h and sage_paged.h hold: device pointers, caller-owned buffers, nothing allocated, arguments
  * checked before anything is launched, indices in device memory checked by the kernels and recorded in the status block.
  */

@@ -1,4 +1,4 @@
-"""The cache's operators together, as a serving loop runs them: drafted trees judged and kept, beams forked and grown, each
+"""The cache's operators together, as a serving loop runs them: drafted trees verified and kept, beams forked and grown, each
 step against lists of the tokens that every sequence should hold."""
 import random
 
