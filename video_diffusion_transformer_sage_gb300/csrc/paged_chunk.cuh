@@ -1430,11 +1430,14 @@ cudaError_t launch_t(const PagedAttnArgs& a, const sage_paged_kv& kv, cudaStream
   const double count = static_cast<double>(likely - whole), tile_us = 0.51 + 0.94 * D / 128;
   const int64_t tiles = std::max(1, (a.b.cap + kBN - 1) / kBN);
   const int64_t most = std::min<int64_t>({kPagedSlots / std::max<int64_t>(rest, 1), sms, std::max<int64_t>(1, tiles / 4)});
+  // A tree's few rows may wait for HBM instead, however their keys are split (6.5 TB/s; 12 trees of 48 rows over 9000 keys of 8
+  // heads of 128 channels: 81 us whole, 92 in three parts; of 64 51 and 59).
+  const double hbm = kTree ? count / static_cast<double>(blocks) * static_cast<double>(tiles * kBN) * (2 * D * e) / 6.5e6 : 0.0;
   auto last_wave = [&](int64_t k) {
     const double items = count * static_cast<double>(k) * (odd && !one ? 1.0 - 0.5 / static_cast<double>(blocks) : 1.0);
     const double item = tile_us * (one ? 0.5 : 1.0) * static_cast<double>((tiles + k - 1) / k) + 3.0;
     const double part_bytes = std::min<double>(static_cast<double>(mean), 256.0) * D * 4;
-    return std::ceil(items / sms) * item + (k > 1 ? (whole > 0 ? 10.0 : 6.0) + items * part_bytes * 2 / 3.4e6 : 0.0);
+    return std::max(std::ceil(items / sms) * item, hbm) + (k > 1 ? (whole > 0 ? 10.0 : 6.0) + items * part_bytes * 2 / 3.4e6 : 0.0);
   };
   int64_t splits = 1;
   for (int64_t k = 2; k <= most; ++k)
