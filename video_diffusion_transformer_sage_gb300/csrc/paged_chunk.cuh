@@ -1439,8 +1439,11 @@ cudaError_t launch_t(const PagedAttnArgs& a, const sage_paged_kv& kv, cudaStream
     const double part_bytes = std::min<double>(static_cast<double>(mean), 256.0) * D * 4;
     return std::max(std::ceil(items / sms) * item, hbm) + (k > 1 ? (whole > 0 ? 10.0 : 6.0) + items * part_bytes * 2 / 3.4e6 : 0.0);
   };
+  // Nor are the keys of trees split that are left over behind whole units: contexts are ragged, and the shortest are left
+  // (lengths between a third and all of 4000 keys, 8 heads of 128 channels: 24 trees of 48 rows 54 us, split 68, 40 of 200
+  // rows 112 and 156; of one length 119 and 112, 176 and 199).
   int64_t splits = 1;
-  for (int64_t k = 2; k <= most; ++k)
+  for (int64_t k = 2; k <= most && !(kTree && whole > 0); ++k)
     if (last_wave(k) < last_wave(splits)) splits = k;
   p.splits = static_cast<int>(splits);
   p.halve = !one;
