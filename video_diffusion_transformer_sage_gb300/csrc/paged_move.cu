@@ -21,10 +21,11 @@
 // Which items have been read stands in a ring of 8 numbers per CTA: in place `item mod its length` the round of the last item read,
 // each put there after the one a round before it.  Items ascend within a CTA, reading waits for nothing but that and a buffer, and
 // the lowest item not yet read finds its place ready: so every wait ends.
-// The long kernel's steps on compact_frames (24192 tokens of 56 heads, 1.39 GB; floor 196 us): an item read, waited for and written
+// The long kernel's steps on compact_frames (23184 tokens of 56 heads, 1.33 GB; floor 196 us): an item read, waited for and written
 // in turn, two CTAs per SM 554 us; reading and writing by warps of their own 420-520, 200 of it waiting for all items drawn
 // before; the search and bulk copies 337; eight items found ahead, the lists side by side, no fences, a place in the ring for every
-// item in work 220 (6.3 TB/s; 207 without looking at the ring).  Rows of 256 bytes, by 16 bytes a thread: 353 for as much.
+// item in work 220 (6.0 TB/s; 207 without looking at the ring).  Rows of 256 bytes, by 16 bytes a thread: 24000 tokens
+// 354, where heads lie together 270.
 #include <algorithm>
 
 #include "paged_batch.cuh"
