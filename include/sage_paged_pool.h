@@ -96,8 +96,8 @@ sage_status sage_paged_copy(const sage_paged_kv* cache, const int32_t* src, cons
  *   n_keep   device int32 [n_seqs].
  * Of the batch, kv_len (the tokens before the call) and page_table are read.  A token whose page, old or new, is out of range
  * is not moved (16).  Pages that are written belong to one sequence (a shared page would change for all).
- *   ws       256-byte aligned, >= SAGE_PAGED_WS_HEADER bytes, zeroed once: a workspace of sage_paged_attn, or its header
- *            alone.  Calls that may overlap on the GPU need workspaces of their own.
+ *   ws       256-byte aligned, >= SAGE_PAGED_WS_HEADER bytes, zeroed once (and again after a recorded timeout): a workspace of
+ *            sage_paged_attn, or its header alone.  Calls that may overlap on the GPU need workspaces of their own.
  * One launch.  Lists longer than an item of 64 KB (256 tokens, or as many as one head's rows allow) are worked through in
  * pieces of 48 KB; more than 2^25 of them are refused (SAGE_ERR_UNSUPPORTED). */
 sage_status sage_paged_compact(const sage_paged_kv* cache, const sage_paged_batch* batch, const int32_t* first,
