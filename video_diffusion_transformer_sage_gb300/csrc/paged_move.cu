@@ -38,7 +38,7 @@ namespace {
 constexpr int kMoveThreads = 256;
 constexpr int kCopyPer = 8;                                    // 16-byte pieces of a thread
 constexpr int kCopyPieces = kMoveThreads * kCopyPer;           // 32 KB
-constexpr int kItemPieces = 4096, kLongPieces = 3072;          // of an item: 64 KB, of a long list 48 KB
+constexpr int kItemPieces = 64 * 64, kLongPieces = 48 * 64;    // 16 bytes each, of an item: 64 KB, of a long list 48 KB
 constexpr int kLongItems = 8, kLongBuffers = 4;                // in work in a CTA
 constexpr int kMovePlaces = 8;                                 // of the ring, for each CTA: no item waits for one that is not drawn
 static_assert(kMovePlaces >= kLongItems, "items wait for their places");
