@@ -57,10 +57,10 @@ sage_status sage_paged_tree(const sage_paged_batch* batch, int64_t n_tokens, con
  * becomes 0, its lse -infinity.  A new token that no row sees may hold anything, as slots without a token; the rest of
  * [0, kv_len) (with a window: of [P + 1 - window, kv_len)) must be finite.
  * All else as for sage_paged_attn: views, cache, batch, sm_scale, out, lse, ws, errors, and the choice of a kernel by the
- * batch's mean rows.  Whoever comes last, parts are joined in the order of their keys.  So is the precision, but that the
- * kernel for many rows over an E4M3 cache holds q as the sum of two E4M3 values times a power of two per row: exact but
- * for values 2^-10 below the row's largest, which keep an absolute error of 2^-17 of it (q . k is then at most
- * 2^-17 max |q_c| sum |k_c| off); an infinite q counts as NaN there. */
+ * batch's mean rows.  Whoever comes last, parts are joined in the order of their keys.  So is the precision: where
+ * sage_paged_attn holds q as fp16, the kernel for many rows over an E4M3 cache holds it as the sum of three E5M2 values times a
+ * power of two per row, exact but for values 2^-23 below the row's largest, which keep an absolute error of 2^-31 of it
+ * (fp16: 2^-14 and 2^-25).  An infinite q counts as NaN there. */
 sage_status sage_paged_attn_tree(const sage_view* q, const sage_paged_kv* cache, const sage_paged_batch* batch,
                                  const sage_paged_tree_mask* tree, float sm_scale, int64_t window, void* out,
                                  int64_t out_stride_token, int64_t out_stride_head, float* lse, void* ws, size_t ws_bytes,

@@ -52,6 +52,7 @@ namespace {
 constexpr int kBM = 128, kBN = 128;
 constexpr uint64_t kChunkWaitNs = 2000000000ull;
 constexpr int kItemWaits = 64;   // such waits for all of an item's key tiles
+constexpr int kSplitUp = 14;    // log2 of a row's largest value where Q is split into E5M2 values
 constexpr float kRise = 8.0f;   // log2 of how far a maximum may fall behind before O is rescaled
 
 template <int D, bool kE4M3, bool kTree>
@@ -59,18 +60,19 @@ struct ChunkCfg {
   static constexpr int kThreads = kE4M3 ? 512 : 384;
   static constexpr int kPanels = D / 64;
   static constexpr int kPanelBytes = 128 * 128;               // 128 rows of 64 channels
-  static constexpr int kQTileBytes = kBM * D * 2;
   static constexpr int kTileBytes = kBN * D * 2;              // a K or V tile in 16 bits
   static constexpr int kStageBytes = 2 * kTileBytes;
   // A tree has few rows for the keys that it sees, so the loads have to be far ahead: K and V apart, each in a ring of
   // its own.  (One row tile at D = 64 with the shared ring of four: 97 us for 12032 keys of 152 heads in bf16, 112 in E4M3, of
   // which 73 and 87 remain when K and V come from L2: a load's latency in every step.)  With E4M3 K is not widened either: Q
-  // is split into two E4M3 values, and Q K^T takes the codes as they lie (kNativeK; widening both took ~2100 cycles a tile,
+  // is split into three E5M2 values, and Q K^T takes the codes as they lie (kNativeK; widening both took ~2100 cycles a tile,
   // 148 us of verify_e4m3).
   static constexpr bool kNativeK = kTree && kE4M3;
-  static constexpr int kKStages = !kTree ? (D == 128 ? 2 : 4) : kE4M3 ? (D == 128 ? 3 : 6) : (D == 128 ? 2 : 5);
+  // The three of a row: a panel each, or (D = 64) two halves of a panel's rows and a tile of 64-byte rows.
+  static constexpr int kQTileBytes = !kNativeK ? kBM * D * 2 : D == 128 ? 3 * kPanelBytes : kPanelBytes + kBM * 64;
+  static constexpr int kKStages = !kTree ? (D == 128 ? 2 : 4) : kE4M3 ? (D == 128 ? 2 : 6) : (D == 128 ? 2 : 5);
   static constexpr int kVStages = !kTree ? (D == 128 ? 2 : 4) : kE4M3 ? (D == 128 ? 2 : 3) : (D == 128 ? 2 : 5);
-  static constexpr int kRawStages = kNativeK ? (D == 128 ? 3 : 7) : 1;
+  static constexpr int kRawStages = kNativeK ? (D == 128 ? 2 : 6) : 1;
   static constexpr int kRawSides = kNativeK ? 1 : 2;          // staging tiles of V, or of K and V
   static constexpr int kBits = kNativeK ? 16 : 8;             // key tiles whose loaded boxes are remembered
   // K and V of a tile have barriers of their own where the ring is short (D = 128): a K stage is free again once
@@ -241,6 +243,8 @@ __device__ __forceinline__ float max64(const uint32_t* s) {
 
 // Instruction descriptor bits: bf16 operands (fp16 is 0), B MN-major.
 constexpr uint32_t kIdescBf16 = (1u << 7) | (1u << 10), kIdescBmn = 1u << 16;
+// Of the 8-bit kind: A holds E5M2 (B E4M3, which is 0).
+constexpr uint32_t kIdescE5m2 = 1u << 7;
 // Low descriptor word of a V tile as MN-major B: rows of 64 channels (128 bytes), 8-key groups 1024 bytes
 // apart (the stride offset of kSdescHi), the next 64 channels a panel further (leading offset).
 __device__ __forceinline__ uint32_t vdesc_lo(uint32_t saddr) {
@@ -274,7 +278,7 @@ __device__ __forceinline__ void warp_tc_commit(uint64_t* bar) {
       : "memory");
 }
 
-// E4M3 by E4M3.
+// 8-bit floats.
 __device__ __forceinline__ void warp_mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                                uint32_t accumulate) {
   asm volatile(
@@ -293,14 +297,16 @@ __device__ __forceinline__ uint64_t raw_desc_of_lo(uint32_t lo) {
 template <int D, bool kE4M3, bool kTree>
 __device__ __forceinline__ void issue_qk(uint32_t s_tmem, uint32_t ql, uint32_t kl) {
   if constexpr (ChunkCfg<D, kE4M3, kTree>::kNativeK) {
-    // Both values of Q, 32 channels a step: of D = 128 in a panel each, of D = 64 in a half of the row each.
-    constexpr uint32_t idesc8 = idesc_f32acc(kBM, kBN);
+    // The three values of Q (E5M2) by K (E4M3), 32 channels a step.
+    constexpr uint32_t idesc8 = idesc_f32acc(kBM, kBN) | kIdescE5m2;
+    constexpr int kPanel = ChunkCfg<D, kE4M3, kTree>::kPanelBytes;
 #pragma unroll
-    for (int part = 0; part < 2; ++part)
+    for (int part = 0; part < 3; ++part)
 #pragma unroll
       for (int kk = 0; kk < D / 32; ++kk) {
-        const uint32_t qo = (D == 128 ? part * ChunkCfg<D, kE4M3, kTree>::kPanelBytes + kk * 32 : part * 64 + kk * 32) >> 4;
-        warp_mma_f8_ss(s_tmem, sdesc_of_lo(ql + qo), raw_desc_of_lo<D>(kl + (kk * 32 >> 4)), idesc8, part + kk > 0 ? 1u : 0u);
+        const uint32_t lo = ql + ((D == 128 || part == 2 ? (D == 128 ? part : 1) * kPanel + kk * 32 : part * 64 + kk * 32) >> 4);
+        warp_mma_f8_ss(s_tmem, D == 64 && part == 2 ? raw_desc_of_lo<D>(lo) : sdesc_of_lo(lo), raw_desc_of_lo<D>(kl + (kk * 32 >> 4)),
+                       idesc8, part + kk > 0 ? 1u : 0u);
       }
     return;
   }
@@ -328,6 +334,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   else
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
   return w;
+}
+
+// Two E5M2 values (low byte first): E5M2 is the upper byte of fp16.
+__device__ __forceinline__ float2 float2_of_e5m2x2(uint16_t c) {
+  const __half2_raw h{static_cast<uint16_t>(c << 8), static_cast<uint16_t>(c & 0xFF00u)};
+  return __half22float2(__half2(h));
 }
 
 // Bit k of word w: key 32 w + k of the tile lies in [lo, hi) and its box was loaded.
@@ -1081,28 +1093,38 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3, kTree>::kThreads, 1)
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
           int e = static_cast<int>((__float_as_uint(mx) >> 23) & 255) - 127;
-          e = mx == 0.0f ? 0 : min(max(e, -126), 126);
+          e = mx == 0.0f ? 0 : min(max(e, C::kNativeK ? kSplitUp - 126 : -126), 126);
+          if (C::kNativeK) e -= kSplitUp;
           const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
           if constexpr (C::kNativeK) {
-            // The sum of two E4M3 values times 2^(e - 7), the row's largest in [128, 256): exact but for values 2^-10
-            // below it, which keep an absolute error of 2^-17 of the row's largest.  What is no number stays none.
-            uint16_t part[2][4];
+            // The sum of three E5M2 values times 2^e, the row's largest in [2^14, 2^15).  A value's 8 bits rounded to three leave at
+            // most 16 units of the last; those rounded to three bits leave one unit at most.  So it is exact where the
+            // unit is no less than E5M2's smallest step, 2^-16: but for values 2^-23 below the row's largest, which keep an absolute
+            // error of 2^-31 of it.  What is no number stays none.
+            // (Two E4M3 values keep 2^-17 of the row's largest, an E4M3 and an E5M2 one 2^-21, where fp16 keeps 2^-25.  Two
+            // took 98 us where these take 104, 19 sequences of 12032 keys, 8 heads of 128 channels, 40 rows; at 64 channels 77
+            // and 78: the third panel costs D = 128 a stage of K and one of V's codes.  256 rows: 168 and 182, 132 and 132.)
+            uint16_t part[3][4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              float y[2] = {__uint_as_float(w[x] << 16) * down * 128.0f, __uint_as_float(w[x] & 0xFFFF0000u) * down * 128.0f};
+              float y[2] = {__uint_as_float(w[x] << 16) * down, __uint_as_float(w[x] & 0xFFFF0000u) * down};
 #pragma unroll
               for (int i = 0; i < 2; ++i) y[i] = fabsf(y[i]) < INFINITY ? y[i] : __uint_as_float(0x7FFFFFFFu);
-              part[0][x] = e4m3x2(y[0], y[1]);
-              uint32_t back;
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(part[0][x]));
-              const float2 first = __half22float2(*reinterpret_cast<const __half2*>(&back));
-              part[1][x] = e4m3x2(y[0] - first.x, y[1] - first.y);
+#pragma unroll
+              for (int i = 0; i < 3; ++i) {
+                part[i][x] = e5m2x2(y[0], y[1]);
+                const float2 taken = float2_of_e5m2x2(part[i][x]);
+                y[0] -= taken.x;
+                y[1] -= taken.y;
+              }
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int ch = (D == 64 ? i * 4 : 0) + (c8 >> 1);   // 16-byte chunk of the row
-              *reinterpret_cast<uint2*>(tile + (D == 128 ? i * C::kPanelBytes : 0) + rr * 128 + ((ch ^ (rr & 7)) << 4) + (c8 & 1) * 8) =
-                  make_uint2(pack_h2(part[i][0], part[i][1]), pack_h2(part[i][2], part[i][3]));
+            for (int i = 0; i < 3; ++i) {
+              const uint2 v8 = make_uint2(pack_h2(part[i][0], part[i][1]), pack_h2(part[i][2], part[i][3]));
+              const int ch = (D == 64 && i < 2 ? i * 4 : 0) + (c8 >> 1);   // 16-byte chunk of the row
+              uint8_t* at = D == 64 && i == 2 ? tile + C::kPanelBytes + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4)
+                                              : tile + (D == 128 ? i * C::kPanelBytes : 0) + rr * 128 + ((ch ^ (rr & 7)) << 4);
+              *reinterpret_cast<uint2*>(at + (c8 & 1) * 8) = v8;
             }
           } else {
             uint32_t f[4];
@@ -1141,8 +1163,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, kE4M3, kTree>::kThreads, 1)
         // (In a unit of one row tile slot 0's warps wrote the exponents.)
         if (one && t == 1) ok = wait(q_full, k & 1, kWherePagedFull);
         else __syncwarp();
-        c *= __ldg(a.k_scale + u.h) * __uint_as_float(static_cast<uint32_t>(q_exp[first + r]) << 23) *
-             (C::kNativeK ? 0.0078125f : 1.0f);
+        const float ks = __ldg(a.k_scale + u.h), qs = __uint_as_float(static_cast<uint32_t>(q_exp[first + r]) << 23);
+        // (The split's factor is 2^-14 of the other: with the scale first, which is large where q is small, it does not underflow.)
+        c = C::kNativeK ? c * qs * ks : c * (ks * qs);
       }
       float m = -INFINITY, l = 0.0f;
       const int key_t0 = u.t0 * kBN;
