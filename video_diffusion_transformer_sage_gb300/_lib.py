@@ -402,8 +402,24 @@ def _driver():
 
 @functools.lru_cache(maxsize=None)
 def _side_stream(index: int) -> torch.cuda.Stream:
-    """The stream of a device that status blocks are zeroed on, apart from whatever else goes on."""
-    return torch.cuda.Stream(index)
+    """The stream of a device that status blocks are zeroed on, apart from whatever else goes on.  Not one of torch's: those are
+    given out again after 32, and a capture on the same stream would take the zeroing in and fail at the wait for it."""
+    driver, device = _driver(), ctypes.c_int()
+    context, stream = ctypes.c_void_p(), ctypes.c_void_p()
+
+    def call(name, *args):
+        code = getattr(driver, name)(*args)
+        if code != 0:
+            raise RuntimeError(f"{name} failed: {code}")
+
+    call("cuDeviceGet", ctypes.byref(device), index)
+    call("cuDevicePrimaryCtxRetain", ctypes.byref(context), device)   # torch's context, for the life of the process
+    call("cuCtxPushCurrent_v2", context)
+    try:
+        call("cuStreamCreate", ctypes.byref(stream), 1)               # 1: does not wait for the default stream
+    finally:
+        call("cuCtxPopCurrent_v2", ctypes.byref(context))
+    return torch.cuda.ExternalStream(stream.value, device=torch.device("cuda", index))
 
 
 @contextlib.contextmanager
