@@ -11,6 +11,7 @@
 //   3  each warp gives its rows the pages from their place in the list on.
 #include "paged_batch.cuh"
 #include "paged_check.h"
+#include "paged_pool_walk.h"
 #include "sage_paged_pool.h"
 
 namespace sage {
@@ -79,18 +80,14 @@ __global__ void __launch_bounds__(kReleaseThreads) paged_release_kernel(const __
 }
 
 // ------------------------------------------------------------------------------------------- reserve, fork
-// This warp's part of the counts: [from, to) in steps of 128 pages.
-__device__ __forceinline__ void part_of_counts(const PoolArgs& a, int& from, int& to) {
-  const int warp = blockIdx.x * kPoolWarps + (threadIdx.x >> 5);
-  const int64_t tiles = (static_cast<int64_t>(a.n_pages) + 127) / 128;
-  constexpr int kAll = kPoolCtas * kPoolWarps;
-  from = static_cast<int>(min(tiles * warp / kAll * 128, static_cast<int64_t>(a.n_pages)));
-  to = static_cast<int>(min(tiles * (warp + 1) / kAll * 128, static_cast<int64_t>(a.n_pages)));
+// This warp's part of the counts.
+__device__ __forceinline__ PoolPart part_of_counts(const PoolArgs& a) {
+  return pool_part(a.n_pages, blockIdx.x * kPoolWarps + (threadIdx.x >> 5), kPoolCtas * kPoolWarps);
 }
 // Bit j: page p + j is free, of the four from p on.
-__device__ __forceinline__ uint32_t free_of_four(const PoolArgs& a, int p, int to) {
+__device__ __forceinline__ uint32_t free_of_four(const PoolArgs& a, uint32_t p, uint32_t to) {
   int c[4] = {1, 1, 1, 1};
-  if (p + 4 <= to) {
+  if (pool_four_whole(p, to)) {
     const int4 v = __ldcg(reinterpret_cast<const int4*>(a.refs + p));
     c[0] = v.x; c[1] = v.y; c[2] = v.z; c[3] = v.w;
   } else {
@@ -100,23 +97,22 @@ __device__ __forceinline__ uint32_t free_of_four(const PoolArgs& a, int p, int t
   }
   return (c[0] == 0) | (c[1] == 0) << 1 | (c[2] == 0) << 2 | (c[3] == 0) << 3;
 }
-// A warp's part of up to kKept * 128 pages (all of 2^19) is kept as bits between counting and listing.
-constexpr int kKept = 16;
+// A warp's part of up to kPoolStep pages (all of 2^19) is kept as bits between counting and listing.
 __device__ __forceinline__ uint64_t count_free(const PoolArgs& a) {
   const int lane = threadIdx.x & 31;
-  int from, to, n = 0;
-  part_of_counts(a, from, to);
+  const PoolPart part = part_of_counts(a);
+  int n = 0;
   uint64_t kept = 0;
-  for (int p0 = from; p0 < to; p0 += 128 * kKept) {
-    uint32_t f[kKept];
+  for (uint32_t p0 = part.from; p0 < part.to; p0 += kPoolStep) {
+    uint32_t f[kPoolKept];
 #pragma unroll
-    for (int k = 0; k < kKept; ++k) {
-      const int p = p0 + k * 128 + lane * 4;
-      f[k] = p < to ? free_of_four(a, p, to) : 0;
+    for (int k = 0; k < kPoolKept; ++k) {
+      const uint32_t p = pool_four(p0, k, lane);
+      f[k] = p < part.to ? free_of_four(a, p, part.to) : 0;
     }
     kept = 0;
 #pragma unroll
-    for (int k = 0; k < kKept; ++k) kept |= static_cast<uint64_t>(f[k]) << (4 * k);
+    for (int k = 0; k < kPoolKept; ++k) kept |= static_cast<uint64_t>(f[k]) << (4 * k);
     n += __popcll(kept);
   }
   n = warp_sum(n);
@@ -126,19 +122,18 @@ __device__ __forceinline__ uint64_t count_free(const PoolArgs& a) {
 // Writes this warp's free pages to the list, which begins with `before` of other warps', up to `most` in all.
 __device__ __forceinline__ void list_free(const PoolArgs& a, uint64_t kept, int before, int64_t most) {
   const int lane = threadIdx.x & 31;
-  int from, to;
-  part_of_counts(a, from, to);
-  for (int p0 = from; p0 < to && before < most; p0 += 128 * kKept) {
-    if (to - from > 128 * kKept) {   // more than was kept: read again
+  const PoolPart part = part_of_counts(a);
+  for (uint32_t p0 = part.from; p0 < part.to && before < most; p0 += kPoolStep) {
+    if (part.to - part.from > kPoolStep) {   // more than was kept: read again
       kept = 0;
-      for (int k = 0; k < kKept; ++k) {
-        const int p = p0 + k * 128 + lane * 4;
-        if (p < to) kept |= static_cast<uint64_t>(free_of_four(a, p, to)) << (4 * k);
+      for (int k = 0; k < kPoolKept; ++k) {
+        const uint32_t p = pool_four(p0, k, lane);
+        if (p < part.to) kept |= static_cast<uint64_t>(free_of_four(a, p, part.to)) << (4 * k);
       }
     }
     // The free pages of four groups of 128 added up at a time, a byte each (at most 128).
 #pragma unroll
-    for (int k4 = 0; k4 < kKept; k4 += 4) {
+    for (int k4 = 0; k4 < kPoolKept; k4 += 4) {
       const uint32_t bits = static_cast<uint32_t>(kept >> (4 * k4)) & 0xFFFFu;
       uint32_t mine = 0;
 #pragma unroll
@@ -151,7 +146,7 @@ __device__ __forceinline__ void list_free(const PoolArgs& a, uint64_t kept, int 
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if ((bits >> (4 * k + j)) & 1u) {
-            if (at < most) a.list[at] = p0 + (k4 + k) * 128 + lane * 4 + j;
+            if (at < most) a.list[at] = static_cast<int>(pool_four(p0, k4 + k, lane) + j);
             ++at;
           }
         before += static_cast<int>((all >> (8 * k)) & 255u);
