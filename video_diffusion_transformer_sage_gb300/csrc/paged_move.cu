@@ -23,9 +23,9 @@
 // the lowest item not yet read finds its place ready: so every wait ends.
 // The long kernel's steps on compact_frames (23184 tokens of 56 heads, 1.33 GB; floor 196 us): an item read, waited for and written
 // in turn, two CTAs per SM 554 us; reading and writing by warps of their own 420-520, 200 of it waiting for all items drawn
-// before; the search and bulk copies 337; eight items found ahead, the lists side by side, no fences, a place in the ring for every
-// item in work 220 (6.0 TB/s; 207 without looking at the ring).  Rows of 256 bytes, by 16 bytes a thread: 24000 tokens
-// 354, where heads lie together 270.
+// before; the search and bulk copies 337; eight items found ahead, the lists side by side, a place in the ring for every
+// item in work 220 (207 without looking at the ring); a fence an item, which that one lacked, 230 (5.8 TB/s).  Rows of 256 bytes,
+// by 16 bytes a thread, before the fence: 24000 tokens 354, where heads lie together 270.
 #include <algorithm>
 
 #include "paged_batch.cuh"
@@ -125,6 +125,19 @@ __device__ __forceinline__ uint4 load_shared16(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
 }
+
+// The ring's numbers, put and looked at without an order of their own; fence_gpu between what they stand for and them.
+__device__ __forceinline__ void ring_put(uint16_t* place, uint32_t n) {
+  asm volatile("st.relaxed.gpu.global.u16 [%0], %1;" ::"l"(place), "h"(static_cast<uint16_t>(n)) : "memory");
+}
+__device__ __forceinline__ uint32_t ring_get(const uint16_t* place) {
+  uint16_t n;
+  asm volatile("ld.relaxed.gpu.global.u16 %0, [%1];" : "=h"(n) : "l"(place) : "memory");
+  return n;
+}
+__device__ __forceinline__ void fence_gpu() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
+// What this thread has seen done comes before its bulk stores to global memory.
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
 struct MoveShared {
   int64_t from[kItemTokens], to[kItemTokens];   // bytes from the pages' beginning; from < 0: not moved
@@ -268,7 +281,7 @@ __global__ void __launch_bounds__(LongCfg<kBulk>::kThreads, 1) paged_compact_lon
   __shared__ volatile int s_abort;
   __shared__ int s_last;
   int32_t* next = a.counters;
-  volatile uint16_t* ring = reinterpret_cast<uint16_t*>(next + 2);
+  uint16_t* ring = reinterpret_cast<uint16_t*>(next + 2);
   const uint32_t places = kMovePlaces * gridDim.x;   // at most kPagedMoveRing
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -346,12 +359,15 @@ __global__ void __launch_bounds__(LongCfg<kBulk>::kThreads, 1) paged_compact_lon
     }
   } else if (warp <= kFinders + static_cast<int>(B)) {
     // ------------------------------------------------------------ announce, and look at the ring
-    // No fences: an item's rows have arrived in shared memory before its number is stored, and a write that is issued after the
-    // number was seen cannot change what was read.  (With fences 45 us more of compact_frames.)
+    // An item's rows have arrived in shared memory (`full`), its place in the ring holds the round before, and most often the
+    // items that it waits for are there: one fence of all lanes stands behind all three and before the item's own number and its
+    // writing.  So whoever sees that number, or a later one of its place, writes after the rows were read.  (Without a fence,
+    // in no order that PTX's memory model gives: 195 us instead of 205 of compact_frames, 303 instead of 325 where heads lie
+    // apart; with an acquire at each look and a release at each number 204 and 330.)
     for (uint32_t k = warp - kFinders - 1;; k += B) {
       const bool ok = wait(found, k, M);
       const uint32_t item = item_of(ok, k), round = item / places, far = li[k % M].far, near = li[k % M].near;
-      volatile uint16_t* at = ring + item % places;
+      uint16_t* at = ring + item % places;
       const uint64_t t0 = global_timer_ns();
       auto late = [&] {
         __nanosleep(40);
@@ -362,21 +378,21 @@ __global__ void __launch_bounds__(LongCfg<kBulk>::kThreads, 1) paged_compact_lon
         bool all = true;
         for (uint32_t d = near + lane; d <= far; d += 32) {
           const uint32_t other = item - d * a.units;
-          all &= ring[other % places] >= other / places + 1;
+          all &= ring_get(ring + other % places) >= other / places + 1;
         }
         return __all_sync(0xffffffffu, all);
       };
       bool all = true;
       if (item < a.items) {
-        while (!s_abort && *at < round) late();   // the item a round before
-        __syncwarp();
+        while (!__all_sync(0xffffffffu, s_abort || ring_get(at) >= round)) late();   // the item a round before
         all = far == 0 || clear();
       }
       if (wait(full, k, B) && item < a.items) {
-        if (lane == 0) *at = static_cast<uint16_t>(round + 1);
-        while (!all && !s_abort) {
-          all = clear();
-          if (!all) late();
+        fence_gpu();
+        if (lane == 0) ring_put(at, round + 1);
+        if (!all) {
+          while (!clear() && !__any_sync(0xffffffffu, s_abort)) late();
+          fence_gpu();
         }
       }
       pass(go, k, B);
@@ -418,6 +434,7 @@ __global__ void __launch_bounds__(LongCfg<kBulk>::kThreads, 1) paged_compact_lon
       if (item < a.items && li[k % M].moved > 0 && !s_abort) {
         const Item it = li[k % M].it;
         if (kBulk) {
+          fence_proxy_async_global();
           for (int t = me; t < it.count; t += 32)
             if (sh[k % M].from[t] >= 0)
               bulk_store(it.side->pages + sh[k % M].to[t], smem_raw + buf * kLongPieces * 16 + t * it.per * 16, it.per * 16);
