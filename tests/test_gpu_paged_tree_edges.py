@@ -56,3 +56,18 @@ def test_scores_over_e4m3_keep_the_precision_of_the_plain_call(kind, d, hq, hkv,
     assert torch.equal(out.float(), vd.float())                       # one weight: V itself
     sage.sage_paged_attn(q, cache, batch, sm_scale=sm, window=1, lse=plain)
     assert bool(((plain.double() - s).abs() <= lim).all())
+
+
+@pytest.mark.parametrize("kv_len,first", [(-2 ** 31, 0), (-2 ** 31 + 1, 0), (-1, 0), (2, 0), (300, 0), (301, 1), (2 ** 31 - 1, 2 ** 31 - 301)])
+@pytest.mark.parametrize("window", [0, 2])
+def test_positions_of_lengths_at_the_types_ends(kv_len, first, window):
+    """A tree of 300 tokens, all children of the first: positions are max(0, kv_len - 300) + depth, whatever the length; small
+    trees beside it."""
+    status = sage.status_block()
+    batch = sage.PagedBatch(_i32([0, 300, 303]), _i32([kv_len, kv_len]), _i32([[0], [0]]))
+    parents = [-1] + [0] * 299 + [-1, -1, -1]
+    tree = sage.sage_paged_tree(_i32(parents), batch, status=status, words=10, window=window)
+    assert tree.depth.tolist() == [0] + [1] * 299 + [0] * 3
+    second = max(0, kv_len - 3)
+    assert tree.positions.tolist() == [first] + [first + 1] * 299 + [second] * 3
+    assert sage.sage_check_device_status(status) == (0, 0)

@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kTreeThreads) paged_tree_kernel(const __grid_c
   if (threadIdx.x == 0 && n > 32ll * a.mask_words) record_bad_index(a.status, kWhereLength);
   __syncthreads();
   auto parent = [&](int i) { return i < kTreeShared ? up[i] : checked(i); };
-  const int prefix = max(0, __ldg(a.b.kv_len + blockIdx.x) - n);
+  const int prefix = max(__ldg(a.b.kv_len + blockIdx.x), n) - n;   // (the least of lengths less n would wrap)
   const int window = a.window > 0 ? a.window : INT32_MAX;
   if (n <= kTreeThreads) {
     // ------------------------------------------------------------ rows joined
