@@ -13,7 +13,7 @@
  * The rules of sage.h and sage_paged.h hold: device pointers, caller-owned buffers, nothing allocated, arguments checked
  * before anything is launched.  What lies in device memory is checked by the kernels: an index that is out of range is never
  * followed, the rest goes on, and the status block records SAGE_ERR_INVALID_ARG with `where` = 16 (page), 17 (length), 23 (kept
- * position), 24 (a page given back that nobody holds) or 25 (row of the page table); an expired wait has where = 26.
+ * position), 24 (a page given back or shared that nobody holds) or 25 (row of the page table); an expired wait has where = 26.
  * Everything is read on the device, so a captured graph may be replayed after the numbers changed.  Results are
  * determined by the inputs, whatever runs when.
  */
@@ -71,7 +71,8 @@ sage_status sage_paged_reserve(const sage_paged_pool* pool, const int32_t* lo, c
  *                                     (as for sage_paged_reserve), or the fork is not possible, and the child's row is empty.
  * Not possible (where = 25): a row that does not exist, src = dst, a dst row that holds a page, one that an earlier fork of the
  * call has as dst, a src that is a dst of the call.  n_tokens is taken into [0, max_pages * page_size] (17).  An entry of the
- * source without a valid page (16) is -1 in the child, or not copied.  n_forks at most n_rows.  One launch. */
+ * source without a valid page (16), or whose page nobody held before the call (24), is -1 in the child, or not copied.  n_forks at
+ * most n_rows.  One launch. */
 sage_status sage_paged_fork(const sage_paged_pool* pool, const int32_t* src_rows, const int32_t* dst_rows,
                             const int32_t* n_tokens, int64_t n_forks, int32_t* copy_src, int32_t* copy_dst,
                             int32_t* copy_tokens, int32_t* ok, void* ws, size_t ws_bytes, void* stream);

@@ -9,6 +9,8 @@
 //   2  every CTA adds up both (sums of a few hundred numbers, cheaper than a barrier more), each warp writes the numbers of
 //      its free pages to their places in the list, as far as they are needed;
 //   3  each warp gives its rows the pages from their place in the list on.
+// A fork's full pages are shared in step 2 already: whether anybody holds them is asked of counts that no page given out has
+// changed yet, and those that change there, of pages held, stay above 0.
 #include "paged_batch.cuh"
 #include "paged_check.h"
 #include "paged_pool_walk.h"
@@ -283,6 +285,7 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     paged_fork_kernel(const __grid_constant__ PoolArgs a) {
   __shared__ int64_t sh[2][kPoolWarps];
   __shared__ uint8_t mine[kMaxSeqs / kPoolCtas];   // of the CTA's forks: 1 has its row, 2 is possible, 4 needs a page
+  __shared__ uint8_t in_order[kMaxSeqs / kPoolCtas];   // of their sources: 1 the first page, 2 the begun one is somebody's
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int cap = a.max_pages << a.page_shift;
   int from, to;
@@ -317,44 +320,61 @@ __global__ void __cluster_dims__(kPoolCtas, 1, 1) __launch_bounds__(kPoolThreads
     return state >> 2;
   }, sh);
   list_free(a, kept, s.free_before, s.all);
+  auto need = [&](int k) { return mine[k - from] >> 2; };
+  // Whether fork k of `state` is made, its page at `at` of the list.
+  auto made = [&](int state, int n, int64_t at) { return (state & 2) && (n == 0 || at < s.free_all); };
+  for_each_in_order(from, to, s.before, need, [&](int k, int n, int64_t at) {
+    if (!made(mine[k - from], n, at)) return;
+    const int32_t* parent = row_of(__ldg(a.src + k));
+    int32_t* child = row_of(__ldg(a.dst + k));
+    const int full = length(k) >> a.page_shift, entries = full + n;   // the begun page's too
+    constexpr int kAhead = 4;   // entries of a lane whose loads are in flight together
+    int flags = 0;
+    for (int i0 = 0; i0 < entries; i0 += 32 * kAhead) {
+      int page[kAhead], count[kAhead];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        const int i = i0 + x * 32 + lane;
+        page[x] = i < entries ? __ldcg(parent + i) : -1;
+      }
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) count[x] = page[x] >= 0 && page[x] < a.n_pages ? __ldcg(a.refs + page[x]) : 0;
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        const int i = i0 + x * 32 + lane;
+        if (i >= entries) continue;
+        if (count[x] <= 0) record_bad_index(a.status, page[x] >= 0 && page[x] < a.n_pages ? kWhereCount : kWherePage);
+        if (i == full) {
+          flags |= count[x] > 0 ? 2 : 0;
+          continue;
+        }
+        if (count[x] > 0) atomicAdd(a.refs + page[x], 1);
+        if (i > 0) child[i] = count[x] > 0 ? page[x] : -1;   // (entry 0 holds the mark until step 3)
+        else flags |= count[x] > 0 ? 1 : 0;
+      }
+    }
+    flags = __reduce_or_sync(0xffffffffu, flags);
+    if (lane == 0) in_order[k - from] = static_cast<uint8_t>(flags);
+  });
   cluster_barrier();
-  for_each_in_order(from, to, s.before, [&](int k) { return mine[k - from] >> 2; }, [&](int k, int n, int64_t at) {
+  for_each_in_order(from, to, s.before, need, [&](int k, int n, int64_t at) {
     const int state = mine[k - from];
-    const bool can = state & 2, good = can && (n == 0 || at < s.free_all);
+    const bool good = made(state, n, at);
     const int len = length(k), full = len >> a.page_shift, part = len & ((1 << a.page_shift) - 1);
     int c_src = -1, c_dst = -1, c_tokens = 0;
-    if (!can && lane == 0) record_bad_index(a.status, kWhereRow);
-    if (state & 1) {   // the row is this fork's, with a mark in entry 0
+    if (lane == 0 && !(state & 2)) record_bad_index(a.status, kWhereRow);
+    if (lane == 0 && (state & 1)) {   // the row is this fork's, with a mark in entry 0
       int32_t* child = row_of(__ldg(a.dst + k));
-      if (!good && lane == 0) child[0] = -1;
-      if (good) {
-        const int32_t* parent = row_of(__ldg(a.src + k));
-        for (int i = lane; i < full; i += 32) {
-          int page = __ldcg(parent + i);
-          if (page < 0 || page >= a.n_pages) {
-            record_bad_index(a.status, kWherePage);
-            page = -1;
-          } else {
-            atomicAdd(a.refs + page, 1);
-          }
-          child[i] = page;
-        }
-        if (n) {
-          c_dst = __ldcg(a.list + at);
-          c_src = __ldcg(parent + full);
-          c_tokens = part;
-          if (c_src < 0 || c_src >= a.n_pages) {
-            if (lane == 0) record_bad_index(a.status, kWherePage);
-            c_src = -1;
-          }
-          if (lane == 0) {
-            child[full] = c_dst;
-            a.refs[c_dst] = 1;
-          }
-        } else if (full == 0 && lane == 0) {
-          child[0] = -1;
-        }
+      const int32_t* parent = row_of(__ldg(a.src + k));
+      const int flags = good ? in_order[k - from] : 0;
+      if (good && n) {
+        if (flags & 2) c_src = __ldcg(parent + full);
+        c_dst = __ldcg(a.list + at);
+        c_tokens = part;
+        child[full] = c_dst;
+        a.refs[c_dst] = 1;
       }
+      if (!good || full > 0 || n == 0) child[0] = flags & 1 ? __ldcg(parent) : -1;
     }
     if (lane == 0) {
       a.copy_src[k] = c_src;
