@@ -68,11 +68,11 @@ sage_status sage_paged_reserve(const sage_paged_pool* pool, const int32_t* lo, c
  *   copy_src, copy_dst, copy_tokens   device int32 [n_forks]: the begun page, the child's, and how many tokens of it; -1, -1, 0
  *                                     where there is nothing to copy (sage_paged_copy takes the lists as they are).
  *   ok                                device int32 [n_forks]: 1 where the child was made.  0: the free pages did not last
- *                                     (as for sage_paged_reserve), or the fork is not possible, and the child's row is empty.
- * Not possible (where = 25): a row that does not exist, src = dst, a dst row that holds a page, one that an earlier fork of the
- * call has as dst, a src that is a dst of the call.  n_tokens is taken into [0, max_pages * page_size] (17).  An entry of the
- * source without a valid page (16), or whose page nobody held before the call (24), is -1 in the child, or not copied.  n_forks at
- * most n_rows.  One launch. */
+ *                                     (as for sage_paged_reserve) and the child's row is empty, or the fork is not possible.
+ * Not possible (where = 25): a row that does not exist, src = dst, a dst row that holds a page; and among the forks left, a dst
+ * that an earlier one has, a src that is a dst of one of them.  (A fork not possible by itself changes no row and stands in no
+ * other's way.)  n_tokens is taken into [0, max_pages * page_size] (17).  An entry of the source without a valid page (16), or
+ * whose page nobody held before the call (24), is -1 in the child, or not copied.  n_forks at most n_rows.  One launch. */
 sage_status sage_paged_fork(const sage_paged_pool* pool, const int32_t* src_rows, const int32_t* dst_rows,
                             const int32_t* n_tokens, int64_t n_forks, int32_t* copy_src, int32_t* copy_dst,
                             int32_t* copy_tokens, int32_t* ok, void* ws, size_t ws_bytes, void* stream);

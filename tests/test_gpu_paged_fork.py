@@ -69,3 +69,26 @@ def test_many_forks_of_rows_that_name_free_pages():
         assert after == want
         first = first or (got, after, tab)
         assert first == (got, after, tab)
+
+
+def test_forks_that_are_not_possible_by_themselves_stand_in_no_others_way():
+    """Row 3 is the dst of a fork with src = dst, row 1 that of one whose src does not exist and that of one whose dst holds a
+    page: other forks have row 3 and 2 as src and row 1 as dst all the same."""
+    world = [0, 1, 1, 0, 0], [[-1, -1], [-1, -1], [1, -1], [2, -1], [-1, -1]]
+    got, refs, table, status = _fork(*world, [3, 3], [3, 4], [8, 8])
+    assert got == [[-1, -1], [-1, -1], [0, 0], [0, 1]] and status == (1, 25)
+    assert table == [[-1, -1], [-1, -1], [1, -1], [2, -1], [2, -1]] and refs == [0, 1, 2, 0, 0]
+    got, refs, table, status = _fork(*world, [9, 2], [1, 1], [8, 8])
+    assert got == [[-1, -1], [-1, -1], [0, 0], [0, 1]] and status == (1, 25)
+    assert table == [[-1, -1], [1, -1], [1, -1], [2, -1], [-1, -1]] and refs == [0, 2, 1, 0, 0]
+    got, refs, table, status = _fork(*world, [3, 2], [2, 1], [8, 8])
+    assert got == [[-1, -1], [-1, -1], [0, 0], [0, 1]] and status == (1, 25)
+    assert table == [[-1, -1], [1, -1], [1, -1], [2, -1], [-1, -1]] and refs == [0, 2, 1, 0, 0]
+
+
+def test_forks_possible_by_themselves_stand_in_others_way():
+    """The second fork to a row, and a fork of a row that is made in the call."""
+    world = [0, 1, 0], [[1, -1], [-1, -1], [-1, -1], [-1, -1]]
+    got, refs, table, status = _fork(*world, [0, 0, 1], [1, 1, 2], [8, 8, 8])
+    assert got == [[-1] * 3, [-1] * 3, [0] * 3, [1, 0, 0]] and status == (1, 25)
+    assert table == [[1, -1], [1, -1], [-1, -1], [-1, -1]] and refs == [0, 2, 0]
