@@ -30,6 +30,7 @@
 
 #include "paged_batch.cuh"
 #include "paged_check.h"
+#include "paged_kept.h"
 #include "sage_paged_pool.h"
 
 namespace sage {
@@ -257,17 +258,9 @@ struct LongItem {
 __device__ __forceinline__ int first_not_below(const CompactArgs& a, int b, int n, int64_t place) {
   const int lane = threadIdx.x & 31;
   const int32_t* keep = a.keep + b * a.keep_stride;
-  int lo = 0;
-  while (n > 0) {
-    const int step = (n + 31) / 32, at = lo + min((lane + 1) * step, n) - 1;   // the last entry of each part
-    const uint32_t below = __ballot_sync(0xffffffffu, __ldg(keep + at) < place);
-    const int parts = __popc(below);   // parts that lie below as a whole
-    const int skip = min(parts * step, n);
-    lo += skip;
-    n = step == 1 || skip == n ? 0 : min(step, n - skip) - 1;   // (a part's last entry is known)
-    if (step == 1) break;
-  }
-  return lo;
+  return kept_search(n, [&](int lo, int step, int m) {
+    return __popc(__ballot_sync(0xffffffffu, __ldg(keep + kept_part_end(lo, step, m, lane)) < place));
+  });
 }
 
 template <bool kBulk>
@@ -341,17 +334,16 @@ __global__ void __launch_bounds__(LongCfg<kBulk>::kThreads, 1) paged_compact_lon
         uint32_t moved = 0;
         for (int t = lane; t < it.count; t += 32) moved += m.from[t] >= 0;
         moved = __reduce_add_sync(0xffffffffu, moved);
-        // The entries before this item that stand in its new places: as many as it has tokens, at most.
         const int from = it.count > 0 && it.i0 > 0
                              ? first_not_below(a, it.b, it.i0, static_cast<int64_t>(__ldg(a.first + it.b)) + it.i0)
                              : it.i0;
-        const int end = min(it.i0, from + it.count);
+        const KeptWait w = kept_wait(it.i0, it.count, a.tokens, from);
         if (lane == 0) {
           LongItem& l = li[k % M];
           l.it = it;
           l.moved = moved;
-          l.far = from < end ? it.i0 / a.tokens - from / a.tokens : 0;
-          l.near = from < end ? it.i0 / a.tokens - (end - 1) / a.tokens : 0;
+          l.near = w.near;
+          l.far = w.far;
         }
       }
       pass(found, k, M);
