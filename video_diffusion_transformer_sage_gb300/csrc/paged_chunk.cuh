@@ -17,7 +17,7 @@
 //
 // bf16 cache: bf16 operands, one TMA box per page and 64 channels, straight into the swizzled tiles.
 // E4M3 cache: the codes come by TMA into a staging tile and one warpgroup widens them to fp16 (exact) in
-// the swizzled tiles; Q is held as fp16 times a power of two per row and P as fp16.
+// the swizzled tiles; Q is held as fp16 times a power of two per row and P as fp16.  (Of a tree only V is widened; see ChunkCfg.)
 //
 // One CTA per SM works through the items (units, or shares of a unit's keys), drawn from a counter; the pipeline does
 // not drain between them: the next unit's Q, K and V are loaded and its first S formed while O of the last one leaves.
@@ -33,7 +33,7 @@
 // items for the units that do not fill the SMs a last time; each then leaves (maximum, sum, O) in the workspace, and paged_join_kernel adds the parts in the order of their keys.
 //
 // kTree: the new tokens of a sequence are a tree (sage_paged_tree.h); which of them a row sees is a row of bits, looked at in
-// the key tiles that hold new tokens alone.  Compiled apart (paged_chunk_tree.cu), so the plain kernels stay as they are.
+// the key tiles that hold new tokens alone.  Compiled apart (paged_chunk_tree.cu).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -21,7 +21,7 @@
 // joined through shared memory at the end of a segment.
 //
 // kTree: the new tokens of a sequence are a tree (sage_paged_tree.h); which of them a row sees is a row of bits, looked at in
-// the key tiles that hold new tokens alone.  Compiled apart (paged_few_tree.cu), so the plain kernels stay as they are.
+// the key tiles that hold new tokens alone.  Compiled apart (paged_few_tree.cu).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
